@@ -1,5 +1,6 @@
 /*
- * swiglu_bwd.h — C ABI of the MI355X (gfx950) SwiGLU backward and Swish-gradient library.
+ * swiglu_bwd.h — C ABI of the MI355X (gfx950) SwiGLU backward and Swish-gradient library, with
+ * the operators around the gate: layer norm, token log probabilities, distillation.
  *
  * Sources (web pages; cited by title and section):
  *   [SwiGLU page]  "PyPTO-Gym 实战: Fused SwiGLU 反向传播算子 (Ascend NPU 三 Kernel 融合实现)",
@@ -239,6 +240,136 @@ swg_status swish_grad_strided(const void* grad, const void* x, void* grad_x, int
                               const int64_t* sizes, const int64_t* grad_strides,
                               const int64_t* x_strides, const int64_t* out_strides,
                               swg_dtype dtype, const float* beta, void* stream);
+
+/*
+ * Operators around the gate: the layer norm in front of it and, at the vocabulary end, token
+ * log probabilities and distillation from a teacher's top logits.  They share these rules:
+ *   - Matrices are rows of contiguous elements a row stride (ld*, in elements, at least the
+ *     row length when there is more than one row) apart, so a slice of a wider buffer is
+ *     taken as it is; every other buffer is contiguous.  Pointers need the alignment of
+ *     their element only.  Rows, row lengths: below 2^31.
+ *   - Element types: bf16, fp16 or fp32 as stated; statistics, losses and per-row
+ *     gradients are fp32; token ids are int64.  Arithmetic and sums are fp32, each result
+ *     is rounded once; results do not change from run to run.
+ *   - Outputs may not overlap another buffer (SWG_ERR_INVALID; two views that interleave
+ *     within one address range count as overlapping) unless a call allows it.
+ *   - No rows (M or R = 0): SWG_OK and nothing is launched, except that a layer norm
+ *     gradient that is overwritten becomes 0.  Rows of no elements: SWG_ERR_INVALID.
+ */
+
+/*
+ * Layer norm over the rows of x [M, N]:
+ *   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps)
+ *   y = (x - mean) rstd w + b
+ * x, y: dtype, row strides ldx, ldy.  w, b: [N], of wdtype = dtype or SWG_FP32 (other
+ * pairs: SWG_ERR_UNSUPPORTED), either may be NULL (1 and 0).  mean, rstd: [M] for the
+ * backward pass, either may be NULL.  eps: finite, >= 0.
+ */
+swg_status layer_norm_fwd(const void* x, int64_t ldx, const void* w, const void* b,
+                          void* y, int64_t ldy, float* mean, float* rstd,
+                          int64_t M, int64_t N, float eps, swg_dtype dtype,
+                          swg_dtype wdtype, void* stream);
+
+/*
+ * Its gradients, xh = (x - mean) rstd with the forward's statistics:
+ *   dx = rstd (dy w - c1 - xh c2),  c1 = sum(dy w) / N,  c2 = sum(dy w xh) / N
+ *   dw[n] = sum_m dy xh,  db[n] = sum_m dy
+ * dy, x, dx: dtype; w (may be NULL), dw, db: wdtype.  dx, dw or db may be NULL (not wanted).
+ * dx is overwritten.  accumulate = 0: dw and db are overwritten; otherwise the sums are
+ * added to their contents before the one rounding (as swiglu_bwd_b does with db).
+ * workspace: layer_norm_bwd_workspace_size(M, N, dtype) bytes (fp32 partial sums), 16-byte
+ * aligned; may be NULL when dw and db are.
+ */
+swg_status layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                          const void* w, const float* mean, const float* rstd,
+                          void* dx, int64_t lddx, void* dw, void* db, int accumulate,
+                          int64_t M, int64_t N, swg_dtype dtype, swg_dtype wdtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
+
+/*
+ * Log probabilities over rows of logits z [R, V] (dtype, row stride ld) at a temperature
+ * (finite, > 0): a = z / temperature, lse = log sum exp a, p = exp(a - lse).
+ *   logprob[r] = a_t - lse for t = targets[r]; 0 for t = ignore_index; NaN for any other
+ *                t outside [0, V)
+ *   entropy[r] = - sum p (a - lse)
+ *   lse[r]
+ *   top_id[r, j], top_logprob[r, j], j < top: the ids of the largest logits, largest first
+ *                and equal ones by rising id (-0 equals +0, NaN ranks with -inf), and their
+ *                log probabilities.  0 <= top <= min(V, SWG_MAX_TOP).
+ * targets and logprob may both be NULL; entropy and lse may be NULL; top_id and top_logprob
+ * may be NULL when top = 0.  A logit of -inf is a masked entry (p = 0).  A row of nothing
+ * else has lse = -inf, every log probability -inf (but 0 for ignore_index) and entropy 0;
+ * a NaN or +inf logit makes the row's values NaN.
+ * workspace: token_logprobs_workspace_size(R, V, top, dtype) bytes, 16-byte aligned (0 where
+ * the rows alone fill the GPU).
+ */
+#define SWG_MAX_TOP 128
+swg_status token_logprobs(const void* logits, int64_t ld, const int64_t* targets,
+                          float* logprob, float* entropy, float* lse,
+                          float* top_logprob, int64_t* top_id, int64_t top,
+                          int64_t R, int64_t V, float temperature, int64_t ignore_index,
+                          swg_dtype dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+size_t token_logprobs_workspace_size(int64_t R, int64_t V, int64_t top, swg_dtype dtype);
+
+/*
+ * Gradient of log probabilities and entropy, with the forward's lse and entropy:
+ *   dlogits[v] = (g (1[v = t] - p_v) - h p_v (a_v - lse + entropy)) / temperature
+ * for g = dlogprob[r] (0 where t = ignore_index; a row whose t is any other id outside
+ * [0, V) gets NaN), h = dentropy[r].  targets and dlogprob may both be NULL (g = 0), entropy
+ * and dentropy may both be NULL (h = 0).  Masked entries (p = 0) get 0, or g at the target.  dlogits:
+ * dtype, row stride ldd, overwritten; it may be exactly logits (same pointer and stride).
+ */
+swg_status token_logprobs_bwd(const void* logits, int64_t ld, const int64_t* targets,
+                              const float* lse, const float* entropy,
+                              const float* dlogprob, const float* dentropy,
+                              void* dlogits, int64_t ldd, int64_t R, int64_t V,
+                              float temperature, int64_t ignore_index, swg_dtype dtype,
+                              void* stream);
+
+/*
+ * Distillation loss of a student's logits [R, V] against a teacher's entries [R, k] (values
+ * `top`, of top_dtype: logits or log probabilities; ids `top_ids`; an id outside [0, V) is
+ * padding), 1 <= k <= SWG_MAX_TEACHER, e.g. what token_logprobs returned for the teacher:
+ *   q = softmax(top / temperature) over the row's entries,  a, lse, p as in token_logprobs
+ *   loss[r] = temperature^2 sum_j q_j (log q_j - (a_{id_j} - lse))
+ * Terms with q_j = 0 count 0; a row without any entry above -inf has loss 0.  A repeated
+ * id counts once per entry.  lse: [R] for the backward pass; may be NULL.  workspace:
+ * distill_workspace_size(R, V, k, dtype) bytes, 16-byte aligned.
+ */
+#define SWG_MAX_TEACHER 1024
+swg_status distill_fwd(const void* logits, int64_t ld, const void* top,
+                       const int64_t* top_ids, int64_t k, float* loss, float* lse,
+                       int64_t R, int64_t V, float temperature, swg_dtype dtype,
+                       swg_dtype top_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+size_t distill_workspace_size(int64_t R, int64_t V, int64_t k, swg_dtype dtype);
+
+/*
+ * Its gradient with respect to the student's logits, with the forward's lse:
+ *   dlogits[v] = dloss[r] temperature (Q p_v - sum_{j: id_j = v} q_j)
+ * Q = 1, or 0 for a row without any entry above -inf.  dloss[r] = 0 gives exactly 0 whatever
+ * the row holds (masked rows).  dlogits: dtype, row stride ldd, overwritten; it may be
+ * exactly logits (same pointer and stride).
+ */
+swg_status distill_bwd(const void* logits, int64_t ld, const void* top,
+                       const int64_t* top_ids, int64_t k, const float* lse,
+                       const float* dloss, void* dlogits, int64_t ldd, int64_t R, int64_t V,
+                       float temperature, swg_dtype dtype, swg_dtype top_dtype,
+                       void* stream);
+
+/*
+ * Both in one call, for a training step that knows its row weights dloss beforehand (such
+ * as 1 / rows): loss and lse as distill_fwd, dlogits as distill_bwd, to within rounding.
+ * lse may not be NULL.  dlogits may be exactly logits.  workspace as distill_fwd.
+ */
+swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
+                           const int64_t* top_ids, int64_t k, const float* dloss,
+                           float* loss, float* lse, void* dlogits, int64_t ldd,
+                           int64_t R, int64_t V, float temperature, swg_dtype dtype,
+                           swg_dtype top_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /*
  * Kernel-duration timing for measurement harnesses.  The next entry-point call made on

@@ -1,4 +1,5 @@
-"""Plain float64 CPU oracle for the SwiGLU backward and the beta-scaled Swish gradient.
+"""Plain float64 CPU oracle for the SwiGLU backward and the beta-scaled Swish gradient, layer
+norm, token log probabilities and distillation from a teacher's top logits.
 
 TEST INFRASTRUCTURE ONLY.  Nothing in the product path may import, call or run this
 module: only the tests, the package's smoke check and the bench's CPU-baseline leg use
@@ -33,7 +34,9 @@ from __future__ import annotations
 import numpy as np
 
 __all__ = ["sigmoid", "silu", "silu_grad", "swish_grad_ref", "b_ref", "w_ref",
-           "x_ref", "swiglu_forward_ref", "swiglu_bwd_ref"]
+           "x_ref", "swiglu_forward_ref", "swiglu_bwd_ref", "layer_norm_ref",
+           "layer_norm_bwd_ref", "log_softmax_ref", "entropy_ref", "top_ref",
+           "token_logprobs_bwd_ref", "teacher_ref", "distill_ref", "distill_bwd_ref"]
 
 
 def _f64(a) -> np.ndarray:
@@ -138,3 +141,105 @@ def swiglu_bwd_ref(dy, x, w_g, w_fc, g, fc):
     dx = x_ref(dg, dfc, w_g, w_fc)
     return {"dg": dg, "dfc": dfc, "db_g": db_g, "db_fc": db_fc,
             "dw_g": dw_g, "dw_fc": dw_fc, "dx": dx}
+
+
+def layer_norm_ref(x, w, b, eps):
+    """y = (x - mean) / sqrt(var + eps) * w + b over the last axis; returns (y, mean, rstd).
+    ``w`` / ``b`` None: 1 / 0."""
+    x = _f64(x)
+    mean = x.mean(1)
+    d = x - mean[:, None]
+    rstd = 1.0 / np.sqrt((d * d).mean(1) + eps)
+    y = d * rstd[:, None]
+    if w is not None:
+        y = y * _f64(w)
+    if b is not None:
+        y = y + _f64(b)
+    return y, mean, rstd
+
+
+def layer_norm_bwd_ref(dy, x, w, mean, rstd):
+    """Gradients (dx, dw, db) of layer_norm_ref with the statistics given."""
+    dy, x = _f64(dy), _f64(x)
+    rs = _f64(rstd)[:, None]
+    xh = (x - _f64(mean)[:, None]) * rs
+    h = dy if w is None else dy * _f64(w)
+    c1 = h.mean(1, keepdims=True)
+    c2 = (h * xh).mean(1, keepdims=True)
+    return rs * (h - c1 - xh * c2), (dy * xh).sum(0), dy.sum(0)
+
+
+def log_softmax_ref(z, t):
+    """(log p, lse) of softmax(z / t) over the last axis.  z = -inf has log p = -inf; a row of
+    nothing else has lse = -inf and log p = -inf."""
+    a = _f64(z) / t
+    m = a.max(1, keepdims=True)
+    m = np.where(np.isneginf(m), 0.0, m)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        lse = m + np.log(np.exp(a - m).sum(1, keepdims=True))
+        lp = np.where(np.isneginf(a), -np.inf, a - lse)
+    return lp, lse[:, 0]
+
+
+def entropy_ref(lp):
+    """- sum p log p, terms with p = 0 counting 0."""
+    p = np.exp(lp)
+    with np.errstate(invalid="ignore"):
+        return -np.where(p > 0, p * lp, 0.0).sum(1)
+
+
+def top_ref(z, k):
+    """Ids of the k largest entries of each row: largest first, equal ones by rising index,
+    NaN as -inf."""
+    z = _f64(z)
+    z = np.where(np.isnan(z), -np.inf, z)
+    return np.argsort(-z, axis=1, kind="stable")[:, :k]
+
+
+def token_logprobs_bwd_ref(z, t, targets, live, lse, entropy, g, h):
+    """d(sum g logprob + h entropy)/dz with lse and entropy given; ``live`` marks the rows
+    whose target counts."""
+    with np.errstate(invalid="ignore"):
+        lp = _f64(z) / t - _f64(lse)[:, None]
+    lp = np.where(np.isneginf(_f64(z)), -np.inf, lp)
+    p = np.exp(lp)
+    g = np.where(live, _f64(g), 0.0)
+    with np.errstate(invalid="ignore"):
+        ent = np.where(p > 0, p * (lp + _f64(entropy)[:, None]), 0.0)
+    d = -g[:, None] * p - _f64(h)[:, None] * ent
+    rows = np.flatnonzero(live)
+    d[rows, np.asarray(targets)[rows]] += g[rows]
+    return d / t
+
+
+def teacher_ref(u, ids, V, t):
+    """(log q, q) of the teacher's entries; ids outside [0, V) are padding; a row without any
+    entry above -inf has q = 0."""
+    u = np.where((ids >= 0) & (ids < V), _f64(u) / t, -np.inf)
+    lq, _ = log_softmax_ref(u, 1.0)
+    return lq, np.exp(lq)
+
+
+def distill_ref(z, t, u, ids):
+    """(loss, lse): t^2 sum q (log q - log p) over the teacher's entries."""
+    V = z.shape[1]
+    lp, lse = log_softmax_ref(z, t)
+    lq, q = teacher_ref(u, ids, V, t)
+    at = np.take_along_axis(lp, np.clip(ids, 0, V - 1), 1)
+    with np.errstate(invalid="ignore"):
+        return t * t * np.where(q > 0, q * (lq - at), 0.0).sum(1), lse
+
+
+def distill_bwd_ref(z, t, u, ids, lse, c):
+    """c t (Q p - q scattered to its ids), 0 where c = 0."""
+    z = _f64(z)
+    V = z.shape[1]
+    _, q = teacher_ref(u, ids, V, t)
+    with np.errstate(invalid="ignore"):
+        p = np.where(np.isneginf(z), 0.0, np.exp(z / t - _f64(lse)[:, None]))
+    d = p * (q.sum(1, keepdims=True) > 0)
+    for r in range(z.shape[0]):
+        np.subtract.at(d[r], np.clip(ids[r], 0, V - 1), q[r])
+    c = _f64(c)[:, None]
+    with np.errstate(invalid="ignore"):
+        return np.where(c == 0, 0.0, c * t * d)

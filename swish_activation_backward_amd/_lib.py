@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -17,7 +18,10 @@ __all__ = ["SwgError", "load_library", "library_path", "swish_grad", "swish_grad
            "swiglu_bwd_b", "swiglu_bwd_b_noalloc", "swiglu_bwd_w", "swiglu_bwd_x", "swiglu_fwd",
            "swiglu_bwd_b_workspace_size", "swiglu_bwd_w_workspace_size", "swg_version",
            "swg_time_next_call", "swiglu_bwd_wx", "swiglu_bwd_wx_workspace_size",
-           "swiglu_bwd_gemm_tile", "swg_set_gemm_tile", "DTYPE_CODE", "STATUS"]
+           "swiglu_bwd_gemm_tile", "swg_set_gemm_tile", "DTYPE_CODE", "STATUS",
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size", "TokenLogprobs",
+           "token_logprobs", "token_logprobs_bwd", "token_logprobs_workspace_size", "distill_fwd",
+           "distill_bwd", "distill_fwd_bwd", "distill_workspace_size", "MAX_TOP", "MAX_TEACHER"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libswiglu_bwd.so"
@@ -85,6 +89,34 @@ def load_library():
         lib.swg_set_gemm_tile.restype = i32
         lib.swiglu_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
         lib.swiglu_fwd.restype = i32
+        f32 = ctypes.c_float
+        lib.layer_norm_fwd.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, f32, i32, i32,
+                                       vp]
+        lib.layer_norm_fwd.restype = i32
+        lib.layer_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i32, i64,
+                                       i64, i32, i32, vp, sz, vp]
+        lib.layer_norm_bwd.restype = i32
+        lib.layer_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
+        lib.layer_norm_bwd_workspace_size.restype = sz
+        lib.token_logprobs.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32, i64,
+                                       i32, vp, sz, vp]
+        lib.token_logprobs.restype = i32
+        lib.token_logprobs_workspace_size.argtypes = [i64, i64, i64, i32]
+        lib.token_logprobs_workspace_size.restype = sz
+        lib.token_logprobs_bwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32,
+                                           i64, i32, vp]
+        lib.token_logprobs_bwd.restype = i32
+        lib.distill_fwd.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, f32, i32, i32, vp, sz,
+                                    vp]
+        lib.distill_fwd.restype = i32
+        lib.distill_workspace_size.argtypes = [i64, i64, i64, i32]
+        lib.distill_workspace_size.restype = sz
+        lib.distill_bwd.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, i64, i64, i64, f32, i32, i32,
+                                    vp]
+        lib.distill_bwd.restype = i32
+        lib.distill_fwd_bwd.argtypes = [vp, i64, vp, vp, i64, vp, vp, vp, vp, i64, i64, i64, f32,
+                                        i32, i32, vp, sz, vp]
+        lib.distill_fwd_bwd.restype = i32
         lib.swg_status_string.argtypes = [i32]
         lib.swg_status_string.restype = ctypes.c_char_p
         lib.swg_last_hip_error.argtypes = []
@@ -401,3 +433,266 @@ def swiglu_fwd(x, w_g, w_fc, b_g, b_fc, g, fc, y, stream=None):
         st = lib.swiglu_fwd(_ptr(x), _ptr(w_g), _ptr(w_fc), _ptr(b_g), _ptr(b_fc), _ptr(g),
                             _ptr(fc), _ptr(y), M, K, N, _dtype_code(x), _stream(stream, dev))
     _check("swiglu_fwd", st, lib)
+
+
+# ---------------------------------------------------------------- row operators
+MAX_TOP = 128          # SWG_MAX_TOP
+MAX_TEACHER = 1024     # SWG_MAX_TEACHER
+
+
+def _rows(name, t, dtype, shape, device):
+    """Checks a matrix whose rows are contiguous (any row stride that keeps them apart) and
+    returns the row stride."""
+    _same_kind(name, t, dtype, shape, device)
+    R, C = shape
+    st = t.stride()
+    if (C > 1 and st[1] != 1) or (R > 1 and st[0] < C):
+        raise ValueError(f"{name}: strides {st} (each row must be contiguous and rows may not "
+                         f"overlap)")
+    return max(st[0], C)
+
+
+def _matrix(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    return t.shape[0], t.shape[1]
+
+
+def _out(name, t, dtype, shape, device):
+    """A contiguous output: the caller's (checked) or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dense(name, t, dtype, shape, device)
+    return t
+
+
+def _size(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _affine(dtype, N, device, **named):
+    """The type of a norm's w, b, dw and db (the given ones agree); ``dtype`` if none is given."""
+    wdtype = None
+    for name, t in named.items():
+        if t is None:
+            continue
+        if wdtype is None:
+            wdtype = t.dtype
+        _dense(name, t, wdtype, (N,), device)
+    wdtype = dtype if wdtype is None else wdtype
+    if wdtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {wdtype}")
+    return wdtype
+
+
+def layer_norm_fwd(x, w, b, y=None, mean=None, rstd=None, eps=1e-5, stream=None):
+    """Layer norm over the rows of x [M, N]: y = (x - mean) rstd w + b.  ``w`` and ``b`` [N] (or
+    None) have x's dtype or fp32.  Returns y [M, N], and the fp32 mean and rstd [M] that
+    ``layer_norm_bwd`` takes; outputs that are not given are allocated."""
+    lib = load_library()
+    M, N = _matrix("x", x)
+    dt, dev = x.dtype, x.device
+    code = _dtype_code(x)
+    ldx = _rows("x", x, dt, (M, N), dev)
+    wdt = _affine(dt, N, dev, w=w, b=b)
+    with _on_device(dev):
+        if y is None:
+            y = torch.empty((M, N), dtype=dt, device=dev)
+        ldy = _rows("y", y, dt, (M, N), dev)
+        mean = _out("mean", mean, torch.float32, (M,), dev)
+        rstd = _out("rstd", rstd, torch.float32, (M,), dev)
+        st = lib.layer_norm_fwd(_ptr(x), ldx, _ptr(w), _ptr(b), _ptr(y), ldy, _ptr(mean),
+                                _ptr(rstd), M, N, eps, code, DTYPE_CODE[wdt],
+                                _stream(stream, dev))
+    _check("layer_norm_fwd", st, lib)
+    return y, mean, rstd
+
+
+def layer_norm_bwd_workspace_size(M: int, N: int, dtype) -> int:
+    return int(load_library().layer_norm_bwd_workspace_size(M, N, DTYPE_CODE[dtype]))
+
+
+def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace=None,
+                   stream=None):
+    """Gradients of ``layer_norm_fwd``: writes dx [M, N], dw and db [N] (each may be None);
+    with ``accumulate`` dw and db are added to (+=)."""
+    lib = load_library()
+    M, N = _matrix("dy", dy)
+    dt, dev = dy.dtype, dy.device
+    code = _dtype_code(dy)
+    lddy = _rows("dy", dy, dt, (M, N), dev)
+    ldx = _rows("x", x, dt, (M, N), dev)
+    lddx = N if dx is None else _rows("dx", dx, dt, (M, N), dev)
+    wdt = _affine(dt, N, dev, w=w, dw=dw, db=db)
+    _dense("mean", mean, torch.float32, (M,), dev)
+    _dense("rstd", rstd, torch.float32, (M,), dev)
+    with _on_device(dev):
+        ws = workspace
+        if dw is not None or db is not None:
+            nbytes = int(lib.layer_norm_bwd_workspace_size(M, N, code))
+            ws = _workspace(nbytes, workspace, dev, stream)
+        st = lib.layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(mean), _ptr(rstd),
+                                _ptr(dx), lddx, _ptr(dw), _ptr(db), int(accumulate), M, N, code,
+                                DTYPE_CODE[wdt], _ptr(ws), _size(ws), _stream(stream, dev))
+    _check("layer_norm_bwd", st, lib)
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` returns, all fp32 but the int64 ids: logprob [R] (None without
+    targets), entropy [R], lse [R], top_logprob and top_id [R, top] (None when top is 0)."""
+    logprob: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logprob: Optional[torch.Tensor]
+    top_id: Optional[torch.Tensor]
+
+
+def token_logprobs_workspace_size(R: int, V: int, top: int, dtype) -> int:
+    return int(load_library().token_logprobs_workspace_size(R, V, top, DTYPE_CODE[dtype]))
+
+
+def token_logprobs(logits, targets=None, top=0, temperature=1.0, ignore_index=-100, out=None,
+                   workspace=None, stream=None):
+    """Log probabilities of the ``targets`` [R] (int64) under softmax(logits / temperature),
+    logits [R, V], with each row's entropy, log-sum-exp and its ``top`` likeliest entries
+    (likeliest first, ties by rising id) with their log probabilities.  Returns
+    ``TokenLogprobs``; ``out`` may hand back an earlier result of the same shape to be
+    overwritten."""
+    lib = load_library()
+    R, V = _matrix("logits", logits)
+    dt, dev = logits.dtype, logits.device
+    code = _dtype_code(logits)
+    ld = _rows("logits", logits, dt, (R, V), dev)
+    if targets is not None:
+        _dense("targets", targets, torch.int64, (R,), dev)
+    if out is None:
+        out = TokenLogprobs(None, None, None, None, None)
+    with _on_device(dev):
+        f32 = torch.float32
+        entropy = _out("out.entropy", out.entropy, f32, (R,), dev)
+        lse = _out("out.lse", out.lse, f32, (R,), dev)
+        logprob = top_lp = top_id = None
+        if targets is not None:
+            logprob = _out("out.logprob", out.logprob, f32, (R,), dev)
+        if top > 0:
+            top_lp = _out("out.top_logprob", out.top_logprob, f32, (R, top), dev)
+            top_id = _out("out.top_id", out.top_id, torch.int64, (R, top), dev)
+        ws = _workspace(int(lib.token_logprobs_workspace_size(R, V, top, code)), workspace, dev,
+                        stream)
+        st = lib.token_logprobs(_ptr(logits), ld, _ptr(targets), _ptr(logprob), _ptr(entropy),
+                                _ptr(lse), _ptr(top_lp), _ptr(top_id), top, R, V, temperature,
+                                ignore_index, code, _ptr(ws), _size(ws), _stream(stream, dev))
+    _check("token_logprobs", st, lib)
+    return TokenLogprobs(logprob, entropy, lse, top_lp, top_id)
+
+
+def token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogits=None,
+                       temperature=1.0, ignore_index=-100, stream=None):
+    """Gradient of ``token_logprobs``'s logprob and entropy with respect to the logits, from
+    dlogprob and dentropy [R] (fp32; either may be None, targets with dlogprob and entropy
+    with dentropy).  ``dlogits`` [R, V] may be ``logits`` itself; it is returned."""
+    lib = load_library()
+    R, V = _matrix("logits", logits)
+    dt, dev = logits.dtype, logits.device
+    code = _dtype_code(logits)
+    ld = _rows("logits", logits, dt, (R, V), dev)
+    if targets is not None:
+        _dense("targets", targets, torch.int64, (R,), dev)
+    for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob),
+                    ("dentropy", dentropy)):
+        if t is not None or name == "lse":
+            _dense(name, t, torch.float32, (R,), dev)
+    with _on_device(dev):
+        if dlogits is None:
+            dlogits = torch.empty((R, V), dtype=dt, device=dev)
+        ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
+        st = lib.token_logprobs_bwd(_ptr(logits), ld, _ptr(targets), _ptr(lse), _ptr(entropy),
+                                    _ptr(dlogprob), _ptr(dentropy), _ptr(dlogits), ldd, R, V,
+                                    temperature, ignore_index, code, _stream(stream, dev))
+    _check("token_logprobs_bwd", st, lib)
+    return dlogits
+
+
+def _teacher(top, top_ids, R, dev):
+    """Checks the teacher's entries [R, k]; returns k and the code of their type."""
+    _, k = _matrix("top", top)
+    _dense("top", top, top.dtype, (R, k), dev)
+    _dense("top_ids", top_ids, torch.int64, (R, k), dev)
+    return k, _dtype_code(top)
+
+
+def distill_workspace_size(R: int, V: int, k: int, dtype) -> int:
+    return int(load_library().distill_workspace_size(R, V, k, DTYPE_CODE[dtype]))
+
+
+def distill_fwd(logits, top, top_ids, temperature=1.0, loss=None, lse=None, workspace=None,
+                stream=None):
+    """Distillation loss of logits [R, V] against a teacher's entries: values ``top`` [R, k]
+    (logits or log probabilities, bf16, fp16 or fp32) at ``top_ids`` [R, k] (int64; ids
+    outside [0, V) are padding).  Returns the fp32 loss [R] (T^2 times the divergence from
+    the teacher's renormalised distribution) and the lse [R] ``distill_bwd`` takes."""
+    lib = load_library()
+    R, V = _matrix("logits", logits)
+    dt, dev = logits.dtype, logits.device
+    code = _dtype_code(logits)
+    ld = _rows("logits", logits, dt, (R, V), dev)
+    k, top_code = _teacher(top, top_ids, R, dev)
+    with _on_device(dev):
+        loss = _out("loss", loss, torch.float32, (R,), dev)
+        lse = _out("lse", lse, torch.float32, (R,), dev)
+        ws = _workspace(int(lib.distill_workspace_size(R, V, k, code)), workspace, dev, stream)
+        st = lib.distill_fwd(_ptr(logits), ld, _ptr(top), _ptr(top_ids), k, _ptr(loss), _ptr(lse),
+                             R, V, temperature, code, top_code, _ptr(ws), _size(ws),
+                             _stream(stream, dev))
+    _check("distill_fwd", st, lib)
+    return loss, lse
+
+
+def distill_bwd(logits, top, top_ids, lse, dloss, dlogits=None, temperature=1.0, stream=None):
+    """Gradient of ``distill_fwd``'s loss with respect to the logits, from dloss [R] (fp32; 0
+    for a masked row).  ``dlogits`` [R, V] may be ``logits`` itself; it is returned."""
+    lib = load_library()
+    R, V = _matrix("logits", logits)
+    dt, dev = logits.dtype, logits.device
+    code = _dtype_code(logits)
+    ld = _rows("logits", logits, dt, (R, V), dev)
+    k, top_code = _teacher(top, top_ids, R, dev)
+    _dense("lse", lse, torch.float32, (R,), dev)
+    _dense("dloss", dloss, torch.float32, (R,), dev)
+    with _on_device(dev):
+        if dlogits is None:
+            dlogits = torch.empty((R, V), dtype=dt, device=dev)
+        ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
+        st = lib.distill_bwd(_ptr(logits), ld, _ptr(top), _ptr(top_ids), k, _ptr(lse),
+                             _ptr(dloss), _ptr(dlogits), ldd, R, V, temperature, code, top_code,
+                             _stream(stream, dev))
+    _check("distill_bwd", st, lib)
+    return dlogits
+
+
+def distill_fwd_bwd(logits, top, top_ids, dloss, dlogits=None, temperature=1.0, loss=None,
+                    lse=None, workspace=None, stream=None):
+    """``distill_fwd`` and ``distill_bwd`` in one call, for a training step that knows the row
+    weights ``dloss`` [R] beforehand.  ``dlogits`` may be ``logits`` itself.  Returns
+    (loss, lse, dlogits)."""
+    lib = load_library()
+    R, V = _matrix("logits", logits)
+    dt, dev = logits.dtype, logits.device
+    code = _dtype_code(logits)
+    ld = _rows("logits", logits, dt, (R, V), dev)
+    k, top_code = _teacher(top, top_ids, R, dev)
+    _dense("dloss", dloss, torch.float32, (R,), dev)
+    with _on_device(dev):
+        loss = _out("loss", loss, torch.float32, (R,), dev)
+        lse = _out("lse", lse, torch.float32, (R,), dev)
+        if dlogits is None:
+            dlogits = torch.empty((R, V), dtype=dt, device=dev)
+        ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
+        ws = _workspace(int(lib.distill_workspace_size(R, V, k, code)), workspace, dev, stream)
+        st = lib.distill_fwd_bwd(_ptr(logits), ld, _ptr(top), _ptr(top_ids), k, _ptr(dloss),
+                                 _ptr(loss), _ptr(lse), _ptr(dlogits), ldd, R, V, temperature,
+                                 code, top_code, _ptr(ws), _size(ws), _stream(stream, dev))
+    _check("distill_fwd_bwd", st, lib)
+    return loss, lse, dlogits

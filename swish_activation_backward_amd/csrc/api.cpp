@@ -510,4 +510,327 @@ swg_status swiglu_fwd(const void* x, const void* w_g, const void* w_fc, const vo
                                gemm_grid_cap(), as_stream(stream)));
 }
 
+// ------------------------------------------------------------------- row operators
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxRowDim = int64_t(1) << 31;
+
+// Row counts, row lengths and row strides of the row operators.
+bool row_dims_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && rows < kMaxRowDim && cols < kMaxRowDim;
+}
+bool stride_ok(int64_t rows, int64_t cols, int64_t ld) { return rows <= 1 || ld >= cols; }
+
+// rows of cols elements, ld apart: the bytes from the first to past the last element; -1 on
+// overflow
+int64_t rows_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t es) {
+  int64_t n;
+  if (rows <= 0 || cols <= 0) return 0;
+  if (__builtin_mul_overflow(rows - 1, ld, &n) || __builtin_add_overflow(n, cols, &n) ||
+      __builtin_mul_overflow(n, es, &n))
+    return -1;
+  return n;
+}
+
+swg_status norm_types(int dtype, int wdtype) {
+  if (!dtype_ok(dtype) || !dtype_ok(wdtype)) return SWG_ERR_INVALID;
+  return wdtype == dtype || wdtype == SWG_FP32 ? SWG_OK : SWG_ERR_UNSUPPORTED;
+}
+
+// finite and above zero, and so is its inverse
+bool temperature_ok(float t) {
+  const float inv = 1.0f / t;
+  return t > 0.0f && t <= 3.4028234663852886e38f && inv > 0.0f && inv <= 3.4028234663852886e38f;
+}
+
+// Checks shared by the operators on logits; `r0` tells that there is nothing to do.
+swg_status vocab_dims(int64_t R, int64_t V, int64_t ld, float temperature, int dtype, bool* r0) {
+  *r0 = false;
+  if (!dtype_ok(dtype) || !row_dims_ok(R, V) || !temperature_ok(temperature) ||
+      !stride_ok(R, V, ld))
+    return SWG_ERR_INVALID;
+  if (R == 0) {
+    *r0 = true;
+    return SWG_OK;
+  }
+  return V == 0 ? SWG_ERR_INVALID : SWG_OK;
+}
+
+// dlogits against logits: the exact same view (in place) is allowed
+Span gradient_input(const void* z, int64_t ld, const void* dz, int64_t ldd, int64_t R,
+                    int64_t V, int64_t es) {
+  if (z == dz && (ld == ldd || R == 1)) return Span{nullptr, 0};
+  return Span{z, rows_bytes(R, V, ld, es)};
+}
+
+VocabArgs vocab_args(const void* z, int64_t ld, int64_t R, int64_t V, float temperature) {
+  VocabArgs a{};
+  a.z = z;
+  a.ld = ld;
+  a.R = R;
+  a.V = V;
+  a.t = temperature;
+  a.inv_t = 1.0f / temperature;
+  return a;
+}
+
+swg_status workspace_check(const void* workspace, size_t have, size_t need) {
+  if (have < need) return SWG_ERR_WORKSPACE;
+  if (need > 0 && workspace == nullptr) return SWG_ERR_NULLPTR;
+  return aligned(workspace, 16) ? SWG_OK : SWG_ERR_INVALID;
+}
+
+// the teacher's entries and the operands every distillation call has
+swg_status distill_checks(const void* logits, const void* top, const int64_t* ids, int64_t k,
+                          const float* dloss, const float* loss, const float* lse, int dtype,
+                          int top_dtype) {
+  if (!logits || !top || !ids) return SWG_ERR_NULLPTR;
+  if (!aligned(logits, (size_t)elem_size(dtype)) || !aligned(top, (size_t)elem_size(top_dtype)) ||
+      !aligned(ids, 8) || !aligned(dloss, 4) || !aligned(loss, 4) || !aligned(lse, 4))
+    return SWG_ERR_INVALID;
+  return SWG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+swg_status layer_norm_fwd(const void* x, int64_t ldx, const void* w, const void* b, void* y,
+                          int64_t ldy, float* mean, float* rstd, int64_t M, int64_t N, float eps,
+                          swg_dtype dtype, swg_dtype wdtype, void* stream) {
+  TimedCall timed_;
+  const swg_status st = norm_types(dtype, wdtype);
+  if (st != SWG_OK) return st;
+  if (!row_dims_ok(M, N) || !stride_ok(M, N, ldx) || !stride_ok(M, N, ldy) || !(eps >= 0.0f) ||
+      eps > 3.4028234663852886e38f)
+    return SWG_ERR_INVALID;
+  if (M == 0) return SWG_OK;
+  if (N == 0) return SWG_ERR_INVALID;
+  if (!x || !y) return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype), ws = elem_size(wdtype);
+  if (!aligned(x, (size_t)es) || !aligned(y, (size_t)es) || !aligned(w, (size_t)ws) ||
+      !aligned(b, (size_t)ws) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return SWG_ERR_INVALID;
+  const Span outs[] = {{y, rows_bytes(M, N, ldy, es)}, {mean, 4 * M}, {rstd, 4 * M}};
+  const Span ins[] = {{x, rows_bytes(M, N, ldx, es)}, {w, N * ws}, {b, N * ws}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  NormArgs a{};
+  a.x = x; a.ldx = ldx; a.w = w; a.b = b; a.y = y; a.ldy = ldy; a.mean = mean; a.rstd = rstd;
+  a.M = M; a.N = N; a.eps = eps;
+  return hip_status(launch_norm_fwd(dtype, wdtype, a, as_stream(stream)));
+}
+
+size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype) {
+  if (!dtype_ok(dtype) || !row_dims_ok(M, N) || M == 0 || N == 0) return 0;
+  return plan_norm_bwd(M, N).ws_bytes;
+}
+
+swg_status layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                          const float* mean, const float* rstd, void* dx, int64_t lddx, void* dw,
+                          void* db, int accumulate, int64_t M, int64_t N, swg_dtype dtype,
+                          swg_dtype wdtype, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  TimedCall timed_;
+  swg_status st = norm_types(dtype, wdtype);
+  if (st != SWG_OK) return st;
+  if (!row_dims_ok(M, N) || !stride_ok(M, N, lddy) || !stride_ok(M, N, ldx) ||
+      (dx && !stride_ok(M, N, lddx)))
+    return SWG_ERR_INVALID;
+  if (M > 0 && N == 0) return SWG_ERR_INVALID;
+  const bool cols = dw != nullptr || db != nullptr;
+  if (N == 0 || (M == 0 && (accumulate || !cols)) || (!dx && !cols)) return SWG_OK;
+  if (M > 0 && (!dy || !x || !mean || !rstd)) return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype), ws = elem_size(wdtype);
+  for (const void* p : {dy, x, (const void*)dx}) if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
+  for (const void* p : {w, (const void*)dw, (const void*)db})
+    if (!aligned(p, (size_t)ws)) return SWG_ERR_INVALID;
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return SWG_ERR_INVALID;
+  NormPlan p{};
+  if (M > 0) p = plan_norm_bwd(M, N);
+  const size_t need = cols ? p.ws_bytes : 0;
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  const Span outs[] = {{dx, dx ? rows_bytes(M, N, lddx, es) : 0}, {dw, N * ws}, {db, N * ws},
+                       {workspace, (int64_t)need}};
+  const Span ins[] = {{dy, rows_bytes(M, N, lddy, es)}, {x, rows_bytes(M, N, ldx, es)},
+                      {w, N * ws}, {mean, 4 * M}, {rstd, 4 * M}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  NormArgs a{};
+  a.x = x; a.ldx = ldx; a.w = w; a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd); a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
+  a.dw = dw; a.db = db; a.accumulate = accumulate != 0; a.M = M; a.N = N;
+  return hip_status(launch_norm_bwd(dtype, wdtype, a, p, static_cast<float*>(workspace),
+                                    as_stream(stream)));
+}
+
+size_t token_logprobs_workspace_size(int64_t R, int64_t V, int64_t top, swg_dtype dtype) {
+  if (!dtype_ok(dtype) || !row_dims_ok(R, V) || R == 0 || V == 0 || top < 0 || top > V ||
+      top > SWG_MAX_TOP)
+    return 0;
+  return plan_vocab(R, V, top, dtype).ws_bytes;
+}
+
+swg_status token_logprobs(const void* logits, int64_t ld, const int64_t* targets, float* logprob,
+                          float* entropy, float* lse, float* top_logprob, int64_t* top_id,
+                          int64_t top, int64_t R, int64_t V, float temperature,
+                          int64_t ignore_index, swg_dtype dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  TimedCall timed_;
+  bool none;
+  swg_status st = vocab_dims(R, V, ld, temperature, dtype, &none);
+  if (st != SWG_OK) return st;
+  if (top < 0) return SWG_ERR_INVALID;
+  if (none) return SWG_OK;
+  if (top > V) return SWG_ERR_INVALID;
+  if (top > SWG_MAX_TOP) return SWG_ERR_UNSUPPORTED;
+  if (!logits || (targets == nullptr) != (logprob == nullptr) ||
+      (top > 0 && (!top_logprob || !top_id)))
+    return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype);
+  if (!aligned(logits, (size_t)es) || !aligned(targets, 8) || !aligned(top_id, 8))
+    return SWG_ERR_INVALID;
+  for (const float* p : {logprob, entropy, lse, top_logprob})
+    if (!aligned(p, 4)) return SWG_ERR_INVALID;
+  const size_t need = plan_vocab(R, V, top, dtype).ws_bytes;
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  const Span outs[] = {{logprob, 4 * R}, {entropy, 4 * R}, {lse, 4 * R},
+                       {top_logprob, 4 * R * top}, {top_id, 8 * R * top},
+                       {workspace, (int64_t)need}};
+  const Span ins[] = {{logits, rows_bytes(R, V, ld, es)}, {targets, 8 * R}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  VocabArgs a = vocab_args(logits, ld, R, V, temperature);
+  a.target = targets; a.ignore = ignore_index; a.logprob = logprob; a.entropy = entropy;
+  a.lse = lse; a.top_logprob = top_logprob; a.top_id = top_id; a.top = top;
+  return hip_status(launch_logprobs(dtype, a, workspace, as_stream(stream)));
+}
+
+swg_status token_logprobs_bwd(const void* logits, int64_t ld, const int64_t* targets,
+                              const float* lse, const float* entropy, const float* dlogprob,
+                              const float* dentropy, void* dlogits, int64_t ldd, int64_t R,
+                              int64_t V, float temperature, int64_t ignore_index,
+                              swg_dtype dtype, void* stream) {
+  TimedCall timed_;
+  bool none;
+  const swg_status st = vocab_dims(R, V, ld, temperature, dtype, &none);
+  if (st != SWG_OK) return st;
+  if (!stride_ok(R, V, ldd)) return SWG_ERR_INVALID;
+  if (none) return SWG_OK;
+  if (!logits || !lse || !dlogits || (targets == nullptr) != (dlogprob == nullptr) ||
+      (entropy == nullptr) != (dentropy == nullptr))
+    return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype);
+  if (!aligned(logits, (size_t)es) || !aligned(dlogits, (size_t)es) || !aligned(targets, 8))
+    return SWG_ERR_INVALID;
+  for (const float* p : {lse, entropy, dlogprob, dentropy})
+    if (!aligned(p, 4)) return SWG_ERR_INVALID;
+  const Span outs[] = {{dlogits, rows_bytes(R, V, ldd, es)}};
+  const Span ins[] = {gradient_input(logits, ld, dlogits, ldd, R, V, es), {targets, 8 * R},
+                      {lse, 4 * R}, {entropy, 4 * R}, {dlogprob, 4 * R}, {dentropy, 4 * R}};
+  if (!outputs_disjoint(outs, ins) || rows_bytes(R, V, ld, es) < 0) return SWG_ERR_INVALID;
+  VocabArgs a = vocab_args(logits, ld, R, V, temperature);
+  a.dz = dlogits; a.lddz = ldd; a.target = targets; a.ignore = ignore_index; a.lse_in = lse;
+  a.entropy_in = entropy; a.dlogprob = dlogprob; a.dentropy = dentropy;
+  return hip_status(launch_logprobs_bwd(dtype, a, as_stream(stream)));
+}
+
+size_t distill_workspace_size(int64_t R, int64_t V, int64_t k, swg_dtype dtype) {
+  if (!dtype_ok(dtype) || !row_dims_ok(R, V) || R == 0 || V == 0 || k < 1 ||
+      k > SWG_MAX_TEACHER)
+    return 0;
+  return plan_vocab(R, V, 0, dtype).ws_bytes;
+}
+
+swg_status distill_fwd(const void* logits, int64_t ld, const void* top, const int64_t* top_ids,
+                       int64_t k, float* loss, float* lse, int64_t R, int64_t V,
+                       float temperature, swg_dtype dtype, swg_dtype top_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  TimedCall timed_;
+  bool none;
+  swg_status st = vocab_dims(R, V, ld, temperature, dtype, &none);
+  if (st != SWG_OK) return st;
+  if (!dtype_ok(top_dtype) || k < 1) return SWG_ERR_INVALID;
+  if (k > SWG_MAX_TEACHER) return SWG_ERR_UNSUPPORTED;
+  if (none) return SWG_OK;
+  st = distill_checks(logits, top, top_ids, k, nullptr, loss, lse, dtype, top_dtype);
+  if (st != SWG_OK) return st;
+  if (!loss) return SWG_ERR_NULLPTR;
+  const size_t need = plan_vocab(R, V, 0, dtype).ws_bytes;
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  const Span outs[] = {{loss, 4 * R}, {lse, 4 * R}, {workspace, (int64_t)need}};
+  const Span ins[] = {{logits, rows_bytes(R, V, ld, elem_size(dtype))},
+                      {top, R * k * elem_size(top_dtype)}, {top_ids, 8 * R * k}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  VocabArgs a = vocab_args(logits, ld, R, V, temperature);
+  a.teacher = top; a.teacher_dtype = top_dtype; a.ids = top_ids; a.k = k; a.loss = loss;
+  a.lse = lse;
+  return hip_status(launch_distill_fwd(dtype, a, workspace, as_stream(stream)));
+}
+
+swg_status distill_bwd(const void* logits, int64_t ld, const void* top, const int64_t* top_ids,
+                       int64_t k, const float* lse, const float* dloss, void* dlogits,
+                       int64_t ldd, int64_t R, int64_t V, float temperature, swg_dtype dtype,
+                       swg_dtype top_dtype, void* stream) {
+  TimedCall timed_;
+  bool none;
+  swg_status st = vocab_dims(R, V, ld, temperature, dtype, &none);
+  if (st != SWG_OK) return st;
+  if (!dtype_ok(top_dtype) || k < 1 || !stride_ok(R, V, ldd)) return SWG_ERR_INVALID;
+  if (k > SWG_MAX_TEACHER) return SWG_ERR_UNSUPPORTED;
+  if (none) return SWG_OK;
+  st = distill_checks(logits, top, top_ids, k, dloss, nullptr, lse, dtype, top_dtype);
+  if (st != SWG_OK) return st;
+  if (!lse || !dloss || !dlogits) return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype);
+  if (!aligned(dlogits, (size_t)es)) return SWG_ERR_INVALID;
+  const Span outs[] = {{dlogits, rows_bytes(R, V, ldd, es)}};
+  const Span ins[] = {gradient_input(logits, ld, dlogits, ldd, R, V, es),
+                      {top, R * k * elem_size(top_dtype)}, {top_ids, 8 * R * k}, {lse, 4 * R},
+                      {dloss, 4 * R}};
+  if (!outputs_disjoint(outs, ins) || rows_bytes(R, V, ld, es) < 0) return SWG_ERR_INVALID;
+  VocabArgs a = vocab_args(logits, ld, R, V, temperature);
+  a.teacher = top; a.teacher_dtype = top_dtype; a.ids = top_ids; a.k = k; a.lse_in = lse;
+  a.dloss = dloss; a.dz = dlogits; a.lddz = ldd;
+  return hip_status(launch_distill_bwd(dtype, a, as_stream(stream)));
+}
+
+swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
+                           const int64_t* top_ids, int64_t k, const float* dloss, float* loss,
+                           float* lse, void* dlogits, int64_t ldd, int64_t R, int64_t V,
+                           float temperature, swg_dtype dtype, swg_dtype top_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  TimedCall timed_;
+  bool none;
+  swg_status st = vocab_dims(R, V, ld, temperature, dtype, &none);
+  if (st != SWG_OK) return st;
+  if (!dtype_ok(top_dtype) || k < 1 || !stride_ok(R, V, ldd)) return SWG_ERR_INVALID;
+  if (k > SWG_MAX_TEACHER) return SWG_ERR_UNSUPPORTED;
+  if (none) return SWG_OK;
+  st = distill_checks(logits, top, top_ids, k, dloss, loss, lse, dtype, top_dtype);
+  if (st != SWG_OK) return st;
+  if (!loss || !lse || !dloss || !dlogits) return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype);
+  if (!aligned(dlogits, (size_t)es)) return SWG_ERR_INVALID;
+  const size_t need = plan_vocab(R, V, 0, dtype).ws_bytes;
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  const Span outs[] = {{dlogits, rows_bytes(R, V, ldd, es)}, {loss, 4 * R}, {lse, 4 * R},
+                       {workspace, (int64_t)need}};
+  const Span ins[] = {gradient_input(logits, ld, dlogits, ldd, R, V, es),
+                      {top, R * k * elem_size(top_dtype)}, {top_ids, 8 * R * k},
+                      {dloss, 4 * R}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  // the other outputs and the workspace against logits also where dlogits is logits
+  const Span rest[] = {{loss, 4 * R}, {lse, 4 * R}, {workspace, (int64_t)need}};
+  const Span z[] = {{logits, rows_bytes(R, V, ld, es)}};
+  if (!outputs_disjoint(rest, z)) return SWG_ERR_INVALID;
+  VocabArgs a = vocab_args(logits, ld, R, V, temperature);
+  a.teacher = top; a.teacher_dtype = top_dtype; a.ids = top_ids; a.k = k; a.dloss = dloss;
+  a.loss = loss; a.lse = lse; a.dz = dlogits; a.lddz = ldd;
+  return hip_status(launch_distill_fwd_bwd(dtype, a, workspace, as_stream(stream)));
+}
+
 }  // extern "C"

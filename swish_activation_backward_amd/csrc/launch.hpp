@@ -94,4 +94,67 @@ hipError_t launch_fwd(int dtype, const void* x, const void* w_g, const void* w_f
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t stream);
 
+// Layer norm.  Row strides in elements; w, b, y, mean, rstd (forward) and dx, dw, db
+// (backward) may be null.
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  const void* b;
+  void* y;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  const void* dy;
+  int64_t lddy;
+  void* dx;
+  int64_t lddx;
+  void* dw;
+  void* db;
+  int accumulate;
+  int64_t M, N;
+  float eps;
+};
+hipError_t launch_norm_fwd(int dtype, int wdtype, const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_bwd(int dtype, int wdtype, const NormArgs& a, const NormPlan& p,
+                           float* part, hipStream_t stream);
+
+// Rows of logits [R, V] (row stride ld) with what the forward and backward of the token log
+// probabilities and of the distillation loss read and write; pointers that a call does not
+// use are null.
+struct VocabArgs {
+  const void* z;
+  int64_t ld;
+  void* dz;
+  int64_t lddz;
+  int64_t R, V;
+  float inv_t;              // 1 / temperature
+  float t;
+  // token log probabilities
+  const int64_t* target;
+  int64_t ignore;
+  float* logprob;
+  float* entropy;
+  float* lse;
+  float* top_logprob;
+  int64_t* top_id;
+  int64_t top;
+  const float* lse_in;
+  const float* entropy_in;
+  const float* dlogprob;
+  const float* dentropy;
+  // distillation: the teacher's entries [R, k]
+  const void* teacher;
+  int teacher_dtype;
+  const int64_t* ids;
+  int64_t k;
+  float* loss;
+  const float* dloss;
+};
+hipError_t launch_logprobs(int dtype, const VocabArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_logprobs_bwd(int dtype, const VocabArgs& a, hipStream_t stream);
+hipError_t launch_distill_fwd(int dtype, const VocabArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_distill_bwd(int dtype, const VocabArgs& a, hipStream_t stream);
+hipError_t launch_distill_fwd_bwd(int dtype, const VocabArgs& a, void* ws, hipStream_t stream);
+
 }  // namespace swg

@@ -276,4 +276,39 @@ inline WXPlan plan_wx(int64_t M, int64_t K, int64_t N, int force_f = 0) {
   return p;
 }
 
+// ---------------------------------------------------------------- row operators
+// Workgroups of a launch over rows (each takes every gridDim.x-th row): a launch holds
+// fewer than 2^32 work items.
+inline unsigned row_grid(int64_t rows) {
+  return (unsigned)(rows < (int64_t(1) << 20) ? rows : (int64_t(1) << 20));
+}
+
+// Layer norm's backward pass: the rows are cut into `parts` blocks of `rows`, each of which
+// leaves one fp32 partial row [dw | db] in the workspace; the finalize kernel sums them in
+// block order.
+struct NormPlan {
+  int64_t rows;
+  int64_t parts;
+  size_t ws_bytes;
+};
+
+inline NormPlan plan_norm_bwd(int64_t M, int64_t N) {
+  NormPlan p{};
+  p.rows = M > 256 * 64 ? ceil_div(M, 256) : 64;
+  p.parts = ceil_div(M, p.rows);
+  p.ws_bytes = (size_t)p.parts * 2 * (size_t)N * sizeof(float);
+  return p;
+}
+
+// Operators on logits [R, V].
+struct VocabPlan {
+  size_t ws_bytes;
+};
+
+inline VocabPlan plan_vocab(int64_t R, int64_t V, int64_t top, int dtype) {
+  VocabPlan p{};
+  p.ws_bytes = 0;
+  return p;
+}
+
 }  // namespace swg
