@@ -7,6 +7,7 @@ arithmetic happens in the library's HIP kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -146,15 +147,21 @@ def _on_device(device):
     if device.type != "cuda":
         raise ValueError(f"tensor on {device}: the library computes on the GPU only "
                          f"(move inputs and outputs to a cuda device)")
+    if device.index == torch.cuda.current_device():
+        return _SAME_DEVICE
     return torch.cuda.device(device)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
 
 
 def _stream(stream, device):
     """The stream handle to launch on: ``stream``, else torch's current stream of the
     tensors' device."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        # the handle itself: a torch.cuda.Stream object costs about a microsecond
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
 
 
 def _check(call, status, lib):
@@ -440,16 +447,28 @@ MAX_TOP = 128          # SWG_MAX_TOP
 MAX_TEACHER = 1024     # SWG_MAX_TEACHER
 
 
+# The checks below test everything at once and leave it to the slow ones to say what is wrong:
+# a call on one row is bound by the host.
 def _rows(name, t, dtype, shape, device):
     """Checks a matrix whose rows are contiguous (any row stride that keeps them apart) and
     returns the row stride."""
-    _same_kind(name, t, dtype, shape, device)
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
+            and t.device == device):
+        _same_kind(name, t, dtype, shape, device)
     R, C = shape
-    st = t.stride()
-    if (C > 1 and st[1] != 1) or (R > 1 and st[0] < C):
-        raise ValueError(f"{name}: strides {st} (each row must be contiguous and rows may not "
-                         f"overlap)")
-    return max(st[0], C)
+    ld, inner = t.stride()
+    if (C > 1 and inner != 1) or (R > 1 and ld < C):
+        raise ValueError(f"{name}: strides {t.stride()} (each row must be contiguous and rows "
+                         f"may not overlap)")
+    return max(ld, C)
+
+
+def _packed(name, t, dtype, shape, device):
+    """Checks a contiguous tensor and returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        _dense(name, t, dtype, shape, device)
+    return t.data_ptr()
 
 
 def _matrix(name, t):
@@ -457,15 +476,19 @@ def _matrix(name, t):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
-    return t.shape[0], t.shape[1]
+    return t.shape
 
 
 def _out(name, t, dtype, shape, device):
     """A contiguous output: the caller's (checked) or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _dense(name, t, dtype, shape, device)
+    _packed(name, t, dtype, shape, device)
     return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _size(ws):
@@ -480,7 +503,7 @@ def _affine(dtype, N, device, **named):
             continue
         if wdtype is None:
             wdtype = t.dtype
-        _dense(name, t, wdtype, (N,), device)
+        _packed(name, t, wdtype, (N,), device)
     wdtype = dtype if wdtype is None else wdtype
     if wdtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {wdtype}")
@@ -503,8 +526,8 @@ def layer_norm_fwd(x, w, b, y=None, mean=None, rstd=None, eps=1e-5, stream=None)
         ldy = _rows("y", y, dt, (M, N), dev)
         mean = _out("mean", mean, torch.float32, (M,), dev)
         rstd = _out("rstd", rstd, torch.float32, (M,), dev)
-        st = lib.layer_norm_fwd(_ptr(x), ldx, _ptr(w), _ptr(b), _ptr(y), ldy, _ptr(mean),
-                                _ptr(rstd), M, N, eps, code, DTYPE_CODE[wdt],
+        st = lib.layer_norm_fwd(_addr(x), ldx, _addr(w), _addr(b), _addr(y), ldy, _addr(mean),
+                                _addr(rstd), M, N, eps, code, DTYPE_CODE[wdt],
                                 _stream(stream, dev))
     _check("layer_norm_fwd", st, lib)
     return y, mean, rstd
@@ -526,16 +549,16 @@ def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace
     ldx = _rows("x", x, dt, (M, N), dev)
     lddx = N if dx is None else _rows("dx", dx, dt, (M, N), dev)
     wdt = _affine(dt, N, dev, w=w, dw=dw, db=db)
-    _dense("mean", mean, torch.float32, (M,), dev)
-    _dense("rstd", rstd, torch.float32, (M,), dev)
+    _packed("mean", mean, torch.float32, (M,), dev)
+    _packed("rstd", rstd, torch.float32, (M,), dev)
     with _on_device(dev):
         ws = workspace
         if dw is not None or db is not None:
             nbytes = int(lib.layer_norm_bwd_workspace_size(M, N, code))
             ws = _workspace(nbytes, workspace, dev, stream)
-        st = lib.layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(mean), _ptr(rstd),
-                                _ptr(dx), lddx, _ptr(dw), _ptr(db), int(accumulate), M, N, code,
-                                DTYPE_CODE[wdt], _ptr(ws), _size(ws), _stream(stream, dev))
+        st = lib.layer_norm_bwd(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(mean), _addr(rstd),
+                                _addr(dx), lddx, _addr(dw), _addr(db), int(accumulate), M, N, code,
+                                DTYPE_CODE[wdt], _addr(ws), _size(ws), _stream(stream, dev))
     _check("layer_norm_bwd", st, lib)
 
 
@@ -566,7 +589,7 @@ def token_logprobs(logits, targets=None, top=0, temperature=1.0, ignore_index=-1
     code = _dtype_code(logits)
     ld = _rows("logits", logits, dt, (R, V), dev)
     if targets is not None:
-        _dense("targets", targets, torch.int64, (R,), dev)
+        _packed("targets", targets, torch.int64, (R,), dev)
     if out is None:
         out = TokenLogprobs(None, None, None, None, None)
     with _on_device(dev):
@@ -581,9 +604,9 @@ def token_logprobs(logits, targets=None, top=0, temperature=1.0, ignore_index=-1
             top_id = _out("out.top_id", out.top_id, torch.int64, (R, top), dev)
         ws = _workspace(int(lib.token_logprobs_workspace_size(R, V, top, code)), workspace, dev,
                         stream)
-        st = lib.token_logprobs(_ptr(logits), ld, _ptr(targets), _ptr(logprob), _ptr(entropy),
-                                _ptr(lse), _ptr(top_lp), _ptr(top_id), top, R, V, temperature,
-                                ignore_index, code, _ptr(ws), _size(ws), _stream(stream, dev))
+        st = lib.token_logprobs(_addr(logits), ld, _addr(targets), _addr(logprob), _addr(entropy),
+                                _addr(lse), _addr(top_lp), _addr(top_id), top, R, V, temperature,
+                                ignore_index, code, _addr(ws), _size(ws), _stream(stream, dev))
     _check("token_logprobs", st, lib)
     return TokenLogprobs(logprob, entropy, lse, top_lp, top_id)
 
@@ -599,17 +622,17 @@ def token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogit
     code = _dtype_code(logits)
     ld = _rows("logits", logits, dt, (R, V), dev)
     if targets is not None:
-        _dense("targets", targets, torch.int64, (R,), dev)
+        _packed("targets", targets, torch.int64, (R,), dev)
     for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob),
                     ("dentropy", dentropy)):
         if t is not None or name == "lse":
-            _dense(name, t, torch.float32, (R,), dev)
+            _packed(name, t, torch.float32, (R,), dev)
     with _on_device(dev):
         if dlogits is None:
             dlogits = torch.empty((R, V), dtype=dt, device=dev)
         ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
-        st = lib.token_logprobs_bwd(_ptr(logits), ld, _ptr(targets), _ptr(lse), _ptr(entropy),
-                                    _ptr(dlogprob), _ptr(dentropy), _ptr(dlogits), ldd, R, V,
+        st = lib.token_logprobs_bwd(_addr(logits), ld, _addr(targets), _addr(lse), _addr(entropy),
+                                    _addr(dlogprob), _addr(dentropy), _addr(dlogits), ldd, R, V,
                                     temperature, ignore_index, code, _stream(stream, dev))
     _check("token_logprobs_bwd", st, lib)
     return dlogits
@@ -618,8 +641,8 @@ def token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogit
 def _teacher(top, top_ids, R, dev):
     """Checks the teacher's entries [R, k]; returns k and the code of their type."""
     _, k = _matrix("top", top)
-    _dense("top", top, top.dtype, (R, k), dev)
-    _dense("top_ids", top_ids, torch.int64, (R, k), dev)
+    _packed("top", top, top.dtype, (R, k), dev)
+    _packed("top_ids", top_ids, torch.int64, (R, k), dev)
     return k, _dtype_code(top)
 
 
@@ -643,8 +666,8 @@ def distill_fwd(logits, top, top_ids, temperature=1.0, loss=None, lse=None, work
         loss = _out("loss", loss, torch.float32, (R,), dev)
         lse = _out("lse", lse, torch.float32, (R,), dev)
         ws = _workspace(int(lib.distill_workspace_size(R, V, k, code)), workspace, dev, stream)
-        st = lib.distill_fwd(_ptr(logits), ld, _ptr(top), _ptr(top_ids), k, _ptr(loss), _ptr(lse),
-                             R, V, temperature, code, top_code, _ptr(ws), _size(ws),
+        st = lib.distill_fwd(_addr(logits), ld, _addr(top), _addr(top_ids), k, _addr(loss), _addr(lse),
+                             R, V, temperature, code, top_code, _addr(ws), _size(ws),
                              _stream(stream, dev))
     _check("distill_fwd", st, lib)
     return loss, lse
@@ -659,14 +682,14 @@ def distill_bwd(logits, top, top_ids, lse, dloss, dlogits=None, temperature=1.0,
     code = _dtype_code(logits)
     ld = _rows("logits", logits, dt, (R, V), dev)
     k, top_code = _teacher(top, top_ids, R, dev)
-    _dense("lse", lse, torch.float32, (R,), dev)
-    _dense("dloss", dloss, torch.float32, (R,), dev)
+    _packed("lse", lse, torch.float32, (R,), dev)
+    _packed("dloss", dloss, torch.float32, (R,), dev)
     with _on_device(dev):
         if dlogits is None:
             dlogits = torch.empty((R, V), dtype=dt, device=dev)
         ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
-        st = lib.distill_bwd(_ptr(logits), ld, _ptr(top), _ptr(top_ids), k, _ptr(lse),
-                             _ptr(dloss), _ptr(dlogits), ldd, R, V, temperature, code, top_code,
+        st = lib.distill_bwd(_addr(logits), ld, _addr(top), _addr(top_ids), k, _addr(lse),
+                             _addr(dloss), _addr(dlogits), ldd, R, V, temperature, code, top_code,
                              _stream(stream, dev))
     _check("distill_bwd", st, lib)
     return dlogits
@@ -683,7 +706,7 @@ def distill_fwd_bwd(logits, top, top_ids, dloss, dlogits=None, temperature=1.0, 
     code = _dtype_code(logits)
     ld = _rows("logits", logits, dt, (R, V), dev)
     k, top_code = _teacher(top, top_ids, R, dev)
-    _dense("dloss", dloss, torch.float32, (R,), dev)
+    _packed("dloss", dloss, torch.float32, (R,), dev)
     with _on_device(dev):
         loss = _out("loss", loss, torch.float32, (R,), dev)
         lse = _out("lse", lse, torch.float32, (R,), dev)
@@ -691,8 +714,8 @@ def distill_fwd_bwd(logits, top, top_ids, dloss, dlogits=None, temperature=1.0, 
             dlogits = torch.empty((R, V), dtype=dt, device=dev)
         ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
         ws = _workspace(int(lib.distill_workspace_size(R, V, k, code)), workspace, dev, stream)
-        st = lib.distill_fwd_bwd(_ptr(logits), ld, _ptr(top), _ptr(top_ids), k, _ptr(dloss),
-                                 _ptr(loss), _ptr(lse), _ptr(dlogits), ldd, R, V, temperature,
-                                 code, top_code, _ptr(ws), _size(ws), _stream(stream, dev))
+        st = lib.distill_fwd_bwd(_addr(logits), ld, _addr(top), _addr(top_ids), k, _addr(dloss),
+                                 _addr(loss), _addr(lse), _addr(dlogits), ldd, R, V, temperature,
+                                 code, top_code, _addr(ws), _size(ws), _stream(stream, dev))
     _check("distill_fwd_bwd", st, lib)
     return loss, lse, dlogits

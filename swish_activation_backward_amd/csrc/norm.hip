@@ -12,8 +12,9 @@
 
 namespace swg {
 
+// ------------------------------------------------------------------ rows of any length
 template <typename T, typename W>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, const W* w,
+__global__ __launch_bounds__(256) void norm_fwd_any_kernel(const T* x, int64_t ldx, const W* w,
                                                        const W* b, T* y, int64_t ldy,
                                                        float* mean, float* rstd, int64_t M,
                                                        int64_t N, float eps) {
@@ -43,7 +44,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
 }
 
 template <typename T, typename W>
-__global__ __launch_bounds__(256) void norm_dx_kernel(const T* dy, int64_t lddy, const T* x,
+__global__ __launch_bounds__(256) void norm_dx_any_kernel(const T* dy, int64_t lddy, const T* x,
                                                       int64_t ldx, const W* w,
                                                       const float* mean, const float* rstd,
                                                       T* dx, int64_t lddx, int64_t M,
@@ -69,10 +70,10 @@ __global__ __launch_bounds__(256) void norm_dx_kernel(const T* dy, int64_t lddy,
 
 // one partial row [dw | db] of fp32 per block of rows
 template <typename T>
-__global__ __launch_bounds__(256) void norm_cols_kernel(const T* dy, int64_t lddy, const T* x,
+__global__ __launch_bounds__(256) void norm_cols_any_kernel(const T* dy, int64_t lddy, const T* x,
                                                         int64_t ldx, const float* mean,
                                                         const float* rstd, float* part,
-                                                        int64_t M, int64_t N, int64_t rows) {
+                                                        int64_t M, int64_t N, int64_t Np, int64_t rows) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= N) return;
   const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = r0 + rows < M ? r0 + rows : M;
@@ -82,30 +83,361 @@ __global__ __launch_bounds__(256) void norm_cols_kernel(const T* dy, int64_t ldd
     sw = __builtin_fmaf(d, (to_f32(x[r * ldx + c]) - mean[r]) * rstd[r], sw);
     sb += d;
   }
-  part[(int64_t)blockIdx.y * 2 * N + c] = sw;
-  part[(int64_t)blockIdx.y * 2 * N + N + c] = sb;
+  part += (int64_t)blockIdx.y * 2 * Np;
+  part[c] = sw;
+  part[Np + c] = sb;
 }
 
+// ------------------------------------------------------------------ rows in registers
+// A row of 8 <= N <= 16384 elements is held by G threads, EC chunks of 8 elements each (chunk
+// j * G + lane starts at column 8 times that).  A row whose length is no multiple of 8 ends
+// with a chunk moved back to the row's end: its first `skip` elements belong to the chunk
+// before as well, count in no sum, and are written twice with the same value.
+template <int G, int EC> struct RowMap {
+  int col[EC];    // first column of the chunk
+  int skip[EC];   // duplicated elements; 8 where the thread has no chunk
+  __device__ inline RowMap(int lane, int64_t n) {
+    const int N = (int)n;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      const int c = (j * G + lane) * 8;
+      col[j] = c + 8 <= N ? c : N - 8;
+      skip[j] = c >= N ? 8 : c - col[j];
+    }
+  }
+  __device__ inline bool has(int j) const { return skip[j] < 8; }
+};
+
+// the first `skip` elements become 0
+__device__ inline void drop(float* f, int skip) {
+  if (skip > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i < skip ? 0.0f : f[i];
+  }
+}
+
+// Sums over the G threads of a row: lanes of a wave, or waves through LDS (one barrier; two
+// successive calls use different halves of `red`, so a third may reuse the first's).
+template <int G> __device__ inline float row_sum(float v, float* red, int wave0) {
+  v = lanes_sum<(G < 64 ? G : 64)>(v);
+  if constexpr (G > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[wave0];
+#pragma unroll
+    for (int i = 1; i < G / 64; ++i) v += red[wave0 + i];
+  }
+  return v;
+}
+
+// w and b as fp32 (1 and 0 where absent)
+template <typename W>
+__device__ inline void load_affine(const W* w, int64_t c, float absent, float* f) {
+  if (w) {
+    Chunk<W> k;
+    k.load(w + c);
+    k.widen(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = absent;
+  }
+}
+
+template <typename T, typename W, int G, int EC>
+__global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, const W* w,
+                                                       const W* b, T* y, int64_t ldy,
+                                                       float* mean, float* rstd, int64_t M,
+                                                       int64_t N, float eps) {
+  constexpr int ROWS = 256 / G;
+  __shared__ float red[2][4];
+  const int lane = threadIdx.x % G;
+  const RowMap<G, EC> map(lane, N);
+  const float inv_n = 1.0f / (float)N;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
+  Chunk<T> cur[EC], next[EC];
+#pragma unroll
+  for (int j = 0; j < EC; ++j) {
+    cur[j].zero();
+    if (map.has(j) && r < M) cur[j].load_stream(x + r * ldx + map.col[j]);
+  }
+  // every thread of the workgroup makes the same number of passes (barriers)
+  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < M; base += step, r += step) {
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      next[j].zero();
+      if (map.has(j) && r + step < M) next[j].load_stream(x + (r + step) * ldx + map.col[j]);
+    }
+    float f[EC][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      cur[j].widen(f[j]);
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = f[j][i];
+      drop(g, map.skip[j]);
+      s += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
+    }
+    const float mu = row_sum<G>(s, red[0], (threadIdx.x / G) * (G / 64)) / (float)N;
+    s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] -= mu, g[i] = f[j][i];
+      drop(g, map.skip[j]);
+      float q = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q = __builtin_fmaf(g[i], g[i], q);
+      s += q;
+    }
+    const float var = row_sum<G>(s, red[1], (threadIdx.x / G) * (G / 64)) / (float)N;
+    const float rs = 1.0f / __builtin_sqrtf(var + eps);
+    if (r < M) {
+#pragma unroll
+      for (int j = 0; j < EC; ++j) {
+        if (!map.has(j)) continue;
+        float g[8], h[8];
+        load_affine(w, map.col[j], 1.0f, g);
+        load_affine(b, map.col[j], 0.0f, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = __builtin_fmaf(f[j][i] * rs, g[i], h[i]);
+        Chunk<T> o;
+        o.narrow(g);
+        o.store_stream(y + r * ldy + map.col[j]);
+      }
+      if (lane == 0) {
+        if (mean) mean[r] = mu;
+        if (rstd) rstd[r] = rs;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < EC; ++j) cur[j] = next[j];
+  }
+}
+
+// Backward: one pass over dy and x.  A workgroup of 1024 threads walks its share of the rows,
+// 1024 / G at a time; each thread keeps the sums dy xh and dy of its own columns in registers,
+// and the row groups of the workgroup add theirs through LDS at the end, in a fixed order, to
+// one partial row [dw | db] (dw and db themselves where there is one workgroup).
+template <typename T, typename W, int G, int EC>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part, int64_t Np) {
+  constexpr int ROWS = 1024 / G;
+  __shared__ float red[2][2][16];
+  __shared__ float sums[ROWS > 1 ? 1024 * EC * 8 : 1];
+  const int lane = threadIdx.x % G, grp = threadIdx.x / G, wave0 = grp * (G / 64);
+  const RowMap<G, EC> map(lane, a.N);
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* x = static_cast<const T*>(a.x);
+  T* dx = static_cast<T*>(a.dx);
+  float w[EC][8], sw[EC][8], sb[EC][8];
+#pragma unroll
+  for (int j = 0; j < EC; ++j) {
+    load_affine(static_cast<const W*>(a.w), map.col[j], 1.0f, w[j]);
+    // keeps duplicates out of c1 and c2; their column sums are not written
+    drop(w[j], map.skip[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sw[j][i] = sb[j][i] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t r = (int64_t)blockIdx.x * ROWS + grp;
+  int half = 0;
+  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.M; base += step, r += step) {
+    Chunk<T> cd[EC], cx[EC];
+    const bool live = r < a.M;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      cd[j].zero();
+      cx[j].zero();
+      if (map.has(j) && live) {
+        cd[j].load_stream(dy + r * a.lddy + map.col[j]);
+        cx[j].load_stream(x + r * a.ldx + map.col[j]);
+      }
+    }
+    const float mu = live ? a.mean[r] : 0.0f, rs = live ? a.rstd[r] : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      float d[8], f[8];
+      cd[j].widen(d);
+      cx[j].widen(f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = (f[i] - mu) * rs, h = d[i] * w[j][i];
+        s1 += h;
+        s2 = __builtin_fmaf(h, xh, s2);
+        sw[j][i] = __builtin_fmaf(d[i], xh, sw[j][i]);
+        sb[j][i] += d[i];
+      }
+    }
+    if (dx) {
+      s1 = lanes_sum<(G < 64 ? G : 64)>(s1);
+      s2 = lanes_sum<(G < 64 ? G : 64)>(s2);
+      if constexpr (G > 64) {
+        if ((threadIdx.x & 63) == 0) {
+          red[half][0][threadIdx.x >> 6] = s1;
+          red[half][1][threadIdx.x >> 6] = s2;
+        }
+        __syncthreads();
+        s1 = red[half][0][wave0];
+        s2 = red[half][1][wave0];
+#pragma unroll
+        for (int i = 1; i < G / 64; ++i) {
+          s1 += red[half][0][wave0 + i];
+          s2 += red[half][1][wave0 + i];
+        }
+        half ^= 1;
+      }
+      const float c1 = s1 / (float)a.N, c2 = s2 / (float)a.N;
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < EC; ++j) {
+          if (!map.has(j)) continue;
+          float d[8], f[8];
+          cd[j].widen(d);
+          cx[j].widen(f);
+          if (map.skip[j] > 0) {
+            float v[8];
+            load_affine(static_cast<const W*>(a.w), map.col[j], 1.0f, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= v[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= w[j][i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float xh = (f[i] - mu) * rs;
+            d[i] = rs * (d[i] - c1 - xh * c2);
+          }
+          Chunk<T> o;
+          o.narrow(d);
+          o.store_stream(dx + r * a.lddx + map.col[j]);
+        }
+      }
+    }
+  }
+  if (!a.dw && !a.db) return;
+  // the row groups' sums, group by group; each thread of the first group ends with its columns'
+  if constexpr (ROWS > 1) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < EC; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sums[(j * 8 + i) * 1024 + threadIdx.x] = which ? sb[j][i] : sw[j][i];
+      __syncthreads();
+      // G * EC * 8 column sums over 1024 threads
+      constexpr int COLS = G * EC * 8;
+      float total[(COLS + 1023) / 1024];
+#pragma unroll
+      for (int q = 0; q < (COLS + 1023) / 1024; ++q) {
+        const int e = q * 1024 + threadIdx.x;
+        total[q] = 0.0f;
+        if (COLS % 1024 == 0 || e < COLS) {
+          for (int g = 0; g < ROWS; ++g) total[q] += sums[(e / G) * 1024 + g * G + e % G];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < (COLS + 1023) / 1024; ++q) {
+        const int e = q * 1024 + threadIdx.x;
+        if (COLS % 1024 == 0 || e < COLS) sums[e] = total[q];
+      }
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int j = 0; j < EC; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            (which ? sb : sw)[j][i] = sums[(j * 8 + i) * G + lane];
+      }
+    }
+    if (grp != 0) return;
+  }
+  W* dw = static_cast<W*>(a.dw);
+  W* db = static_cast<W*>(a.db);
+  float* pw = part + (int64_t)blockIdx.x * 2 * Np;
+#pragma unroll
+  for (int j = 0; j < EC; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < map.skip[j]) continue;
+      const int64_t c = map.col[j] + i;
+      if (gridDim.x > 1) {
+        pw[c] = sw[j][i];
+        pw[Np + c] = sb[j][i];
+      } else {
+        if (dw) dw[c] = from_f32<W>(a.accumulate ? to_f32(dw[c]) + sw[j][i] : sw[j][i]);
+        if (db) db[c] = from_f32<W>(a.accumulate ? to_f32(db[c]) + sb[j][i] : sb[j][i]);
+      }
+    }
+  }
+}
+
+// Sums the partial rows: 16 columns to a workgroup, 64 threads a column group of 4, each over
+// every 64th partial row, then those in order.
 template <typename W>
 __global__ __launch_bounds__(256) void norm_finalize_kernel(const float* part, int64_t nparts,
-                                                            W* dw, W* db, int64_t N, int acc) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= 2 * N) return;
-  W* dst = c < N ? dw : db;
-  if (dst == nullptr) return;
-  dst += c < N ? c : c - N;
-  float s = 0.0f;
-  for (int64_t p = 0; p < nparts; ++p) s += part[p * 2 * N + c];
-  *dst = from_f32<W>(acc ? to_f32(*dst) + s : s);
+                                                            W* dw, W* db, int64_t N, int64_t Np,
+                                                            int acc) {
+  __shared__ f32x4 red[64][4];
+  const int q = threadIdx.x & 3, lane = threadIdx.x >> 2;
+  const int64_t c = ((int64_t)blockIdx.x * 4 + q) * 4;   // column of the 2 Np
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < 2 * Np) {
+    for (int64_t p = lane; p < nparts; p += 64)
+      s += *reinterpret_cast<const f32x4*>(part + p * 2 * Np + c);
+  }
+  red[lane][q] = s;
+  __syncthreads();
+  for (int n = 32; n > 0; n >>= 1) {
+    if (lane < n) red[lane][q] += red[lane + n][q];
+    __syncthreads();
+  }
+  if (threadIdx.x >= 16) return;
+  const int64_t e = (int64_t)blockIdx.x * 16 + threadIdx.x;
+  const int64_t col = e < Np ? e : e - Np;
+  W* dst = e < Np ? dw : db;
+  if (e >= 2 * Np || col >= N || dst == nullptr) return;
+  const float v = red[0][threadIdx.x >> 2][threadIdx.x & 3];
+  dst[col] = from_f32<W>(acc ? to_f32(dst[col]) + v : v);
 }
+
+#define SWG_TRY(EXPR)                          \
+  do {                                         \
+    EXPR;                                      \
+    const hipError_t e_ = hipGetLastError();   \
+    if (e_ != hipSuccess) return e_;           \
+  } while (0)
 
 template <typename T, typename W>
 static hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
-  SWG_LAUNCH((norm_fwd_kernel<T, W>), dim3(row_grid(a.M)), dim3(256), 0, stream,
-             static_cast<const T*>(a.x), a.ldx, static_cast<const W*>(a.w),
-             static_cast<const W*>(a.b), static_cast<T*>(a.y), a.ldy, a.mean, a.rstd, a.M, a.N,
-             a.eps);
-  return hipGetLastError();
+  const T* x = static_cast<const T*>(a.x);
+  const W* w = static_cast<const W*>(a.w);
+  const W* b = static_cast<const W*>(a.b);
+  T* y = static_cast<T*>(a.y);
+#define SWG_FWD(G, EC)                                                                        \
+  SWG_TRY(SWG_LAUNCH((norm_fwd_kernel<T, W, G, EC>),                                          \
+                     dim3(norm_fwd_grid(a.M, 256 / G)), dim3(256), 0, stream, x, a.ldx, w, b, \
+                     y, a.ldy, a.mean, a.rstd, a.M, a.N, a.eps))
+  if (a.N < 8 || a.N > 16384) {
+    SWG_TRY(SWG_LAUNCH((norm_fwd_any_kernel<T, W>), dim3(row_grid(a.M)), dim3(256), 0, stream, x,
+                       a.ldx, w, b, y, a.ldy, a.mean, a.rstd, a.M, a.N, a.eps));
+  } else if (a.N <= 64) SWG_FWD(8, 1);
+  else if (a.N <= 128) SWG_FWD(16, 1);
+  else if (a.N <= 256) SWG_FWD(32, 1);
+  else if (a.N <= 512) SWG_FWD(64, 1);
+  else if (a.N <= 1024) SWG_FWD(64, 2);
+  else if (a.N <= 2048) SWG_FWD(256, 1);
+  else if (a.N <= 4096) SWG_FWD(256, 2);
+  else if (a.N <= 8192) SWG_FWD(256, 4);
+  else SWG_FWD(256, 8);
+#undef SWG_FWD
+  return hipSuccess;
 }
 
 template <typename T, typename W>
@@ -113,25 +445,44 @@ static hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, float* part,
                              hipStream_t stream) {
   const T* dy = static_cast<const T*>(a.dy);
   const T* x = static_cast<const T*>(a.x);
-  if (a.dx && a.M > 0) {
-    SWG_LAUNCH((norm_dx_kernel<T, W>), dim3(row_grid(a.M)), dim3(256), 0, stream, dy, a.lddy, x,
-               a.ldx, static_cast<const W*>(a.w), a.mean, a.rstd, static_cast<T*>(a.dx), a.lddx,
-               a.M, a.N);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  if (a.M > 0 && p.group == 0) {
+    if (a.dx)
+      SWG_TRY(SWG_LAUNCH((norm_dx_any_kernel<T, W>), dim3(row_grid(a.M)), dim3(256), 0, stream,
+                         dy, a.lddy, x, a.ldx, static_cast<const W*>(a.w), a.mean, a.rstd,
+                         static_cast<T*>(a.dx), a.lddx, a.M, a.N));
+    if (!a.dw && !a.db) return hipSuccess;
+    SWG_TRY(SWG_LAUNCH((norm_cols_any_kernel<T>),
+                       dim3((unsigned)ceil_div(a.N, 256), (unsigned)p.parts), dim3(256), 0,
+                       stream, dy, a.lddy, x, a.ldx, a.mean, a.rstd, part, a.M, a.N, p.np,
+                       p.rows));
+  } else if (a.M > 0) {
+#define SWG_BWD(G, EC)                                                                  \
+  case G * 16 + EC:                                                                     \
+    SWG_TRY(SWG_LAUNCH((norm_bwd_kernel<T, W, G, EC>), dim3((unsigned)p.parts),         \
+                       dim3(1024), 0, stream, a, part, p.np));                          \
+    break
+    switch (p.group * 16 + p.chunks) {
+      SWG_BWD(8, 1);
+      SWG_BWD(16, 1);
+      SWG_BWD(32, 1);
+      SWG_BWD(64, 1);
+      SWG_BWD(128, 1);
+      SWG_BWD(128, 2);
+      SWG_BWD(256, 2);
+      SWG_BWD(512, 2);
+      SWG_BWD(1024, 2);
+    }
+#undef SWG_BWD
+    if (p.parts == 1 || (!a.dw && !a.db)) return hipSuccess;
+  } else if (!a.dw && !a.db) {
+    return hipSuccess;
   }
-  if (!a.dw && !a.db) return hipSuccess;
-  if (p.parts > 0) {   // M = 0: the empty sums
-    SWG_LAUNCH((norm_cols_kernel<T>), dim3((unsigned)ceil_div(a.N, 256), (unsigned)p.parts),
-               dim3(256), 0, stream, dy, a.lddy, x, a.ldx, a.mean, a.rstd, part, a.M, a.N,
-               p.rows);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  SWG_LAUNCH((norm_finalize_kernel<W>), dim3((unsigned)ceil_div(2 * a.N, 256)), dim3(256), 0,
-             stream, part, p.parts, static_cast<W*>(a.dw), static_cast<W*>(a.db), a.N,
-             a.accumulate);
-  return hipGetLastError();
+  // M = 0: no partial rows, the empty sums
+  const int64_t np = a.M > 0 ? p.np : ceil_div(a.N, 4) * 4;
+  SWG_TRY(SWG_LAUNCH((norm_finalize_kernel<W>), dim3((unsigned)ceil_div(2 * np, 16)), dim3(256),
+                     0, stream, part, a.M > 0 ? p.parts : 0, static_cast<W*>(a.dw),
+                     static_cast<W*>(a.db), a.N, np, a.accumulate));
+  return hipSuccess;
 }
 
 hipError_t launch_norm_fwd(int dtype, int wdtype, const NormArgs& a, hipStream_t stream) {

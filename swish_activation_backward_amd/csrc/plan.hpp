@@ -283,20 +283,44 @@ inline unsigned row_grid(int64_t rows) {
   return (unsigned)(rows < (int64_t(1) << 20) ? rows : (int64_t(1) << 20));
 }
 
-// Layer norm's backward pass: the rows are cut into `parts` blocks of `rows`, each of which
-// leaves one fp32 partial row [dw | db] in the workspace; the finalize kernel sums them in
-// block order.
+// Workgroups of the norm's forward pass, `rows` rows at a time each: all resident at once, so
+// that each walks over its rows with the next ones' loads in flight.
+inline unsigned norm_fwd_grid(int64_t M, int rows) {
+  const int64_t n = ceil_div(M, rows);
+  return (unsigned)(n < 2048 ? n : 2048);
+}
+
+// Layer norm's backward pass.  Rows of 8 to 16384 elements: `group` threads hold a row, `chunks`
+// chunks of 8 elements each, and one workgroup of 1024 threads per CU leaves one fp32 partial
+// row [dw | db] of 2 np in the workspace (none is needed for a single workgroup).  Other
+// lengths (group = 0): the rows are cut into `parts` blocks of `rows` with one partial row
+// each.  The finalize kernel sums the partial rows in a fixed order.
+// One chunk a thread up to 1024 columns, two above: at [16384, 4096] fp16 two chunks (256
+// threads a row) take 80 us and one (512 threads, half the rows between barriers) 84 us; at
+// [8191, 1023] fp32 one takes 29.5 us and two (a wave a row, more registers) 30.7 us.
 struct NormPlan {
+  int group, chunks;
   int64_t rows;
   int64_t parts;
+  int64_t np;
   size_t ws_bytes;
 };
 
 inline NormPlan plan_norm_bwd(int64_t M, int64_t N) {
   NormPlan p{};
-  p.rows = M > 256 * 64 ? ceil_div(M, 256) : 64;
-  p.parts = ceil_div(M, p.rows);
-  p.ws_bytes = (size_t)p.parts * 2 * (size_t)N * sizeof(float);
+  p.np = ceil_div(N, 4) * 4;
+  if (N < 8 || N > 16384) {
+    p.rows = M > 256 * 64 ? ceil_div(M, 256) : 64;
+    p.parts = ceil_div(M, p.rows);
+    p.ws_bytes = (size_t)p.parts * 2 * (size_t)p.np * sizeof(float);
+    return p;
+  }
+  p.chunks = N <= 1024 ? 1 : 2;
+  p.group = 8;
+  while ((int64_t)p.group * 8 * p.chunks < N) p.group *= 2;
+  const int64_t n = ceil_div(M, 1024 / p.group);
+  p.parts = n < 256 ? n : 256;
+  p.ws_bytes = (size_t)p.parts * 2 * (size_t)p.np * sizeof(float);
   return p;
 }
 
