@@ -693,7 +693,8 @@ swg_status token_logprobs(const void* logits, int64_t ld, const int64_t* targets
     return SWG_ERR_INVALID;
   for (const float* p : {logprob, entropy, lse, top_logprob})
     if (!aligned(p, 4)) return SWG_ERR_INVALID;
-  const size_t need = plan_vocab(R, V, top, dtype).ws_bytes;
+  const VocabPlan p = plan_vocab(R, V, top, dtype);
+  const size_t need = p.ws_bytes;
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   const Span outs[] = {{logprob, 4 * R}, {entropy, 4 * R}, {lse, 4 * R},
@@ -704,7 +705,7 @@ swg_status token_logprobs(const void* logits, int64_t ld, const int64_t* targets
   VocabArgs a = vocab_args(logits, ld, R, V, temperature);
   a.target = targets; a.ignore = ignore_index; a.logprob = logprob; a.entropy = entropy;
   a.lse = lse; a.top_logprob = top_logprob; a.top_id = top_id; a.top = top;
-  return hip_status(launch_logprobs(dtype, a, workspace, as_stream(stream)));
+  return hip_status(launch_logprobs(dtype, a, p, workspace, as_stream(stream)));
 }
 
 swg_status token_logprobs_bwd(const void* logits, int64_t ld, const int64_t* targets,
@@ -757,7 +758,8 @@ swg_status distill_fwd(const void* logits, int64_t ld, const void* top, const in
   st = distill_checks(logits, top, top_ids, k, nullptr, loss, lse, dtype, top_dtype);
   if (st != SWG_OK) return st;
   if (!loss) return SWG_ERR_NULLPTR;
-  const size_t need = plan_vocab(R, V, 0, dtype).ws_bytes;
+  const VocabPlan p = plan_vocab(R, V, 0, dtype);
+  const size_t need = p.ws_bytes;
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   const Span outs[] = {{loss, 4 * R}, {lse, 4 * R}, {workspace, (int64_t)need}};
@@ -767,7 +769,7 @@ swg_status distill_fwd(const void* logits, int64_t ld, const void* top, const in
   VocabArgs a = vocab_args(logits, ld, R, V, temperature);
   a.teacher = top; a.teacher_dtype = top_dtype; a.ids = top_ids; a.k = k; a.loss = loss;
   a.lse = lse;
-  return hip_status(launch_distill_fwd(dtype, a, workspace, as_stream(stream)));
+  return hip_status(launch_distill_fwd(dtype, a, p, workspace, as_stream(stream)));
 }
 
 swg_status distill_bwd(const void* logits, int64_t ld, const void* top, const int64_t* top_ids,
@@ -814,7 +816,8 @@ swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
   if (!loss || !lse || !dloss || !dlogits) return SWG_ERR_NULLPTR;
   const int64_t es = elem_size(dtype);
   if (!aligned(dlogits, (size_t)es)) return SWG_ERR_INVALID;
-  const size_t need = plan_vocab(R, V, 0, dtype).ws_bytes;
+  const VocabPlan p = plan_vocab(R, V, 0, dtype);
+  const size_t need = p.ws_bytes;
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   const Span outs[] = {{dlogits, rows_bytes(R, V, ldd, es)}, {loss, 4 * R}, {lse, 4 * R},
@@ -830,7 +833,7 @@ swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
   VocabArgs a = vocab_args(logits, ld, R, V, temperature);
   a.teacher = top; a.teacher_dtype = top_dtype; a.ids = top_ids; a.k = k; a.dloss = dloss;
   a.loss = loss; a.lse = lse; a.dz = dlogits; a.lddz = ldd;
-  return hip_status(launch_distill_fwd_bwd(dtype, a, workspace, as_stream(stream)));
+  return hip_status(launch_distill_fwd_bwd(dtype, a, p, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -151,10 +151,13 @@ struct VocabArgs {
   float* loss;
   const float* dloss;
 };
-hipError_t launch_logprobs(int dtype, const VocabArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_logprobs(int dtype, const VocabArgs& a, const VocabPlan& p, void* ws,
+                           hipStream_t stream);
 hipError_t launch_logprobs_bwd(int dtype, const VocabArgs& a, hipStream_t stream);
-hipError_t launch_distill_fwd(int dtype, const VocabArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_distill_fwd(int dtype, const VocabArgs& a, const VocabPlan& p, void* ws,
+                              hipStream_t stream);
 hipError_t launch_distill_bwd(int dtype, const VocabArgs& a, hipStream_t stream);
-hipError_t launch_distill_fwd_bwd(int dtype, const VocabArgs& a, void* ws, hipStream_t stream);
+hipError_t launch_distill_fwd_bwd(int dtype, const VocabArgs& a, const VocabPlan& p, void* ws,
+                                  hipStream_t stream);
 
 }  // namespace swg
