@@ -50,16 +50,16 @@ template <typename T> __device__ inline void fill_masked(Chunk<T>& c) {
 
 constexpr float kLowest = -3.4028234663852886e38f;
 
-// A running softmax over values z: m the largest (at least the lowest finite number, so that
-// differences stay defined over masked entries), s = sum 2^d, t = sum d 2^d for d = (z - m) c,
-// c = log2(e) / T.  A masked entry has 2^d = 0; its d is bounded where it is multiplied.  A
-// NaN or +inf makes s and t NaN.
+// Sums of a softmax over values z relative to a value m: s = sum 2^d, t = sum d 2^d for
+// d = (z - m) c, c = log2(e) / T; m is at least the lowest finite number, so that differences
+// stay defined over masked entries.  A masked entry has 2^d = 0; its d is bounded where it is
+// multiplied.  A NaN or +inf makes s and t NaN.
 struct Soft {
   float m, s, t;
 };
 __device__ inline float bound_d(float d) { return __builtin_fmaxf(d, -1000.0f); }
 
-// the same sums relative to a maximum m >= a.m
+// the same sums relative to m >= a.m
 __device__ inline void soft_move(Soft& a, float m, float c) {
   const float d = bound_d((a.m - m) * c);
   const float w = __builtin_amdgcn_exp2f(d);
@@ -82,6 +82,116 @@ template <int NT> __device__ inline void soft_block(Soft& a, float c, float* red
   a.t = block_sum<NT>(a.t, red);
 }
 
+// The running form, where an element costs one fma, one exponential, an addition and the fma
+// of t: d = z c - b against a reference b that need not be the maximum.  b moves only when a
+// chunk's largest d passes kLift, so that few waves ever branch; up to there an fp32 sum loses
+// nothing.  m is the largest value (-inf for none; NaN does not count).
+struct Run {
+  float b, m, s, t;
+};
+constexpr float kLift = 4.0f;
+constexpr float kNoRef = -1e30f;
+// z c has to stay far from overflow and from kNoRef: otherwise the row's sums are formed again
+// in the differences z - m
+__device__ inline bool run_in_range(float m, float c) {
+  return __builtin_fabsf(m * c) < 1e29f || __builtin_fabsf(m) == __builtin_inff();
+}
+
+__device__ inline void run_move(Run& a, float b) {
+  const float d = bound_d(a.b - b);
+  const float w = __builtin_amdgcn_exp2f(d);
+  a.t = w * __builtin_fmaf(d, a.s, a.t);
+  a.s *= w;
+  a.b = b;
+}
+
+// The instructions themselves: the language's maximum first makes a signaling NaN of either
+// operand quiet, one instruction each.
+__device__ inline float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
+__device__ inline float max2(float x, float y) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+  return r;
+}
+__device__ inline float max8(const float* f) {
+  return max2(max3(max3(f[0], f[1], f[2]), f[3], f[4]), max3(f[5], f[6], f[7]));
+}
+
+// 8 elements, the largest of which is gm
+template <bool ENT> __device__ inline void run_chunk(Run& a, const float* f, float gm, float c) {
+  a.m = max2(a.m, gm);
+  const float top = gm * c;
+  if (top - a.b > kLift) run_move(a, top);
+  const float t0 = a.t;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = __builtin_fmaf(f[i], c, -a.b);
+    const float e = __builtin_amdgcn_exp2f(d);
+    a.s += e;
+    if constexpr (ENT) a.t = __builtin_fmaf(d, e, a.t);
+  }
+  if constexpr (ENT) {
+    if (a.t != a.t) {   // masked entries: -inf times 0
+      a.t = t0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = __builtin_fmaf(f[i], c, -a.b);
+        a.t = __builtin_fmaf(bound_d(d), __builtin_amdgcn_exp2f(d), a.t);
+      }
+    }
+  }
+}
+
+__device__ inline void run_single(Run& a, float x, float c) {
+  a.m = __builtin_fmaxf(a.m, x);
+  const float top = x * c;
+  if (top - a.b > kLift) run_move(a, top);
+  const float d = top - a.b, e = __builtin_amdgcn_exp2f(d);
+  a.s += e;
+  a.t = __builtin_fmaf(bound_d(d), e, a.t);
+}
+
+// over the workgroup, the same in every thread: one barrier.  `red` holds 4 floats a wave and
+// may be used again after the next barrier.
+template <int NT> __device__ inline void run_block(Run& a, float* red) {
+  a.m = wave_max(a.m);
+  run_move(a, wave_max(a.b));
+  a.s = wave_sum(a.s);
+  a.t = wave_sum(a.t);
+  if constexpr (NT > 64) {
+    f32x4* r = reinterpret_cast<f32x4*>(red);
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = f32x4{a.b, a.m, a.s, a.t};
+    __syncthreads();
+    float b = kNoRef;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) {
+      b = __builtin_fmaxf(b, r[i][0]);
+      a.m = __builtin_fmaxf(a.m, r[i][1]);
+    }
+    a.s = a.t = 0.0f;
+    a.b = b;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) {
+      Run o{r[i][0], 0.0f, r[i][2], r[i][3]};
+      run_move(o, b);
+      a.s += o.s;
+      a.t += o.t;
+    }
+  }
+}
+
+// relative to the maximum
+__device__ inline Soft run_soft(const Run& a, float c) {
+  if (a.m == neg_inf()) return Soft{kLowest, a.s, a.t};
+  const float d = __builtin_fmaf(a.m, c, -a.b);
+  const float w = __builtin_amdgcn_exp2f(-d);
+  return Soft{a.m, a.s * w, __builtin_fmaf(-d, a.s, a.t) * w};
+}
+
 // What a row's sums give.  log p = (z - m) / T - ls.
 struct RowStat {
   float m, ls, lse, entropy;
@@ -102,31 +212,41 @@ __device__ inline float log_prob(const RowStat& r, float z, float inv_t) {
 
 // ------------------------------------------------------------------ top entries
 // A workgroup's selection of the k largest keys of a row.  While the row is read, the largest
-// value of every group of chunks is kept (`gkeys`).  A value that at least k group maxima
+// value of every group of chunks is kept (`gmax`).  A value that at least k group maxima
 // reach bounds the k-th largest entry from below, and only the groups that reach it, about k
 // of them, are read again: their entries from the bound on are the candidates, ordered at the
-// end by counting.  Where equal values leave no bound with few groups, the entries above it
-// are candidates and, of those equal to it, the first ones by index, found by a scan.
+// end by counting.
+//
+// The bound comes from a histogram of the maxima, linear in the value between the smallest of
+// the threads' largest maxima (there are at least k such threads) and the largest of all: one
+// pass and a scan of 512 bins.  Where that leaves too many groups (equal or masked entries),
+// it comes from a bisection of the keys, and where equal values leave no bound with few
+// groups, the entries above it are candidates and, of those equal to it, the first ones by
+// index, found by a scan of the row.
 constexpr int kSlack = 64;          // keys a selection may leave beyond k before the ordering
-__host__ __device__ inline int top_groups(int k) { return k + k / 4 + 8; }
+constexpr int kBins = 512;
+__host__ __device__ inline int top_groups(int k) { return k + k / 8 + 8; }
 __host__ __device__ inline int top_candidates(int k, int group) {
   return top_groups(k) * group + 2 * k + 16;
 }
 
 template <int NT> struct TopState {
-  uint32_t* gkeys;   // one per group of the tile
+  float* gmax;       // one per group of the tile
   uint32_t* glist;   // chosen groups
   u64* cand;         // candidates
   u64* sel;          // k + kSlack
   u64* best;         // k, in order
-  int* count;        // [0] candidates, [1] groups, [2..] counts of the waves, twice
+  uint32_t* hist;    // kBins, and the partial ranks
+  int* count;        // TopCount<NT>::N
   int k;
 };
+// [0] candidates, [1] groups or chosen keys, then the waves' counts and bounds, twice
+template <int NT> struct TopCount { static constexpr int N = 4 + 4 * (NT / 64); };
 
-// the number of threads' flags over the workgroup; successive calls alternate `half`
+// the sum of the waves' counts; successive calls alternate `half`
 template <int NT> __device__ inline int block_count(int wave_count, int* count, int& half) {
   if constexpr (NT == 64) return wave_count;
-  int* c = count + 2 + half * (NT / 64);
+  int* c = count + 4 + half * (NT / 64);
   half ^= 1;
   if ((threadIdx.x & 63) == 0) c[threadIdx.x >> 6] = wave_count;
   __syncthreads();
@@ -136,21 +256,90 @@ template <int NT> __device__ inline int block_count(int wave_count, int* count, 
   return n;
 }
 
-// Bisects for a bound: `lo` such that at least k of the n keys are >= lo and either no more
-// than `most`, or lo + 1 is reached by fewer than k.  Returns the count at lo.  The same in
-// every thread; n >= k.
-template <int NT, typename K>
-__device__ inline int bisect(const K* keys, int n, int k, int most, K hi, int* count, K& lo) {
+// smallest and largest over the workgroup; a barrier
+template <int NT> __device__ inline void block_bounds(float& lo, float& hi, int* count) {
+  lo = -wave_max(-lo);
+  hi = wave_max(hi);
+  if constexpr (NT > 64) {
+    float* c = reinterpret_cast<float*>(count + 4 + 2 * (NT / 64));
+    if ((threadIdx.x & 63) == 0) {
+      c[(threadIdx.x >> 6) * 2] = lo;
+      c[(threadIdx.x >> 6) * 2 + 1] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) {
+      lo = __builtin_fminf(lo, c[i * 2]);
+      hi = __builtin_fmaxf(hi, c[i * 2 + 1]);
+    }
+  } else {
+    __syncthreads();
+  }
+}
+
+// Bins of the histogram: falling values, equal ones together.
+struct Bins {
+  float hi, scale;
+  __device__ inline Bins(float lo, float hi_) : hi(hi_) {
+    scale = (float)(kBins - 1) / (hi - lo);
+  }
+  __device__ inline bool usable(float lo) const {
+    return lo > neg_inf() && lo < hi && hi < __builtin_inff() && scale < __builtin_inff();
+  }
+  __device__ inline float at(float v) const { return (hi - v) * scale; }
+  __device__ inline void add(uint32_t* hist, float v) const {
+    const int b = (int)at(v);
+    atomicAdd(&hist[b < kBins ? b : kBins - 1], 1u);
+  }
+};
+
+// From a complete histogram: the fewest first bins that hold k, as `limit` (a value v is in
+// them if bins.at(v) < limit); returns how many they hold, 0 if all together hold fewer.  Every
+// wave scans by itself, kBins / 64 bins to a lane.
+__device__ inline int hist_bound(const uint32_t* hist, int k, float& limit) {
+  constexpr int PER = kBins / 64;
+  const int lane = threadIdx.x & 63;
+  int c[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = (int)hist[lane * PER + i];
+    sum += c[i];
+  }
+  int incl = sum;
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xf, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xa, 0xf, false);
+  incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xc, 0xf, false);
+  const u64 over = __ballot(incl >= k);
+  if (over == 0) return 0;
+  int run = incl - sum, bin = 0, reach = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    run += c[i];
+    if (reach == 0 && run >= k) {
+      reach = run;
+      bin = lane * PER + i + 1;
+    }
+  }
+  const int at = __builtin_ctzll(over);
+  const int bins = __builtin_amdgcn_readlane(bin, at);
+  limit = bins >= kBins ? __builtin_inff() : (float)bins;   // the last bin has no lower end
+  return __builtin_amdgcn_readlane(reach, at);
+}
+
+// Bisects for a bound: `lo` such that at least k of n keys are >= lo and either no more than
+// `most`, or lo + 1 is reached by fewer than k.  count_from(x) is the number of the wave's keys
+// >= x.  Returns the count at lo.  The same in every thread; n >= k.
+template <int NT, typename K, typename F>
+__device__ inline int bisect(F count_from, int n, int k, int most, K hi, int* count, K& lo) {
   int half = 0, at_lo = n;
   lo = 0;
+  __syncthreads();
   while (at_lo > most && hi - lo > 1) {
     const K mid = lo + (hi - lo) / 2;
-    int c = 0;
-    for (int i = threadIdx.x & ~63; i < n; i += NT) {
-      const int j = i + (threadIdx.x & 63);
-      c += __popcll(__ballot(j < n && keys[j] >= mid));
-    }
-    c = block_count<NT>(c, count, half);
+    const int c = block_count<NT>(count_from(mid), count, half);
     if (c >= k) {
       lo = mid;
       at_lo = c;
@@ -162,73 +351,156 @@ __device__ inline int bisect(const K* keys, int n, int k, int most, K hi, int* c
   return at_lo;
 }
 
-// the k largest of the n candidates to `best`, in falling order; the rest of best becomes 0
-template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n) {
+__device__ inline float key_float(u64 key) { return key_value((uint32_t)(key >> 32)); }
+
+// the k largest of the n candidates to `best`, in falling order; the rest of best becomes 0.
+// At least k of the candidates are >= floor_key.  Called after a barrier, ends with one.
+template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n, u64 floor_key) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const u64* from = w.cand;
   if (n > w.k + kSlack) {
-    u64 lo;
-    n = bisect<NT, u64>(w.cand, n, w.k, w.k + kSlack, ~0ull, w.count, lo);
-    const int all = w.count[0];
-    if (threadIdx.x == 0) w.count[1] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < all; i += NT) {
+    // a bound by value, or else by the keys themselves
+    float lo = __builtin_inff(), hi = neg_inf(), limit = 0.0f;
+    for (int i = threadIdx.x; i < n; i += NT) {
       const u64 key = w.cand[i];
-      if (key >= lo) w.sel[atomicAdd(&w.count[1], 1)] = key;
+      if (key >= floor_key && key != 0) {
+        lo = __builtin_fminf(lo, key_float(key));
+        hi = __builtin_fmaxf(hi, key_float(key));
+      }
+    }
+    for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
+    if (threadIdx.x == 0) w.count[1] = 0;
+    block_bounds<NT>(lo, hi, w.count);
+    const Bins bins(lo, hi);
+    auto counts = [&](u64 key) { return key != 0 && key_float(key) >= lo; };
+    int reach = 0;
+    if (bins.usable(lo)) {
+      for (int i = threadIdx.x; i < n; i += NT)
+        if (counts(w.cand[i])) bins.add(w.hist, key_float(w.cand[i]));
+      __syncthreads();
+      reach = hist_bound(w.hist, w.k, limit);
+    }
+    u64 least = 0;
+    const bool by_value = reach >= w.k && reach <= w.k + kSlack;
+    if (!by_value)
+      bisect<NT, u64>([&](u64 x) {
+        int c = 0;
+        for (int i = wave * 64; i < n; i += NT)
+          c += __popcll(__ballot(i + lane < n && w.cand[i + lane] >= x));
+        return c;
+      }, n, w.k, w.k + kSlack, ~0ull, w.count, least);
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const u64 key = w.cand[i];
+      if (by_value ? counts(key) && bins.at(key_float(key)) < limit : key >= least)
+        w.sel[atomicAdd(&w.count[1], 1)] = key;
     }
     __syncthreads();
     from = w.sel;
+    n = w.count[1];
   }
-  for (int i = threadIdx.x; i < w.k; i += NT)
-    if (i >= n) w.best[i] = 0;
-  for (int i = threadIdx.x; i < n; i += NT) {
-    const u64 key = from[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += from[j] > key;
-    if (rank < w.k) w.best[rank] = key;
+  // rank by counting the larger keys: a wave takes 64 keys against a share of all of them
+  constexpr int WAVES = NT / 64;
+  const int blocks = (n + 63) / 64;
+  const int parts = blocks > 0 && blocks <= WAVES ? WAVES / blocks : 1;
+  const int len = (n + parts - 1) / parts;
+  if (parts == 1) {
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const u64 key = from[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += from[j] > key;
+      if (rank < w.k) w.best[rank] = key;
+    }
+  } else {
+    const int i = (wave % blocks) * 64 + lane, part = wave / blocks;
+    u64 key = 0;
+    if (part < parts && i < n) {
+      key = from[i];
+      const int j1 = (part + 1) * len < n ? (part + 1) * len : n;
+      int rank = 0;
+#pragma unroll 8
+      for (int j = part * len; j < j1; ++j) rank += from[j] > key;
+      w.hist[part * (blocks * 64) + i] = (uint32_t)rank;
+    }
+    __syncthreads();
+    if (part == 0 && i < n) {
+      int rank = 0;
+      for (int q = 0; q < parts; ++q) rank += (int)w.hist[q * (blocks * 64) + i];
+      if (rank < w.k) w.best[rank] = key;
+    }
   }
+  for (int i = n + threadIdx.x; i < w.k; i += NT) w.best[i] = 0;
   __syncthreads();
 }
 
 // the candidates of one tile: chunks [t0, t1) of `body`, whose first element is entry `first`
-// of the row; groups of GU chunks, NT apart
-template <typename T, int NT, int U, int GU>
+// of the row; groups of GU chunks, NT apart.  Each thread wrote its own groups' maxima, the
+// largest of which is `largest`; the histogram is clear.
+template <typename T, int NT, int U, int GU, int SLOTS>
 __device__ inline void collect_tile(const TopState<NT>& w, const T* body, int64_t first,
-                                    int64_t t0, int64_t t1, int slots) {
+                                    int64_t t0, int64_t t1, float largest) {
+  constexpr int NS = SLOTS / NT;
   const int k = w.k, most = top_groups(k);
-  __syncthreads();   // the group keys are written
-  uint32_t top = 0;
-  int groups = 0;
-  for (int i = threadIdx.x; i < slots; i += NT) {
-    const uint32_t g = w.gkeys[i];
-    top = g > top ? g : top;
-    groups += g != 0;
-  }
-  // bounds of the bisection: all groups, and the largest key
-  float* red = reinterpret_cast<float*>(w.sel);
-  groups = (int)block_sum<NT>((float)groups, red);
+  const int chunks = (int)(t1 - t0);
+  // group j of the thread exists while its first chunk does
+  auto exists = [&](int j) { return j * (NT * (GU == 1 ? 1 : U)) + (int)threadIdx.x < chunks; };
+  const int groups = GU == 1 ? chunks
+                             : chunks / (NT * U) * NT +
+                                   (chunks % (NT * U) < NT ? chunks % (NT * U) : NT);
+  float gv[NS];
+  float least = __builtin_inff();
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t o = __shfl_xor(top, d);
-    top = o > top ? o : top;
+  for (int j = 0; j < NS; ++j) {
+    gv[j] = exists(j) ? w.gmax[j * NT + threadIdx.x] : neg_inf();
+    if (exists(j)) least = __builtin_fminf(least, gv[j]);
   }
-  if constexpr (NT > 64) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(w.sel) + 64;
-    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = top;
-    __syncthreads();
-    for (int i = 0; i < NT / 64; ++i) top = r[i] > top ? r[i] : top;
-  }
-  uint32_t bound = 0;
-  int reach = groups;
-  if (groups > most)
-    reach = bisect<NT, uint32_t>(w.gkeys, slots, k, most, top + 1, w.count, bound);
-  const bool ties = reach > most;             // too many groups at the bound itself
-  const uint32_t from = ties ? bound + 1 : (bound ? bound : 1);
+  // between the smallest of the threads' largest maxima (of all where k is above NT) and the
+  // largest lie at least k; threads with nothing but masked entries do not count
+  float hi = largest, lo = k <= NT ? largest : least;
+  if (lo == neg_inf()) lo = __builtin_inff();
   if (threadIdx.x == 0) w.count[1] = 0;
+  block_bounds<NT>(lo, hi, w.count);
+  const int before = w.count[0];
+  const Bins bins(lo, hi);
+  uint32_t from = 0, bound = 0;   // least keys of the candidates and of the groups
+  float limit = __builtin_inff();
+  bool by_value = false, ties = false;
+  if (groups > most) {
+    int reach = 0;
+    if (bins.usable(lo)) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        if (exists(j) && gv[j] >= lo) bins.add(w.hist, gv[j]);
+      __syncthreads();
+      reach = hist_bound(w.hist, k, limit);
+    }
+    by_value = reach >= k && reach <= most;
+    if (!by_value) {
+      reach = bisect<NT, uint32_t>([&](uint32_t x) {
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) c += __popcll(__ballot(exists(j) && value_key(gv[j]) >= x));
+        return c;
+      }, groups, k, most, value_key(hi) + 1, w.count, bound);
+      ties = reach > most;   // too many groups at the bound itself
+      from = bound + ties;
+    }
+  }
+  auto passes = [&](float v) {
+    return by_value ? v >= lo && bins.at(v) < limit : value_key(v) >= from;
+  };
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) mine |= (uint32_t)(exists(j) && passes(gv[j])) << j;
+  if (mine) {
+    int at = atomicAdd(&w.count[1], __popc(mine));
+    do {
+      w.glist[at++] = (uint32_t)((__builtin_ctz(mine)) * NT + threadIdx.x);
+      mine &= mine - 1;
+    } while (mine);
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < slots; i += NT)
-    if (w.gkeys[i] >= from) w.glist[atomicAdd(&w.count[1], 1)] = (uint32_t)i;
-  __syncthreads();
-  const int chosen = w.count[1], before = w.count[0];
+  const int chosen = w.count[1];
   for (int i = threadIdx.x; i < chosen * GU; i += NT) {
     const int g = (int)w.glist[i / GU], u = i % GU;
     const int64_t q = GU == 1 ? t0 + g : t0 + (int64_t)(g / NT) * (NT * U) + u * NT + g % NT;
@@ -237,29 +509,33 @@ __device__ inline void collect_tile(const TopState<NT>& w, const T* body, int64_
     c.load(body + q * 8);
     float f[8];
     c.widen(f);
+    uint32_t hits = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (value_key(f[e]) >= from)
-        w.cand[atomicAdd(&w.count[0], 1)] = entry_key(f[e], (uint32_t)(first + q * 8 + e));
-    }
+    for (int e = 0; e < 8; ++e) hits |= (uint32_t)passes(f[e]) << e;
+    if (hits == 0) continue;
+    int at = atomicAdd(&w.count[0], __popc(hits));
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (hits >> e & 1) w.cand[at++] = entry_key(f[e], (uint32_t)(first + q * 8 + e));
   }
   __syncthreads();
   if (!ties) return;
   // the first k - (those above) entries equal to the bound, chunk by chunk in the row's order
-  int need = k - (w.count[0] - before), half = 0;
+  int need = k - (w.count[0] - before);
+  int half = 0;
   for (int64_t base = t0; base < t1 && need > 0; base += NT) {
     const int64_t q = base + threadIdx.x;
     float f[8];
-    int mine = 0;
+    int equal = 0;
     if (q < t1) {
       Chunk<T> c;
       c.load(body + q * 8);
       c.widen(f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mine += value_key(f[e]) == bound;
+      for (int e = 0; e < 8; ++e) equal += value_key(f[e]) == bound;
     }
     // the number before this thread's, in the wave and then over the waves
-    int incl = mine;
+    int incl = equal;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(incl, d);
@@ -267,12 +543,12 @@ __device__ inline void collect_tile(const TopState<NT>& w, const T* body, int64_
     }
     const int wave_total = __shfl(incl, 63);
     const int total = block_count<NT>(wave_total, w.count, half);
-    int rank = incl - mine;
+    int rank = incl - equal;
     if constexpr (NT > 64) {
-      const int* c = w.count + 2 + (half ^ 1) * (NT / 64);
+      const int* c = w.count + 4 + (half ^ 1) * (NT / 64);
       for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) rank += c[i];
     }
-    if (q < t1 && mine) {
+    if (q < t1 && equal) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (value_key(f[e]) == bound) {
@@ -384,20 +660,17 @@ __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum
 }
 
 // what a thread reads of a row ahead of the stream: the target, or its first teacher entry
-template <typename T, int MODE>
-__device__ inline Entry row_entry(const VocabArgs& a, int64_t r, float& z_mine) {
-  Entry e{-1, neg_inf()};
-  z_mine = 0.0f;
+template <int MODE> __device__ inline Entry row_entry(const VocabArgs& a, int64_t r) {
   if constexpr (MODE == kLogprobs) {
+    Entry e{-1, neg_inf()};
     if (a.target && threadIdx.x == 0) {
       const int64_t id = a.target[r];
       if (id >= 0 && id < a.V) e.id = id;
     }
+    return e;
   } else {
-    e = load_entry(a, r, threadIdx.x);
+    return load_entry(a, r, threadIdx.x);
   }
-  if (e.id >= 0) z_mine = to_f32(static_cast<const T*>(a.z)[r * a.ld + e.id]);
-  return e;
 }
 
 extern __shared__ __attribute__((aligned(16))) char swg_vocab_lds[];
@@ -409,12 +682,12 @@ template <typename T> struct Pass { static constexpr int U = sizeof(T) == 2 ? 4 
 // One row, or one of `split` segments of it, by a workgroup of NT threads.  A segment leaves
 // its sums and its k best keys in the workspace; join_kernel finishes the row.
 template <typename T, int NT, int GU, int SLOTS, int MODE, bool TOP, bool ENT>
-__global__ __launch_bounds__(NT) void rows_kernel(VocabArgs a, int split, int64_t seg,
-                                                  Soft* part, u64* part_keys) {
+__global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int split, int64_t seg,
+                                                     Soft* part, u64* part_keys) {
   constexpr int U = Pass<T>::U;
   constexpr int ITERS = SLOTS * GU / (NT * U);   // passes of a tile
-  __shared__ float red[NT / 64];
-  __shared__ int count[2 + 2 * (NT / 64)];
+  __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
+  __shared__ int count[TopCount<NT>::N];
   TopState<NT> w;
   const int k = (int)a.top;
   if constexpr (TOP) {
@@ -422,8 +695,9 @@ __global__ __launch_bounds__(NT) void rows_kernel(VocabArgs a, int split, int64_
     w.cand = reinterpret_cast<u64*>(swg_vocab_lds);
     w.sel = w.cand + top_candidates(k, GU * 8);
     w.best = w.sel + k + kSlack;
-    w.gkeys = reinterpret_cast<uint32_t*>(w.best + k);
-    w.glist = w.gkeys + SLOTS;
+    w.gmax = reinterpret_cast<float*>(w.best + k);
+    w.hist = reinterpret_cast<uint32_t*>(w.gmax + SLOTS);
+    w.glist = w.hist + kBins;
     w.count = count;
   }
   const float c = a.inv_t * kLog2e;
@@ -433,27 +707,13 @@ __global__ __launch_bounds__(NT) void rows_kernel(VocabArgs a, int split, int64_
     const RowCut cut(z, a.V);
     const T* body = z + cut.head;
     const int64_t c0 = part_i * seg, c1 = c0 + seg < cut.chunks ? c0 + seg : cut.chunks;
-    float z_mine = 0.0f;
+    const int64_t lone = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
     Entry mine{-1, neg_inf()};
-    if (split == 1) mine = row_entry<T, MODE>(a, r, z_mine);
-    if constexpr (TOP) {
-      __syncthreads();
-      if (threadIdx.x == 0) count[0] = 0;
-      __syncthreads();
-    }
-    Soft sum{kLowest, 0.0f, 0.0f};
-    {
-      const int64_t i = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
-      if (i >= 0) {
-        const float x = to_f32(z[i]);
-        sum.m = __builtin_fmaxf(sum.m, x);
-        soft_add<ENT>(sum, x, c);
-        if constexpr (TOP) w.cand[atomicAdd(&count[0], 1)] = entry_key(x, (uint32_t)i);
-      }
-    }
-    // one pass: U chunks of the thread, from `base` on
-    auto load = [&](Chunk<T>* ch, int64_t base) {
-      if (base + NT * U <= c1) {
+    if (split == 1) mine = row_entry<MODE>(a, r);
+    float z_lone = lone >= 0 ? to_f32(z[lone]) : neg_inf();
+    // one pass: U chunks of the thread, from `base` on, before t1
+    auto load = [&](Chunk<T>* ch, int64_t base, int64_t t1) {
+      if (base + NT * U <= t1) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
           ch[u].load_stream(body + (base + u * NT + threadIdx.x) * 8);
@@ -462,69 +722,98 @@ __global__ __launch_bounds__(NT) void rows_kernel(VocabArgs a, int split, int64_
         for (int u = 0; u < U; ++u) {
           const int64_t q = base + u * NT + threadIdx.x;
           fill_masked(ch[u]);
-          if (q < c1) ch[u].load_stream(body + q * 8);
+          if (q < t1) ch[u].load_stream(body + q * 8);
         }
       }
     };
+    const int64_t tile = (int64_t)ITERS * NT * U;
     Chunk<T> cur[U], next[U];
-    load(cur, c0);
-    for (int64_t t0 = c0; t0 < c1; t0 += (int64_t)ITERS * NT * U) {
-      const int64_t t1 = TOP && t0 + ITERS * NT * U < c1 ? t0 + ITERS * NT * U : c1;
+    load(cur, c0, TOP && c0 + tile < c1 ? c0 + tile : c1);
+    const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
+
+    __syncthreads();   // LDS of the item before
+    if constexpr (TOP) {
+      if (threadIdx.x == 0) count[0] = 0;
+      for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
+      __syncthreads();
+    }
+    Run sum{kNoRef, neg_inf(), 0.0f, 0.0f};
+    if (lone >= 0) {
+      run_single(sum, z_lone, c);
+      if constexpr (TOP) w.cand[atomicAdd(&count[0], 1)] = entry_key(z_lone, (uint32_t)lone);
+    }
+    for (int64_t t0 = c0; t0 < c1; t0 += tile) {
+      const int64_t t1 = TOP && t0 + tile < c1 ? t0 + tile : c1;
+      float largest = neg_inf();   // of this tile's chunks
       int it = 0;
       for (int64_t base = t0; base < t1; base += NT * U, ++it) {
-        load(next, base + NT * U);
-        float f[U][8], gm[U];
+        load(next, base + NT * U, t1);
+        float group = neg_inf();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          cur[u].widen(f[u]);
-          gm[u] = __builtin_fmaxf(
-              __builtin_fmaxf(__builtin_fmaxf(f[u][0], f[u][1]),
-                              __builtin_fmaxf(f[u][2], f[u][3])),
-              __builtin_fmaxf(__builtin_fmaxf(f[u][4], f[u][5]),
-                              __builtin_fmaxf(f[u][6], f[u][7])));
-        }
-        float m = gm[0];
+          float f[8];
+          cur[u].widen(f);
+          float gm = max8(f);
+          if constexpr (TOP) {
+            // only a signaling NaN or 8 NaN come out as NaN; of the others the largest counts
+            if (gm != gm) {
+              gm = neg_inf();
 #pragma unroll
-        for (int u = 1; u < U; ++u) m = __builtin_fmaxf(m, gm[u]);
-        if constexpr (TOP) {
-          if constexpr (GU == 1) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-              w.gkeys[(it * U + u) * NT + threadIdx.x] =
-                  base + u * NT + threadIdx.x < t1 ? value_key(gm[u]) : 0;
-          } else {
-            w.gkeys[it * NT + threadIdx.x] = base + threadIdx.x < t1 ? value_key(m) : 0;
+              for (int i = 0; i < 8; ++i) gm = f[i] > gm ? f[i] : gm;
+            }
+            if constexpr (GU == 1) w.gmax[(it * U + u) * NT + threadIdx.x] = gm;
+            group = max2(group, gm);
           }
+          run_chunk<ENT>(sum, f, gm, c);
         }
-        soft_move(sum, __builtin_fmaxf(sum.m, m), c);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) soft_add<ENT>(sum, f[u][i], c);
+        if constexpr (TOP) {
+          if constexpr (GU > 1) w.gmax[it * NT + threadIdx.x] = group;
+          largest = max2(largest, group);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) cur[u] = next[u];
       }
       if constexpr (TOP) {
-        collect_tile<T, NT, U, GU>(w, body, cut.head, t0, t1, it * (GU == 1 ? U : 1) * NT);
+        collect_tile<T, NT, U, GU, SLOTS>(w, body, cut.head, t0, t1, largest);
         if (t1 < c1) {   // the best so far are the next tile's first candidates
-          order_top<NT>(w, count[0]);
+          order_top<NT>(w, count[0], 0);
           const int n = count[0] < k ? count[0] : k;
           for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = w.best[i];
+          for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
           __syncthreads();
           if (threadIdx.x == 0) count[0] = n;
+          load(cur, t1, t1 + tile < c1 ? t1 + tile : c1);
         }
       }
       if constexpr (!TOP) break;
     }
-    soft_block<NT>(sum, c, red);
-    if constexpr (TOP) {
+    run_block<NT>(sum, red);
+    Soft soft;
+    if (run_in_range(sum.m, c)) {
+      soft = run_soft(sum, c);
+    } else {
+      soft = Soft{sum.m, 0.0f, 0.0f};
+      if (lone >= 0) soft_add<ENT>(soft, z_lone, c);
+      for (int64_t q = c0 + threadIdx.x; q < c1; q += NT) {
+        Chunk<T> ch;
+        ch.load(body + q * 8);
+        float f[8];
+        ch.widen(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) soft_add<ENT>(soft, f[i], c);
+      }
       __syncthreads();
-      order_top<NT>(w, count[0]);
+      soft.s = block_sum<NT>(soft.s, red);
+      soft.t = block_sum<NT>(soft.t, red);
+    }
+    if constexpr (TOP) {
+      if constexpr (NT == 64) __syncthreads();
+      order_top<NT>(w, count[0], 0);
     }
     if (split == 1) {
-      finish_row<T, NT, MODE>(a, r, sum, TOP ? w.best : nullptr, mine, z_mine, red);
+      finish_row<T, NT, MODE>(a, r, soft, TOP ? w.best : nullptr, mine, z_mine, red);
     } else {
-      if (threadIdx.x == 0) part[item] = sum;
+      if (threadIdx.x == 0) part[item] = soft;
       if constexpr (TOP) {
         for (int i = threadIdx.x; i < k; i += NT) part_keys[item * k + i] = w.best[i];
       }
@@ -538,7 +827,7 @@ __global__ __launch_bounds__(256) void join_kernel(VocabArgs a, int split, const
                                                    const u64* part_keys) {
   constexpr int NT = 256;
   __shared__ float red[NT / 64];
-  __shared__ int count[2 + 2 * (NT / 64)];
+  __shared__ int count[TopCount<NT>::N];
   const float c = a.inv_t * kLog2e;
   const int k = (int)a.top, n = k * split;
   TopState<NT> w;
@@ -546,21 +835,28 @@ __global__ __launch_bounds__(256) void join_kernel(VocabArgs a, int split, const
   w.cand = reinterpret_cast<u64*>(swg_vocab_lds);
   w.sel = w.cand + n;
   w.best = w.sel + k + kSlack;
-  w.gkeys = w.glist = nullptr;
+  w.hist = reinterpret_cast<uint32_t*>(w.best + k);
+  w.gmax = nullptr;
+  w.glist = nullptr;
   w.count = count;
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-    float z_mine;
-    const Entry mine = row_entry<T, MODE>(a, r, z_mine);
+    const Entry mine = row_entry<MODE>(a, r);
+    const float z_mine =
+        mine.id >= 0 ? to_f32(static_cast<const T*>(a.z)[r * a.ld + mine.id]) : 0.0f;
     Soft sum{kLowest, 0.0f, 0.0f};
     if ((int)threadIdx.x < split) sum = part[r * split + threadIdx.x];
-    if (k > 0) {
-      for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = part_keys[r * n + i];
-      if (threadIdx.x == 0) count[0] = n;
-    }
+    for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = part_keys[r * n + i];
     soft_block<NT>(sum, c, red);
     if (k > 0) {
       __syncthreads();
-      order_top<NT>(w, n);
+      // each segment's last key bounds the row's last one from below
+      u64 floor_key = 0;
+#pragma unroll 8
+      for (int i = 0; i < split; ++i) {
+        const u64 key = w.cand[i * k + k - 1];
+        floor_key = key > floor_key ? key : floor_key;
+      }
+      order_top<NT>(w, n, floor_key);
     }
     finish_row<T, NT, MODE>(a, r, sum, k > 0 ? w.best : nullptr, mine, z_mine, red);
     __syncthreads();
@@ -725,7 +1021,7 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split) {
 // ------------------------------------------------------------------ launches
 static size_t top_lds(int k, int group, int slots) {
   return sizeof(u64) * (size_t)(top_candidates(k, group) + 2 * k + kSlack) +
-         sizeof(uint32_t) * (size_t)(slots + top_groups(k));
+         sizeof(uint32_t) * (size_t)(slots + top_groups(k) + kBins);
 }
 
 template <typename T, int MODE, bool ENT>
@@ -754,7 +1050,9 @@ static hipError_t forward_rows(const VocabArgs& a, const VocabPlan& p, void* ws,
 #undef SWG_ROWS
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.split == 1) return e;
-  const size_t lds = k > 0 ? sizeof(u64) * (size_t)(k * p.split + 2 * k + kSlack) : 0;
+  const size_t lds = k > 0 ? sizeof(u64) * (size_t)(k * p.split + 2 * k + kSlack) +
+                                 sizeof(uint32_t) * kBins
+                           : 0;
   SWG_LAUNCH((join_kernel<T, MODE>), dim3(row_grid(a.R)), dim3(256), lds, stream, a, p.split,
              part, keys);
   return hipGetLastError();
