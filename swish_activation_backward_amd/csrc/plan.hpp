@@ -325,31 +325,33 @@ inline NormPlan plan_norm_bwd(int64_t M, int64_t N) {
 }
 
 // Operators on logits [R, V]: a workgroup of `threads` reads a row, or one of `split` segments
-// of `seg` chunks (8 elements) where the rows alone do not fill the GPU.  A split row's sums
-// (12 bytes a segment) and best keys (8 bytes each, from byte keys_at on) go through the
-// workspace.
+// of `seg` chunks (8 elements) where the rows alone do not fill the GPU.  Segments are whole
+// passes of 256 threads (64 bytes each); a split row leaves the segments' sums (12 bytes each)
+// and, for its top entries, row_max group maxima (fp32, one to a thread and pass, from byte
+// max_at on) in the workspace.
 struct VocabPlan {
   int threads, split;
   int64_t seg;
-  size_t keys_at;
+  int64_t row_max;
+  size_t max_at;
   size_t ws_bytes;
 };
 
 inline VocabPlan plan_vocab(int64_t R, int64_t V, int64_t top, int dtype) {
   VocabPlan p{};
-  const int64_t chunks = ceil_div(V, 8);
-  // segments of 2048 elements at least, 64 at most, for 512 workgroups
-  int64_t split = ceil_div(512, R < 1 ? 1 : R);
-  if (split > chunks / 256) split = chunks / 256;
+  const int64_t pass = dtype == 2 ? 512 : 1024;   // chunks
+  const int64_t passes = ceil_div(V, 8 * pass);
+  int64_t split = R < 512 ? ceil_div(1024, R < 1 ? 1 : R) : 1;
+  if (split > passes) split = passes;
   if (split > 64) split = 64;
-  if (top * split > 4096) split = 4096 / top;   // the joining workgroup holds all best keys
   if (split < 1) split = 1;
-  p.seg = ceil_div(chunks, split);
-  p.split = (int)ceil_div(chunks, p.seg);
-  p.threads = p.split > 1 ? 256 : V <= 4096 ? 64 : V <= 32768 ? 256 : 512;
+  p.seg = ceil_div(passes, split) * pass;
+  p.split = (int)ceil_div(passes * pass, p.seg);
+  p.threads = V <= 4096 ? 64 : 256;
+  p.row_max = passes * 256;
   if (p.split > 1) {
-    p.keys_at = (size_t)ceil_div(R * p.split * 12, 16) * 16;
-    p.ws_bytes = p.keys_at + (size_t)(R * p.split * top) * 8;
+    p.max_at = (size_t)ceil_div(R * p.split * 12, 16) * 16;
+    p.ws_bytes = p.max_at + (top > 0 ? (size_t)(R * p.row_max) * 4 : 0);
   }
   return p;
 }

@@ -75,13 +75,6 @@ template <bool ENT> __device__ inline void soft_add(Soft& a, float z, float c) {
   if constexpr (ENT) a.t = __builtin_fmaf(bound_d(d), e, a.t);
 }
 
-template <int NT> __device__ inline void soft_block(Soft& a, float c, float* red) {
-  const float m = block_max<NT>(a.m, red);
-  soft_move(a, m, c);
-  a.s = block_sum<NT>(a.s, red);
-  a.t = block_sum<NT>(a.t, red);
-}
-
 // The running form, where an element costs one fma, one exponential, an addition and the fma
 // of t: d = z c - b against a reference b that need not be the maximum.  b moves only when a
 // chunk's largest d passes kLift, so that few waves ever branch; up to there an fp32 sum loses
@@ -222,19 +215,17 @@ __device__ inline float log_prob(const RowStat& r, float z, float inv_t) {
 // pass and a scan of 512 bins.  Where that leaves too many groups (equal or masked entries),
 // it comes from a bisection of the keys, and where equal values leave no bound with few
 // groups, the entries above it are candidates and, of those equal to it, the first ones by
-// index, found by a scan of the row.
-constexpr int kSlack = 64;          // keys a selection may leave beyond k before the ordering
+// index, found by a scan of the row.  Where the chosen groups hold too many entries (rows in
+// order), a bisection of their keys raises the bound.
+constexpr int kSlack = 64;          // entries of a tile that may be candidates beyond k
 constexpr int kBins = 512;
 __host__ __device__ inline int top_groups(int k) { return k + k / 8 + 8; }
-__host__ __device__ inline int top_candidates(int k, int group) {
-  return top_groups(k) * group + 2 * k + 16;
-}
+// a tile's, the best k so far and the row's single elements
+__host__ __device__ inline int top_candidates(int k) { return 2 * k + kSlack + 16; }
 
 template <int NT> struct TopState {
-  float* gmax;       // one per group of the tile
   uint32_t* glist;   // chosen groups
   u64* cand;         // candidates
-  u64* sel;          // k + kSlack
   u64* best;         // k, in order
   uint32_t* hist;    // kBins, and the partial ranks
   int* count;        // TopCount<NT>::N
@@ -351,75 +342,32 @@ __device__ inline int bisect(F count_from, int n, int k, int most, K hi, int* co
   return at_lo;
 }
 
-__device__ inline float key_float(u64 key) { return key_value((uint32_t)(key >> 32)); }
-
-// the k largest of the n candidates to `best`, in falling order; the rest of best becomes 0.
-// At least k of the candidates are >= floor_key.  Called after a barrier, ends with one.
-template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n, u64 floor_key) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const u64* from = w.cand;
-  if (n > w.k + kSlack) {
-    // a bound by value, or else by the keys themselves
-    float lo = __builtin_inff(), hi = neg_inf(), limit = 0.0f;
-    for (int i = threadIdx.x; i < n; i += NT) {
-      const u64 key = w.cand[i];
-      if (key >= floor_key && key != 0) {
-        lo = __builtin_fminf(lo, key_float(key));
-        hi = __builtin_fmaxf(hi, key_float(key));
-      }
-    }
-    for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
-    if (threadIdx.x == 0) w.count[1] = 0;
-    block_bounds<NT>(lo, hi, w.count);
-    const Bins bins(lo, hi);
-    auto counts = [&](u64 key) { return key != 0 && key_float(key) >= lo; };
-    int reach = 0;
-    if (bins.usable(lo)) {
-      for (int i = threadIdx.x; i < n; i += NT)
-        if (counts(w.cand[i])) bins.add(w.hist, key_float(w.cand[i]));
-      __syncthreads();
-      reach = hist_bound(w.hist, w.k, limit);
-    }
-    u64 least = 0;
-    const bool by_value = reach >= w.k && reach <= w.k + kSlack;
-    if (!by_value)
-      bisect<NT, u64>([&](u64 x) {
-        int c = 0;
-        for (int i = wave * 64; i < n; i += NT)
-          c += __popcll(__ballot(i + lane < n && w.cand[i + lane] >= x));
-        return c;
-      }, n, w.k, w.k + kSlack, ~0ull, w.count, least);
-    for (int i = threadIdx.x; i < n; i += NT) {
-      const u64 key = w.cand[i];
-      if (by_value ? counts(key) && bins.at(key_float(key)) < limit : key >= least)
-        w.sel[atomicAdd(&w.count[1], 1)] = key;
-    }
-    __syncthreads();
-    from = w.sel;
-    n = w.count[1];
-  }
-  // rank by counting the larger keys: a wave takes 64 keys against a share of all of them
+// the k largest of the n candidates to `best`, in falling order; called after a barrier, ends
+// with one.  The rank of a key is the number of larger ones: a wave takes 64 keys against a
+// share of all of them.
+template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n) {
   constexpr int WAVES = NT / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int blocks = (n + 63) / 64;
   const int parts = blocks > 0 && blocks <= WAVES ? WAVES / blocks : 1;
-  const int len = (n + parts - 1) / parts;
   if (parts == 1) {
     for (int i = threadIdx.x; i < n; i += NT) {
-      const u64 key = from[i];
+      const u64 key = w.cand[i];
       int rank = 0;
 #pragma unroll 8
-      for (int j = 0; j < n; ++j) rank += from[j] > key;
+      for (int j = 0; j < n; ++j) rank += w.cand[j] > key;
       if (rank < w.k) w.best[rank] = key;
     }
   } else {
+    const int len = (n + parts - 1) / parts;
     const int i = (wave % blocks) * 64 + lane, part = wave / blocks;
     u64 key = 0;
     if (part < parts && i < n) {
-      key = from[i];
+      key = w.cand[i];
       const int j1 = (part + 1) * len < n ? (part + 1) * len : n;
       int rank = 0;
 #pragma unroll 8
-      for (int j = part * len; j < j1; ++j) rank += from[j] > key;
+      for (int j = part * len; j < j1; ++j) rank += w.cand[j] > key;
       w.hist[part * (blocks * 64) + i] = (uint32_t)rank;
     }
     __syncthreads();
@@ -429,29 +377,38 @@ template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n,
       if (rank < w.k) w.best[rank] = key;
     }
   }
-  for (int i = n + threadIdx.x; i < w.k; i += NT) w.best[i] = 0;
   __syncthreads();
 }
 
+// The thread's group j of a tile exists while its first chunk does.
+template <int NT, int U, int GU> __device__ inline bool group_exists(int j, int chunks) {
+  return j * (NT * (GU == 1 ? 1 : U)) + (int)threadIdx.x < chunks;
+}
+// element j NT + thread of `gmax` is the maximum of the thread's group j
+template <int NT, int U, int GU, int NS>
+__device__ inline void load_groups(const float* gmax, int64_t chunks, float (&gv)[NS]) {
+#pragma unroll
+  for (int j = 0; j < NS; ++j)
+    gv[j] = group_exists<NT, U, GU>(j, (int)chunks) ? gmax[j * NT + threadIdx.x] : neg_inf();
+}
+
 // the candidates of one tile: chunks [t0, t1) of `body`, whose first element is entry `first`
-// of the row; groups of GU chunks, NT apart.  Each thread wrote its own groups' maxima, the
-// largest of which is `largest`; the histogram is clear.
+// of the row; groups of GU chunks, NT apart.  gv[j] is the maximum of the thread's group j, -inf
+// for none; the histogram is clear.
 template <typename T, int NT, int U, int GU, int SLOTS>
-__device__ inline void collect_tile(const TopState<NT>& w, const T* body, int64_t first,
-                                    int64_t t0, int64_t t1, float largest) {
+__device__ inline void collect_tile(const TopState<NT>& w, const float (&gv)[SLOTS / NT],
+                                    const T* body, int64_t first, int64_t t0, int64_t t1) {
   constexpr int NS = SLOTS / NT;
   const int k = w.k, most = top_groups(k);
   const int chunks = (int)(t1 - t0);
-  // group j of the thread exists while its first chunk does
-  auto exists = [&](int j) { return j * (NT * (GU == 1 ? 1 : U)) + (int)threadIdx.x < chunks; };
+  auto exists = [&](int j) { return group_exists<NT, U, GU>(j, chunks); };
   const int groups = GU == 1 ? chunks
                              : chunks / (NT * U) * NT +
                                    (chunks % (NT * U) < NT ? chunks % (NT * U) : NT);
-  float gv[NS];
-  float least = __builtin_inff();
+  float least = __builtin_inff(), largest = neg_inf();
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
-    gv[j] = exists(j) ? w.gmax[j * NT + threadIdx.x] : neg_inf();
+    largest = max2(largest, gv[j]);
     if (exists(j)) least = __builtin_fminf(least, gv[j]);
   }
   // between the smallest of the threads' largest maxima (of all where k is above NT) and the
@@ -501,24 +458,55 @@ __device__ inline void collect_tile(const TopState<NT>& w, const T* body, int64_
   }
   __syncthreads();
   const int chosen = w.count[1];
-  for (int i = threadIdx.x; i < chosen * GU; i += NT) {
-    const int g = (int)w.glist[i / GU], u = i % GU;
-    const int64_t q = GU == 1 ? t0 + g : t0 + (int64_t)(g / NT) * (NT * U) + u * NT + g % NT;
-    if (q >= t1) continue;
-    Chunk<T> c;
-    c.load(body + q * 8);
-    float f[8];
-    c.widen(f);
+  auto each_chunk = [&](auto use) {   // of the chosen groups
+    for (int i = threadIdx.x; i < chosen * GU; i += NT) {
+      const int g = (int)w.glist[i / GU], u = i % GU;
+      const int64_t q = GU == 1 ? t0 + g : t0 + (int64_t)(g / NT) * (NT * U) + u * NT + g % NT;
+      if (q >= t1) continue;
+      Chunk<T> c;
+      c.load(body + q * 8);
+      float f[8];
+      c.widen(f);
+      use(f, (uint32_t)(first + q * 8));
+    }
+  };
+  const int room = before + k + kSlack;
+  each_chunk([&](const float* f, uint32_t id) {
     uint32_t hits = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) hits |= (uint32_t)passes(f[e]) << e;
-    if (hits == 0) continue;
+    if (hits == 0) return;
     int at = atomicAdd(&w.count[0], __popc(hits));
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (hits >> e & 1) w.cand[at++] = entry_key(f[e], (uint32_t)(first + q * 8 + e));
-  }
+    for (int e = 0; e < 8; ++e) {
+      if (hits >> e & 1) {
+        if (at < room) w.cand[at] = entry_key(f[e], id + e);
+        ++at;
+      }
+    }
+  });
   __syncthreads();
+  if (w.count[0] > room) {
+    u64 lowest;
+    bisect<NT, u64>([&](u64 x) {
+      int c = 0;
+      each_chunk([&](const float* f, uint32_t id) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c += passes(f[e]) && entry_key(f[e], id + e) >= x;
+      });
+      return (int)lanes_sum<64>((float)c);
+    }, w.count[0] - before, k, k + kSlack, ~0ull, w.count, lowest);
+    if (threadIdx.x == 0) w.count[0] = before;
+    __syncthreads();
+    each_chunk([&](const float* f, uint32_t id) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const u64 key = entry_key(f[e], id + e);
+        if (passes(f[e]) && key >= lowest) w.cand[atomicAdd(&w.count[0], 1)] = key;
+      }
+    });
+    __syncthreads();
+  }
   if (!ties) return;
   // the first k - (those above) entries equal to the bound, chunk by chunk in the row's order
   int need = k - (w.count[0] - before);
@@ -560,6 +548,16 @@ __device__ inline void collect_tile(const TopState<NT>& w, const T* body, int64_
     }
     need -= total;
   }
+  __syncthreads();
+}
+
+// the best k candidates become the only ones, and the histogram is clear
+template <int NT> __device__ inline void keep_best(const TopState<NT>& w) {
+  const int n = w.count[0] < w.k ? w.count[0] : w.k;
+  order_top<NT>(w, w.count[0]);
+  for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = w.best[i];
+  for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
+  if (threadIdx.x == 0) w.count[0] = n;
   __syncthreads();
 }
 
@@ -679,30 +677,54 @@ extern __shared__ __attribute__((aligned(16))) char swg_vocab_lds[];
 // is worked on.
 template <typename T> struct Pass { static constexpr int U = sizeof(T) == 2 ? 4 : 2; };
 
-// One row, or one of `split` segments of it, by a workgroup of NT threads.  A segment leaves
-// its sums and its k best keys in the workspace; join_kernel finishes the row.
-template <typename T, int NT, int GU, int SLOTS, int MODE, bool TOP, bool ENT>
-__global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int split, int64_t seg,
-                                                     Soft* part, u64* part_keys) {
-  constexpr int U = Pass<T>::U;
-  constexpr int ITERS = SLOTS * GU / (NT * U);   // passes of a tile
+// What a workgroup does about the top entries: nothing, their selection, or, where it has a
+// segment of the row only, leaving the group maxima to join_kernel.
+enum { kNoTop = 0, kTop = 1, kTopLater = 2 };
+
+// a tile's LDS beside the group maxima
+__device__ inline void top_lds_layout(u64* lds, int k, u64*& cand, u64*& best, uint32_t*& hist,
+                                      uint32_t*& glist) {
+  cand = lds;
+  best = cand + top_candidates(k);
+  hist = reinterpret_cast<uint32_t*>(best + k);
+  glist = hist + kBins;
+}
+static size_t top_lds_bytes(int k) {
+  return sizeof(u64) * (size_t)(top_candidates(k) + k) +
+         sizeof(uint32_t) * (size_t)(kBins + top_groups(k));
+}
+
+// A row's passes are NT U chunks each and its tiles, over which top entries are selected at a
+// time, SLOTS groups of GU chunks.
+template <typename T, int NT, int GU, int SLOTS> struct RowShape {
+  static constexpr int U = Pass<T>::U;
+  static constexpr int64_t PASS = NT * U;
+  static constexpr int ITERS = SLOTS * GU / (NT * U);   // passes of a tile
+  static constexpr int64_t TILE = ITERS * PASS;
+};
+
+// One row, or one segment of it (blockIdx.y of gridDim.y, `seg` chunks each, whole passes), by a
+// workgroup of NT threads.  A segment leaves its sums in the workspace; join_kernel finishes the
+// row.
+template <typename T, int NT, int GU, int SLOTS, int MODE, int TOP, bool ENT>
+__global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, Soft* part,
+                                                     float* part_max, int64_t row_max) {
+  using Shape = RowShape<T, NT, GU, SLOTS>;
+  constexpr int U = Shape::U;
+  constexpr int64_t PASS = Shape::PASS, TILE = Shape::TILE;
   __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
   __shared__ int count[TopCount<NT>::N];
+  __shared__ float gmax[TOP == kTop ? SLOTS : 1];
   TopState<NT> w;
   const int k = (int)a.top;
-  if constexpr (TOP) {
+  if constexpr (TOP == kTop) {
     w.k = k;
-    w.cand = reinterpret_cast<u64*>(swg_vocab_lds);
-    w.sel = w.cand + top_candidates(k, GU * 8);
-    w.best = w.sel + k + kSlack;
-    w.gmax = reinterpret_cast<float*>(w.best + k);
-    w.hist = reinterpret_cast<uint32_t*>(w.gmax + SLOTS);
-    w.glist = w.hist + kBins;
     w.count = count;
+    top_lds_layout(reinterpret_cast<u64*>(swg_vocab_lds), k, w.cand, w.best, w.hist, w.glist);
   }
   const float c = a.inv_t * kLog2e;
-  for (int64_t item = blockIdx.x; item < a.R * split; item += gridDim.x) {
-    const int64_t r = item / split, part_i = item % split;
+  const int split = (int)gridDim.y, part_i = (int)blockIdx.y;
+  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const T* z = static_cast<const T*>(a.z) + r * a.ld;
     const RowCut cut(z, a.V);
     const T* body = z + cut.head;
@@ -713,7 +735,7 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int split, int
     float z_lone = lone >= 0 ? to_f32(z[lone]) : neg_inf();
     // one pass: U chunks of the thread, from `base` on, before t1
     auto load = [&](Chunk<T>* ch, int64_t base, int64_t t1) {
-      if (base + NT * U <= t1) {
+      if (base + PASS <= t1) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
           ch[u].load_stream(body + (base + u * NT + threadIdx.x) * 8);
@@ -726,13 +748,12 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int split, int
         }
       }
     };
-    const int64_t tile = (int64_t)ITERS * NT * U;
     Chunk<T> cur[U], next[U];
-    load(cur, c0, TOP && c0 + tile < c1 ? c0 + tile : c1);
+    load(cur, c0, TOP == kTop && c0 + TILE < c1 ? c0 + TILE : c1);
     const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
 
-    __syncthreads();   // LDS of the item before
-    if constexpr (TOP) {
+    __syncthreads();   // LDS of the row before
+    if constexpr (TOP == kTop) {
       if (threadIdx.x == 0) count[0] = 0;
       for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
       __syncthreads();
@@ -740,52 +761,53 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int split, int
     Run sum{kNoRef, neg_inf(), 0.0f, 0.0f};
     if (lone >= 0) {
       run_single(sum, z_lone, c);
-      if constexpr (TOP) w.cand[atomicAdd(&count[0], 1)] = entry_key(z_lone, (uint32_t)lone);
+      if constexpr (TOP == kTop)
+        w.cand[atomicAdd(&count[0], 1)] = entry_key(z_lone, (uint32_t)lone);
     }
-    for (int64_t t0 = c0; t0 < c1; t0 += tile) {
-      const int64_t t1 = TOP && t0 + tile < c1 ? t0 + tile : c1;
-      float largest = neg_inf();   // of this tile's chunks
-      int it = 0;
-      for (int64_t base = t0; base < t1; base += NT * U, ++it) {
-        load(next, base + NT * U, t1);
+    for (int64_t t0 = c0; t0 < c1; t0 += TILE) {
+      const int64_t t1 = TOP == kTop && t0 + TILE < c1 ? t0 + TILE : c1;
+      float* out_max = nullptr;
+      if constexpr (TOP == kTop) out_max = gmax + threadIdx.x;
+      if constexpr (TOP == kTopLater)
+        out_max = part_max + r * row_max + t0 / GU + threadIdx.x;
+      for (int64_t base = t0; base < t1; base += PASS) {
+        load(next, base + PASS, t1);
         float group = neg_inf();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           float f[8];
           cur[u].widen(f);
           float gm = max8(f);
-          if constexpr (TOP) {
+          if constexpr (TOP != kNoTop) {
             // only a signaling NaN or 8 NaN come out as NaN; of the others the largest counts
             if (gm != gm) {
               gm = neg_inf();
 #pragma unroll
               for (int i = 0; i < 8; ++i) gm = f[i] > gm ? f[i] : gm;
             }
-            if constexpr (GU == 1) w.gmax[(it * U + u) * NT + threadIdx.x] = gm;
+            if constexpr (GU == 1) out_max[u * NT] = gm;
             group = max2(group, gm);
           }
           run_chunk<ENT>(sum, f, gm, c);
         }
-        if constexpr (TOP) {
-          if constexpr (GU > 1) w.gmax[it * NT + threadIdx.x] = group;
-          largest = max2(largest, group);
+        if constexpr (TOP != kNoTop) {
+          if constexpr (GU > 1) out_max[0] = group;
+          out_max += GU > 1 ? NT : PASS;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) cur[u] = next[u];
       }
-      if constexpr (TOP) {
-        collect_tile<T, NT, U, GU, SLOTS>(w, body, cut.head, t0, t1, largest);
+      if constexpr (TOP == kTop) {
+        float gv[SLOTS / NT];
+        load_groups<NT, U, GU>(gmax, t1 - t0, gv);   // the thread's own writes
+        collect_tile<T, NT, U, GU, SLOTS>(w, gv, body, cut.head, t0, t1);
         if (t1 < c1) {   // the best so far are the next tile's first candidates
-          order_top<NT>(w, count[0], 0);
-          const int n = count[0] < k ? count[0] : k;
-          for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = w.best[i];
-          for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
-          __syncthreads();
-          if (threadIdx.x == 0) count[0] = n;
-          load(cur, t1, t1 + tile < c1 ? t1 + tile : c1);
+          keep_best<NT>(w);
+          load(cur, t1, t1 + TILE < c1 ? t1 + TILE : c1);
         }
+      } else {
+        break;
       }
-      if constexpr (!TOP) break;
     }
     run_block<NT>(sum, red);
     Soft soft;
@@ -806,60 +828,73 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int split, int
       soft.s = block_sum<NT>(soft.s, red);
       soft.t = block_sum<NT>(soft.t, red);
     }
-    if constexpr (TOP) {
-      if constexpr (NT == 64) __syncthreads();
-      order_top<NT>(w, count[0], 0);
-    }
-    if (split == 1) {
-      finish_row<T, NT, MODE>(a, r, soft, TOP ? w.best : nullptr, mine, z_mine, red);
+    if (split > 1) {
+      if (threadIdx.x == 0) part[r * split + part_i] = soft;
     } else {
-      if (threadIdx.x == 0) part[item] = soft;
-      if constexpr (TOP) {
-        for (int i = threadIdx.x; i < k; i += NT) part_keys[item * k + i] = w.best[i];
+      if constexpr (TOP == kTop) {
+        if constexpr (NT == 64) __syncthreads();
+        order_top<NT>(w, count[0]);
       }
+      finish_row<T, NT, MODE>(a, r, soft, TOP == kTop ? w.best : nullptr, mine, z_mine, red);
     }
   }
 }
 
-// Joins a row's segments (at most 64).
-template <typename T, int MODE>
-__global__ __launch_bounds__(256) void join_kernel(VocabArgs a, int split, const Soft* part,
-                                                   const u64* part_keys) {
+// Joins a row's segments (at most 64) and selects its top entries from the group maxima they
+// left (`row_max` a row).
+template <typename T, int GU, int SLOTS, int MODE, int TOP>
+__global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, const Soft* part,
+                                                      const float* part_max, int64_t row_max) {
   constexpr int NT = 256;
-  __shared__ float red[NT / 64];
+  constexpr int64_t TILE = RowShape<T, NT, GU, SLOTS>::TILE;
+  __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
   __shared__ int count[TopCount<NT>::N];
   const float c = a.inv_t * kLog2e;
-  const int k = (int)a.top, n = k * split;
   TopState<NT> w;
-  w.k = k;
-  w.cand = reinterpret_cast<u64*>(swg_vocab_lds);
-  w.sel = w.cand + n;
-  w.best = w.sel + k + kSlack;
-  w.hist = reinterpret_cast<uint32_t*>(w.best + k);
-  w.gmax = nullptr;
-  w.glist = nullptr;
-  w.count = count;
+  const int k = (int)a.top;
+  if constexpr (TOP == kTop) {
+    w.k = k;
+    w.count = count;
+    top_lds_layout(reinterpret_cast<u64*>(swg_vocab_lds), k, w.cand, w.best, w.hist, w.glist);
+  }
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+    const T* z = static_cast<const T*>(a.z) + r * a.ld;
     const Entry mine = row_entry<MODE>(a, r);
-    const float z_mine =
-        mine.id >= 0 ? to_f32(static_cast<const T*>(a.z)[r * a.ld + mine.id]) : 0.0f;
-    Soft sum{kLowest, 0.0f, 0.0f};
-    if ((int)threadIdx.x < split) sum = part[r * split + threadIdx.x];
-    for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = part_keys[r * n + i];
-    soft_block<NT>(sum, c, red);
-    if (k > 0) {
+    const int lane = threadIdx.x & 63;   // every wave joins the sums by itself
+    Soft soft{kLowest, 0.0f, 0.0f};
+    if (lane < split) soft = part[r * split + lane];
+    float z_mine = 0.0f;
+    if constexpr (TOP == kTop) {
+      constexpr int U = Pass<T>::U;
+      const RowCut cut(z, a.V);
+      const int64_t lone = cut.single(threadIdx.x, a.V, true, true);
+      const float* maxima = part_max + r * row_max;
+      const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
+      // all loads of the row's start together
+      float gv[SLOTS / NT];
+      load_groups<NT, U, GU>(maxima, cut.chunks < TILE ? cut.chunks : TILE, gv);
+      if (mine.id >= 0) z_mine = to_f32(z[mine.id]);
+      __syncthreads();   // LDS of the row before
+      if (threadIdx.x == 0) count[0] = 0;
+      for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
       __syncthreads();
-      // each segment's last key bounds the row's last one from below
-      u64 floor_key = 0;
-#pragma unroll 8
-      for (int i = 0; i < split; ++i) {
-        const u64 key = w.cand[i * k + k - 1];
-        floor_key = key > floor_key ? key : floor_key;
+      if (lone >= 0) w.cand[atomicAdd(&count[0], 1)] = entry_key(z_lone, (uint32_t)lone);
+      for (int64_t t0 = 0; t0 < cut.chunks; t0 += TILE) {
+        const int64_t t1 = t0 + TILE < cut.chunks ? t0 + TILE : cut.chunks;
+        if (t0 > 0) {
+          keep_best<NT>(w);
+          load_groups<NT, U, GU>(maxima + t0 / GU, t1 - t0, gv);
+        }
+        collect_tile<T, NT, U, GU, SLOTS>(w, gv, z + cut.head, cut.head, t0, t1);
       }
-      order_top<NT>(w, n, floor_key);
+      order_top<NT>(w, count[0]);
+    } else {
+      if (mine.id >= 0) z_mine = to_f32(z[mine.id]);
     }
-    finish_row<T, NT, MODE>(a, r, sum, k > 0 ? w.best : nullptr, mine, z_mine, red);
-    __syncthreads();
+    soft_move(soft, wave_max(soft.m), c);
+    soft.s = wave_sum(soft.s);
+    soft.t = wave_sum(soft.t);
+    finish_row<T, NT, MODE>(a, r, soft, TOP == kTop ? w.best : nullptr, mine, z_mine, red);
   }
 }
 
@@ -1019,42 +1054,42 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split) {
 }
 
 // ------------------------------------------------------------------ launches
-static size_t top_lds(int k, int group, int slots) {
-  return sizeof(u64) * (size_t)(top_candidates(k, group) + 2 * k + kSlack) +
-         sizeof(uint32_t) * (size_t)(slots + top_groups(k) + kBins);
-}
-
 template <typename T, int MODE, bool ENT>
 static hipError_t forward_rows(const VocabArgs& a, const VocabPlan& p, void* ws,
                                hipStream_t stream) {
-  Soft* part = static_cast<Soft*>(ws);
-  u64* keys = reinterpret_cast<u64*>(static_cast<char*>(ws) + p.keys_at);
-  const int k = (int)a.top;
-#define SWG_ROWS(NT, GU, SLOTS)                                                              \
-  do {                                                                                       \
-    if (k > 0) {                                                                             \
-      if constexpr (MODE == kLogprobs)                                                       \
-        SWG_LAUNCH((rows_kernel<T, NT, GU, SLOTS, MODE, true, ENT>),                         \
-                   dim3(row_grid(a.R * p.split)), dim3(NT), top_lds(k, GU * 8, SLOTS),       \
-                   stream, a, p.split, p.seg, part, keys);                                   \
-    } else {                                                                                 \
-      SWG_LAUNCH((rows_kernel<T, NT, GU, SLOTS, MODE, false, ENT>),                          \
-                 dim3(row_grid(a.R * p.split)), dim3(NT), 0, stream, a, p.split, p.seg, part, \
-                 keys);                                                                      \
-    }                                                                                        \
-  } while (0)
   constexpr int U = Pass<T>::U;
-  if (p.threads == 64) SWG_ROWS(64, 1, 512);
-  else if (p.threads == 256) SWG_ROWS(256, 1, 4096);
-  else SWG_ROWS(512, U, (16384 / U));
+  Soft* part = static_cast<Soft*>(ws);
+  float* part_max = reinterpret_cast<float*>(static_cast<char*>(ws) + p.max_at);
+  const int k = (int)a.top;
+  const size_t lds = k > 0 ? top_lds_bytes(k) : 0;
+  const dim3 grid(row_grid(a.R), (unsigned)p.split);
+#define SWG_ROWS(NT, GU, SLOTS, TOP)                                                           \
+  SWG_LAUNCH((rows_kernel<T, NT, GU, SLOTS, MODE, TOP, ENT>), grid, dim3(NT),                  \
+             TOP == kTop ? lds : 0, stream, a, p.seg, part, part_max, p.row_max)
+  const bool top = MODE == kLogprobs && k > 0;
+  constexpr int kT = MODE == kLogprobs ? kTop : kNoTop;   // distillation has no top entries
+  constexpr int kL = MODE == kLogprobs ? kTopLater : kNoTop;
+  if (p.split > 1) {
+    if (top) SWG_ROWS(256, U, 4096, kL);
+    else SWG_ROWS(256, U, 4096, kNoTop);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (top)
+      SWG_LAUNCH((join_kernel<T, U, 4096, MODE, kT>), dim3(row_grid(a.R)), dim3(256), lds, stream,
+                 a, p.split, part, part_max, p.row_max);
+    else
+      SWG_LAUNCH((join_kernel<T, U, 4096, MODE, kNoTop>), dim3(row_grid(a.R)), dim3(256), 0,
+                 stream, a, p.split, part, part_max, p.row_max);
+  } else if (p.threads == 64) {
+    if (top) SWG_ROWS(64, 1, 512, kT);
+    else SWG_ROWS(64, 1, 512, kNoTop);
+  } else if (!top) {
+    SWG_ROWS(256, U, 4096, kNoTop);
+  } else if constexpr (MODE == kLogprobs) {
+    if (a.V <= 32768) SWG_ROWS(256, 1, 4096, kT);
+    else SWG_ROWS(256, U, 4096, kT);
+  }
 #undef SWG_ROWS
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.split == 1) return e;
-  const size_t lds = k > 0 ? sizeof(u64) * (size_t)(k * p.split + 2 * k + kSlack) +
-                                 sizeof(uint32_t) * kBins
-                           : 0;
-  SWG_LAUNCH((join_kernel<T, MODE>), dim3(row_grid(a.R)), dim3(256), lds, stream, a, p.split,
-             part, keys);
   return hipGetLastError();
 }
 
@@ -1063,12 +1098,11 @@ static hipError_t gradient_rows(const VocabArgs& a, hipStream_t stream) {
   const size_t lds =
       MODE == kDistill ? sizeof(int) * (size_t)(kGradChunks + 8 + 3 * a.k) : sizeof(int);
   const int split = (int)ceil_div(a.V, (int64_t)kGradChunks * 8);
+  const dim3 grid(row_grid(a.R * split));
   if (a.V <= 2048)
-    SWG_LAUNCH((grad_kernel<T, 64, MODE>), dim3(row_grid(a.R * split)), dim3(64), lds, stream, a,
-               split);
+    SWG_LAUNCH((grad_kernel<T, 64, MODE>), grid, dim3(64), lds, stream, a, split);
   else
-    SWG_LAUNCH((grad_kernel<T, 256, MODE>), dim3(row_grid(a.R * split)), dim3(256), lds, stream,
-               a, split);
+    SWG_LAUNCH((grad_kernel<T, 256, MODE>), grid, dim3(256), lds, stream, a, split);
   return hipGetLastError();
 }
 
