@@ -40,6 +40,12 @@ template <typename T> struct Chunk {
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = u32x4{0, 0, 0, 0};
   }
+  // the compiler no longer knows the contents, so that nothing computed from them stays in
+  // registers for a later use
+  __device__ inline void forget() {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(v[i]));
+  }
   __device__ inline void widen(float* f) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) Vec16<T>::widen(v[i], f + i * Vec16<T>::VEC);

@@ -899,36 +899,94 @@ __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, co
 }
 
 // ------------------------------------------------------------------ gradients
-// A workgroup forms up to kGradChunks chunks of a row.  The columns that hold more than their
-// probability (the target, the teacher's entries) are formed with it in the thread that owns
-// them, so the call may overwrite the logits.  The teacher's entries hang in lists by chunk
-// (`first`, `next`); a thread goes through its chunk's list in the order of the entries, so
-// repeated ids add up in a fixed order.
-constexpr int kGradChunks = 2048;
+// The columns that hold more than their probability take part twice: the target is formed in
+// the thread that owns its chunk; the teacher's entries are formed apart, from logits that were
+// read before anything was written (the call may overwrite them), and stored over what the
+// stream wrote once that has arrived.  An entry's column takes off the shares of all entries
+// with its id, in their order, so repeated ids write equal values.
+struct TeacherLds {
+  int* id;       // k; -1 does not count
+  float* share;  // q
+  float* z;      // the logit at id
+};
+__device__ inline TeacherLds teacher_lds(int64_t k) {
+  TeacherLds t;
+  t.id = reinterpret_cast<int*>(swg_vocab_lds);
+  t.share = reinterpret_cast<float*>(t.id + k);
+  t.z = t.share + k;
+  return t;
+}
+static size_t teacher_lds_bytes(int64_t k) { return (size_t)k * 12; }
 
+// fills it (not yet visible to other threads); `mine` and z_mine are the thread's first entry
+template <typename T, int NT>
+__device__ inline void teacher_fill(const TeacherLds& l, const VocabArgs& a, int64_t r,
+                                    const T* z, const Teacher& t, const Entry& mine,
+                                    float z_mine) {
+  Entry e = mine;
+  float x = z_mine;
+  for (int64_t j = threadIdx.x; j < a.k; j += NT) {
+    if (j >= NT) {
+      e = load_entry(a, r, j);
+      x = e.id >= 0 ? to_f32(z[e.id]) : 0.0f;
+    }
+    const bool counts = e.id >= 0 && t.us != 0.0f;
+    l.id[j] = counts ? (int)e.id : -1;
+    l.share[j] = counts ? expf(e.u - t.um) / t.us : 0.0f;
+    l.z[j] = x;
+  }
+}
+
+// stores the entries with columns in [from, to); prob gives a logit's probability
+template <typename T, int NT, typename F>
+__device__ inline void teacher_store(const TeacherLds& l, const VocabArgs& a, T* dz,
+                                     int64_t from, int64_t to, float scale, F prob) {
+  const int k = (int)a.k;
+  // the stream's stores have arrived before one of them is overwritten
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  for (int j = threadIdx.x; j < k; j += NT) {
+    const int id = l.id[j];
+    if (id < from || id >= to || id < 0) continue;
+    float q = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) q += l.id[i] == id ? l.share[i] : 0.0f;
+    dz[id] = from_f32<T>(scale * (prob(l.z[j]) - q));
+  }
+}
+
+// A workgroup forms one of `split` segments of a row, `seg` chunks each.
 template <typename T, int NT, int MODE>
-__global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split) {
+__global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_t seg) {
   constexpr int U = Pass<T>::U;
   __shared__ float red[NT / 64];
-  // lists, one per chunk and one for the single elements
-  int* first = reinterpret_cast<int*>(swg_vocab_lds);
-  int* next = first + kGradChunks + 8;
-  int* column = next + a.k;
-  float* share = reinterpret_cast<float*>(column + a.k);
+  const TeacherLds lds = teacher_lds(MODE == kDistill ? a.k : 0);
   for (int64_t item = blockIdx.x; item < a.R * split; item += gridDim.x) {
     const int64_t r = item / split, part_i = item % split;
     const T* z = static_cast<const T*>(a.z) + r * a.ld;
     T* dz = static_cast<T*>(a.dz) + r * a.lddz;
-    const RowCut cut(z, a.V);
+    const RowCut cut(dz, a.V);
     const T* body = z + cut.head;
     T* out = dz + cut.head;
-    const int64_t c0 = part_i * kGradChunks;
-    const int64_t c1 = c0 + kGradChunks < cut.chunks ? c0 + kGradChunks : cut.chunks;
+    const int64_t c0 = part_i * seg < cut.chunks ? part_i * seg : cut.chunks;
+    const int64_t c1 = c0 + seg < cut.chunks ? c0 + seg : cut.chunks;
     const int64_t lone = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
+    const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
+    Entry mine{-1, neg_inf()};
+    if constexpr (MODE == kDistill) mine = load_entry(a, r, threadIdx.x);
     const float lse_in = a.lse_in[r];
+    auto load = [&](Chunk<T>* ch, int64_t base) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t q = base + u * NT + threadIdx.x;
+        if (q < c1) ch[u].load_stream(body + q * 8);
+      }
+    };
+    Chunk<T> ch[U];
+    load(ch, c0);
     const float lse = lse_in == neg_inf() ? 0.0f : lse_in;   // a row of masked entries: p = 0
 
-    float scale = 0.0f, A = 0.0f, g = 0.0f, h = 0.0f, H = 0.0f, Q = 0.0f;
+    float scale = 0.0f, gain = 0.0f, A = 0.0f, g = 0.0f, h = 0.0f, H = 0.0f;
     int64_t id = -1;
     if constexpr (MODE == kLogprobs) {
       const int64_t t = a.target ? a.target[r] : a.ignore;
@@ -942,7 +1000,7 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split) {
         H = a.entropy_in[r];
       }
       A = __builtin_fmaf(h, H, g);
-      scale = -a.inv_t;
+      gain = -a.inv_t;
     } else {
       const float wgt = a.dloss[r];
       if (wgt == 0.0f) {
@@ -953,74 +1011,35 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split) {
         continue;
       }
       scale = wgt * a.t;
-      __syncthreads();   // the lists' readers of the last item are done
-      for (int i = threadIdx.x; i < kGradChunks + 8; i += NT) first[i] = -1;
-      const Entry mine = load_entry(a, r, threadIdx.x);
-      const Teacher t = teacher_softmax<NT>(a, r, mine, red);
-      Q = t.us == 0.0f ? 0.0f : 1.0f;
-      __syncthreads();
-      Entry e = mine;
-      for (int64_t j = threadIdx.x; j < a.k; j += NT) {
-        if (j >= NT) e = load_entry(a, r, j);
-        if (e.id < 0 || t.us == 0.0f) continue;
-        const int64_t col = e.id - cut.head, ch = col >> 3;
-        int list;
-        if (col < 0 || ch >= cut.chunks) list = kGradChunks;   // single elements
-        else if (ch >= c0 && ch < c1) list = (int)(ch - c0);
-        else continue;
-        column[j] = (int)e.id;
-        share[j] = expf(e.u - t.um) / t.us;
-        next[j] = atomicExch(&first[list], (int)j);
-      }
-      __syncthreads();
+      const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
+      const Teacher t = teacher_softmax<NT>(a, r, mine, red);   // with barriers
+      gain = t.us == 0.0f ? 0.0f : scale;
+      teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine);
+      __syncthreads();   // all entries' logits are read
     }
-    // the teacher's share of column `col` of a list
-    auto teacher_share = [&](int list_first, int col) {
-      float q = 0.0f;
-      for (int last = -1;;) {
-        int best = 0x7fffffff;
-        for (int j = list_first; j >= 0; j = next[j])
-          if (column[j] == col && j > last && j < best) best = j;
-        if (best == 0x7fffffff) return q;
-        q += share[best];
-        last = best;
-      }
-    };
     auto value = [&](float x) {   // log p
       return __builtin_fmaf(x, a.inv_t, -lse);
     };
+    auto prob = [&](float x) { return __builtin_amdgcn_exp2f(value(x) * kLog2e); };
     auto at_target = [&](float x) {
       // g (1 - p) is of the size of g: the division by T in fp64 leaves one rounding to fp32
       // where the product with 1/T would leave three
-      const float lp = value(x), p = __builtin_amdgcn_exp2f(lp * kLog2e);
+      const float lp = value(x), p = prob(x);
       const double ent = p != 0.0f ? (double)(h * p * (lp + H)) : 0.0;
       return (float)(((double)g * (1.0 - (double)p) - ent) / (double)a.t);
     };
     auto plain = [&](float x) {
-      const float lp = value(x), p = __builtin_amdgcn_exp2f(lp * kLog2e);
       if constexpr (MODE == kLogprobs)
-        return p * __builtin_fmaf(h, __builtin_fmaxf(lp, -200.0f), A) * scale;
+        return prob(x) * __builtin_fmaf(h, __builtin_fmaxf(value(x), -200.0f), A) * gain;
       else
-        return scale * (Q * p);
+        return gain * prob(x);
     };
     if (lone >= 0) {
-      const float x = to_f32(z[lone]);
-      float d;
-      if constexpr (MODE == kLogprobs) {
-        d = lone == id && g != 0.0f ? at_target(x) : plain(x);
-      } else {
-        const float p = __builtin_amdgcn_exp2f(value(x) * kLog2e);
-        d = scale * (Q * p - teacher_share(first[kGradChunks], (int)lone));
-      }
+      float d = plain(z_lone);
+      if (MODE == kLogprobs && lone == id && g != 0.0f) d = at_target(z_lone);
       dz[lone] = from_f32<T>(d);
     }
     for (int64_t base = c0; base < c1; base += NT * U) {
-      Chunk<T> ch[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t q = base + u * NT + threadIdx.x;
-        if (q < c1) ch[u].load_stream(body + q * 8);
-      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t q = base + u * NT + threadIdx.x;
@@ -1029,27 +1048,131 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split) {
         ch[u].widen(f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[i] = plain(f[i]);
-        const int64_t col = cut.head + q * 8;
         if constexpr (MODE == kLogprobs) {
+          const int64_t col = cut.head + q * 8;
           if (id >= col && id < col + 8 && g != 0.0f) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (id == col + i) d[i] = at_target(f[i]);
           }
-        } else {
-          const int list = first[q - c0];
-          if (list >= 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float p = __builtin_amdgcn_exp2f(value(f[i]) * kLog2e);
-              d[i] = scale * (Q * p - teacher_share(list, (int)(col + i)));
-            }
-          }
         }
-        ch[u].narrow(d);
-        ch[u].store_stream(out + q * 8);
+        Chunk<T> o;
+        o.narrow(d);
+        o.store_stream(out + q * 8);
       }
+      load(ch, base + NT * U);
     }
+    if constexpr (MODE == kDistill) {
+      const int64_t from = part_i == 0 ? 0 : cut.head + c0 * 8;
+      const int64_t to = part_i == split - 1 ? a.V : cut.head + c1 * 8;
+      teacher_store<T, NT>(lds, a, dz, from, to, scale, prob);
+      __syncthreads();   // LDS of the next item
+    }
+  }
+}
+
+// ------------------------------------------------------------------ distillation in one pass
+// Loss, lse and gradient of a row that a workgroup holds in registers, D chunks a thread: the
+// logits are read once.
+template <typename T, int NT, int D, int WAVES>
+__global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
+  __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
+  const TeacherLds lds = teacher_lds(a.k);
+  const float c = a.inv_t * kLog2e;
+  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+    const T* z = static_cast<const T*>(a.z) + r * a.ld;
+    T* dz = static_cast<T*>(a.dz) + r * a.lddz;
+    const RowCut cut(dz, a.V);
+    const T* body = z + cut.head;
+    T* out = dz + cut.head;
+    const int64_t lone = cut.single(threadIdx.x, a.V, true, true);
+    const Entry mine = load_entry(a, r, threadIdx.x);
+    const float wgt = a.dloss[r];
+    const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
+    // a row-wide address and the thread's offset: chunks differ in scalar registers only
+    auto lane_at = [&](auto* p) {
+      return reinterpret_cast<decltype(p)>((uintptr_t)p + threadIdx.x * (uint32_t)(8 * sizeof(T)));
+    };
+    Chunk<T> ch[D];
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      fill_masked(ch[u]);
+      if (u * NT + (int)threadIdx.x < cut.chunks) ch[u].load_stream(lane_at(body + u * NT * 8));
+    }
+    const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
+    const Teacher t = teacher_softmax<NT>(a, r, mine, red);
+    teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine);
+    __syncthreads();
+
+    Run sum{kNoRef, neg_inf(), 0.0f, 0.0f};
+    if (lone >= 0) run_single(sum, z_lone, c);
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      float f[8];
+      ch[u].widen(f);
+      run_chunk<false>(sum, f, max8(f), c);
+      // one chunk after the other, and widened again where it is used again: the fp32 values of
+      // many chunks do not fit the registers
+      ch[u].forget();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    run_block<NT>(sum, red);   // all of the row is read
+    Soft soft;
+    if (run_in_range(sum.m, c)) {
+      soft = run_soft(sum, c);
+    } else {
+      soft = Soft{sum.m, 0.0f, 0.0f};
+      if (lone >= 0) soft_add<false>(soft, z_lone, c);
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        float f[8];
+        ch[u].widen(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) soft_add<false>(soft, f[i], c);
+        ch[u].forget();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __syncthreads();
+      soft.s = block_sum<NT>(soft.s, red);
+    }
+    const RowStat st = row_stat(soft, a.inv_t);
+    float kl = 0.0f;
+    for (int j = threadIdx.x; j < (int)a.k; j += NT)
+      if (lds.id[j] >= 0)
+        kl += kl_term(t, st, j < NT ? mine.u : load_entry(a, r, j).u, lds.z[j], a.inv_t);
+    if constexpr (NT > 64) __syncthreads();
+    kl = block_sum<NT>(kl, red);
+    if (threadIdx.x == 0) {
+      a.loss[r] = a.t * a.t * kl;
+      a.lse[r] = st.lse;
+    }
+    if (wgt == 0.0f) {
+      Chunk<T> zero;
+      zero.zero();
+      for (int64_t q = threadIdx.x; q < cut.chunks; q += NT) zero.store_stream(out + q * 8);
+      if (lone >= 0) dz[lone] = from_f32<T>(0.0f);
+    } else {
+      const float scale = wgt * a.t;
+      const float over = st.empty ? 0.0f : 1.0f / soft.s;   // p = over 2^((z - m) c)
+      const float gain = t.us == 0.0f ? 0.0f : scale * over;
+      auto power = [&](float x) { return __builtin_amdgcn_exp2f((x - soft.m) * c); };
+      if (lone >= 0) dz[lone] = from_f32<T>(gain * power(z_lone));
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        if (u * NT + (int)threadIdx.x < cut.chunks) {
+          float f[8];
+          ch[u].widen(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = gain * power(f[i]);
+          Chunk<T> o;
+          o.narrow(f);
+          o.store_stream(lane_at(out + u * NT * 8));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      teacher_store<T, NT>(lds, a, dz, 0, a.V, scale, [&](float x) { return over * power(x); });
+    }
+    __syncthreads();   // LDS of the next row
   }
 }
 
@@ -1095,14 +1218,35 @@ static hipError_t forward_rows(const VocabArgs& a, const VocabPlan& p, void* ws,
 
 template <typename T, int MODE>
 static hipError_t gradient_rows(const VocabArgs& a, hipStream_t stream) {
-  const size_t lds =
-      MODE == kDistill ? sizeof(int) * (size_t)(kGradChunks + 8 + 3 * a.k) : sizeof(int);
-  const int split = (int)ceil_div(a.V, (int64_t)kGradChunks * 8);
+  const size_t lds = MODE == kDistill ? teacher_lds_bytes(a.k) : 0;
+  const int split = (int)ceil_div(a.V, 16384);
+  const int64_t seg = ceil_div(ceil_div(a.V, 8), split);
   const dim3 grid(row_grid(a.R * split));
   if (a.V <= 2048)
-    SWG_LAUNCH((grad_kernel<T, 64, MODE>), grid, dim3(64), lds, stream, a, split);
+    SWG_LAUNCH((grad_kernel<T, 64, MODE>), grid, dim3(64), lds, stream, a, split, seg);
   else
-    SWG_LAUNCH((grad_kernel<T, 256, MODE>), grid, dim3(256), lds, stream, a, split);
+    SWG_LAUNCH((grad_kernel<T, 256, MODE>), grid, dim3(256), lds, stream, a, split, seg);
+  return hipGetLastError();
+}
+
+// the one-pass kernel for rows that fit a workgroup's registers, where there are enough of them;
+// otherwise `held` becomes false
+template <typename T>
+static hipError_t distill_rows(const VocabArgs& a, hipStream_t stream, bool& held) {
+  const size_t lds = teacher_lds_bytes(a.k);
+  const int64_t v = a.V * (int64_t)sizeof(T) / 2;   // in units of 16 bits
+  held = true;
+#define SWG_HELD(NT, D, WAVES)                                                               \
+  SWG_LAUNCH((distill_kernel<T, NT, D * 2 / (int)sizeof(T), WAVES>), dim3(row_grid(a.R)),    \
+             dim3(NT), lds, stream, a)
+  if (a.R < 256 || v > 131072) held = false;
+  else if (v <= 2048) SWG_HELD(64, 4, 4);
+  else if (v <= 8192) SWG_HELD(256, 4, 4);
+  else if (v <= 16384) SWG_HELD(256, 8, 4);
+  else if (v <= 32768) SWG_HELD(512, 8, 4);
+  else if (v <= 65536) SWG_HELD(512, 16, 4);
+  else SWG_HELD(512, 32, 2);
+#undef SWG_HELD
   return hipGetLastError();
 }
 
@@ -1130,7 +1274,12 @@ hipError_t launch_distill_bwd(int dtype, const VocabArgs& a, hipStream_t stream)
 }
 hipError_t launch_distill_fwd_bwd(int dtype, const VocabArgs& a, const VocabPlan& p, void* ws,
                                   hipStream_t stream) {
-  const hipError_t e = launch_distill_fwd(dtype, a, p, ws, stream);
+  bool held;
+  hipError_t e = dtype == 0   ? distill_rows<bf16>(a, stream, held)
+                 : dtype == 1 ? distill_rows<fp16>(a, stream, held)
+                              : distill_rows<float>(a, stream, held);
+  if (held || e != hipSuccess) return e;
+  e = launch_distill_fwd(dtype, a, p, ws, stream);
   if (e != hipSuccess) return e;
   VocabArgs b = a;
   b.lse_in = a.lse;
