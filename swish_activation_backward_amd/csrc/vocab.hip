@@ -918,17 +918,18 @@ __device__ inline TeacherLds teacher_lds(int64_t k) {
 }
 static size_t teacher_lds_bytes(int64_t k) { return (size_t)k * 12; }
 
-// fills it (not yet visible to other threads); `mine` and z_mine are the thread's first entry
+// fills it (not yet visible to other threads), with the logits of entries in [from, to); `mine`
+// and z_mine are the thread's first entry
 template <typename T, int NT>
 __device__ inline void teacher_fill(const TeacherLds& l, const VocabArgs& a, int64_t r,
                                     const T* z, const Teacher& t, const Entry& mine,
-                                    float z_mine) {
+                                    float z_mine, int64_t from, int64_t to) {
   Entry e = mine;
   float x = z_mine;
   for (int64_t j = threadIdx.x; j < a.k; j += NT) {
     if (j >= NT) {
       e = load_entry(a, r, j);
-      x = e.id >= 0 ? to_f32(z[e.id]) : 0.0f;
+      x = e.id >= from && e.id < to ? to_f32(z[e.id]) : 0.0f;
     }
     const bool counts = e.id >= 0 && t.us != 0.0f;
     l.id[j] = counts ? (int)e.id : -1;
@@ -960,6 +961,8 @@ template <typename T, int NT, int MODE>
 __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_t seg) {
   constexpr int U = Pass<T>::U;
   __shared__ float red[NT / 64];
+  // a wave's chunks of a pass follow each other
+  const int first = (int)(threadIdx.x >> 6) * (64 * U) + (int)(threadIdx.x & 63);
   const TeacherLds lds = teacher_lds(MODE == kDistill ? a.k : 0);
   for (int64_t item = blockIdx.x; item < a.R * split; item += gridDim.x) {
     const int64_t r = item / split, part_i = item % split;
@@ -975,15 +978,22 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
     Entry mine{-1, neg_inf()};
     if constexpr (MODE == kDistill) mine = load_entry(a, r, threadIdx.x);
     const float lse_in = a.lse_in[r];
+    // the segment's columns
+    const int64_t from = part_i == 0 ? 0 : cut.head + c0 * 8;
+    const int64_t to = part_i == split - 1 ? a.V : cut.head + c1 * 8;
     auto load = [&](Chunk<T>* ch, int64_t base) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t q = base + u * NT + threadIdx.x;
-        if (q < c1) ch[u].load_stream(body + q * 8);
+        const int64_t q = base + first + u * 64;
+        if (q >= c0 && q < c1) ch[u].load_stream(body + q * 8);
       }
     };
-    Chunk<T> ch[U];
-    load(ch, c0);
+    // passes start at a 128-byte line of the output: waves that share one cost 7 % at rows of
+    // 50024 bf16
+    const int64_t start =
+        c0 - (int64_t)((reinterpret_cast<uintptr_t>(out + c0 * 8) & 127) / (8 * sizeof(T)));
+    Chunk<T> ch[U], next[U];
+    load(ch, start);
     const float lse = lse_in == neg_inf() ? 0.0f : lse_in;   // a row of masked entries: p = 0
 
     float scale = 0.0f, gain = 0.0f, A = 0.0f, g = 0.0f, h = 0.0f, H = 0.0f;
@@ -1011,10 +1021,11 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
         continue;
       }
       scale = wgt * a.t;
-      const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
+      const bool here = mine.id >= from && mine.id < to;
+      const float z_mine = here ? to_f32(z[mine.id]) : 0.0f;
       const Teacher t = teacher_softmax<NT>(a, r, mine, red);   // with barriers
       gain = t.us == 0.0f ? 0.0f : scale;
-      teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine);
+      teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine, from, to);
       __syncthreads();   // all entries' logits are read
     }
     auto value = [&](float x) {   // log p
@@ -1039,11 +1050,12 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
       if (MODE == kLogprobs && lone == id && g != 0.0f) d = at_target(z_lone);
       dz[lone] = from_f32<T>(d);
     }
-    for (int64_t base = c0; base < c1; base += NT * U) {
+    for (int64_t base = start; base < c1; base += NT * U) {
+      load(next, base + NT * U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t q = base + u * NT + threadIdx.x;
-        if (q >= c1) continue;
+        const int64_t q = base + first + u * 64;
+        if (q < c0 || q >= c1) continue;
         float f[8], d[8];
         ch[u].widen(f);
 #pragma unroll
@@ -1060,11 +1072,10 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
         o.narrow(d);
         o.store_stream(out + q * 8);
       }
-      load(ch, base + NT * U);
+#pragma unroll
+      for (int u = 0; u < U; ++u) ch[u] = next[u];
     }
     if constexpr (MODE == kDistill) {
-      const int64_t from = part_i == 0 ? 0 : cut.head + c0 * 8;
-      const int64_t to = part_i == split - 1 ? a.V : cut.head + c1 * 8;
       teacher_store<T, NT>(lds, a, dz, from, to, scale, prob);
       __syncthreads();   // LDS of the next item
     }
@@ -1101,7 +1112,7 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
     }
     const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
     const Teacher t = teacher_softmax<NT>(a, r, mine, red);
-    teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine);
+    teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine, 0, a.V);
     __syncthreads();
 
     Run sum{kNoRef, neg_inf(), 0.0f, 0.0f};
@@ -1219,13 +1230,18 @@ static hipError_t forward_rows(const VocabArgs& a, const VocabPlan& p, void* ws,
 template <typename T, int MODE>
 static hipError_t gradient_rows(const VocabArgs& a, hipStream_t stream) {
   const size_t lds = MODE == kDistill ? teacher_lds_bytes(a.k) : 0;
-  const int split = (int)ceil_div(a.V, 16384);
-  const int64_t seg = ceil_div(ceil_div(a.V, 8), split);
+  // Segments of about 16384 elements, 32768 where each prepares the teacher's entries, down to
+  // 8192 where rows are few.  [2048, 65536] bf16 log probabilities take 90 us with 16384 and 95
+  // with 32768 (fewer workgroups to even out), [2047, 50021] with 32 teacher entries 92 and 88.
+  int64_t split = ceil_div(a.V, MODE == kDistill ? 32768 : 16384);
+  const int64_t want = ceil_div(2048, a.R), most = ceil_div(a.V, 8192);
+  if (split < want) split = want < most ? want : most;
+  const int64_t seg = ceil_div(ceil_div(a.V, 8), split * 64) * 64;   // whole lines
   const dim3 grid(row_grid(a.R * split));
   if (a.V <= 2048)
-    SWG_LAUNCH((grad_kernel<T, 64, MODE>), grid, dim3(64), lds, stream, a, split, seg);
+    SWG_LAUNCH((grad_kernel<T, 64, MODE>), grid, dim3(64), lds, stream, a, (int)split, seg);
   else
-    SWG_LAUNCH((grad_kernel<T, 256, MODE>), grid, dim3(256), lds, stream, a, split, seg);
+    SWG_LAUNCH((grad_kernel<T, 256, MODE>), grid, dim3(256), lds, stream, a, (int)split, seg);
   return hipGetLastError();
 }
 
