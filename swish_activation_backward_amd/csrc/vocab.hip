@@ -159,6 +159,15 @@ template <int NT> __device__ inline void run_block(Run& a, float* red) {
     f32x4* r = reinterpret_cast<f32x4*>(red);
     if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = f32x4{a.b, a.m, a.s, a.t};
     __syncthreads();
+    if constexpr (NT > 256) {   // a lane takes a wave's
+      const int lane = threadIdx.x & 15;
+      const f32x4 v = lane < NT / 64 ? r[lane] : f32x4{kNoRef, neg_inf(), 0.0f, 0.0f};
+      a = Run{v[0], lanes_max<16>(v[1]), v[2], v[3]};
+      run_move(a, lanes_max<16>(a.b));
+      a.s = lanes_sum<16>(a.s);
+      a.t = lanes_sum<16>(a.t);
+      return;
+    }
     float b = kNoRef;
 #pragma unroll
     for (int i = 0; i < NT / 64; ++i) {
@@ -1082,6 +1091,10 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
   }
 }
 
+__device__ inline float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
 // ------------------------------------------------------------------ distillation in one pass
 // Loss, lse and gradient of a row that a workgroup holds in registers, D chunks a thread: the
 // logits are read once.
@@ -1100,18 +1113,22 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
     const Entry mine = load_entry(a, r, threadIdx.x);
     const float wgt = a.dloss[r];
     const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
-    // a row-wide address and the thread's offset: chunks differ in scalar registers only
-    auto lane_at = [&](auto* p) {
-      return reinterpret_cast<decltype(p)>((uintptr_t)p + threadIdx.x * (uint32_t)(8 * sizeof(T)));
-    };
+    // Chunk u of the thread, if the row has it.  A row-wide address or number and the thread's
+    // 32-bit offset: chunks differ in scalar registers only.
+    const int chunks = (int)cut.chunks;
+    auto has = [&](int u) { return (int)threadIdx.x < chunks - u * NT; };
+    const uint32_t lane_bytes = threadIdx.x * (uint32_t)(8 * sizeof(T));
     Chunk<T> ch[D];
 #pragma unroll
     for (int u = 0; u < D; ++u) {
       fill_masked(ch[u]);
-      if (u * NT + (int)threadIdx.x < cut.chunks) ch[u].load_stream(lane_at(body + u * NT * 8));
+      if (has(u))
+        ch[u].load_stream(reinterpret_cast<const T*>(
+            reinterpret_cast<const char*>(body + u * NT * 8) + lane_bytes));
     }
     const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
-    const Teacher t = teacher_softmax<NT>(a, r, mine, red);
+    Teacher t = teacher_softmax<NT>(a, r, mine, red);
+    t = Teacher{uniform(t.um), uniform(t.us), uniform(t.lus)};
     teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine, 0, a.V);
     __syncthreads();
 
@@ -1146,6 +1163,9 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
       __syncthreads();
       soft.s = block_sum<NT>(soft.s, red);
     }
+    // the same in every lane: scalar registers
+    soft.m = uniform(soft.m);
+    soft.s = uniform(soft.s);
     const RowStat st = row_stat(soft, a.inv_t);
     float kl = 0.0f;
     for (int j = threadIdx.x; j < (int)a.k; j += NT)
@@ -1160,24 +1180,25 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
     if (wgt == 0.0f) {
       Chunk<T> zero;
       zero.zero();
-      for (int64_t q = threadIdx.x; q < cut.chunks; q += NT) zero.store_stream(out + q * 8);
+      for (int q = threadIdx.x; q < chunks; q += NT) zero.store_stream(out + (int64_t)q * 8);
       if (lone >= 0) dz[lone] = from_f32<T>(0.0f);
     } else {
-      const float scale = wgt * a.t;
-      const float over = st.empty ? 0.0f : 1.0f / soft.s;   // p = over 2^((z - m) c)
-      const float gain = t.us == 0.0f ? 0.0f : scale * over;
+      const float scale = uniform(wgt * a.t);
+      const float over = uniform(st.empty ? 0.0f : 1.0f / soft.s);   // p = over 2^((z - m) c)
+      const float gain = uniform(t.us == 0.0f ? 0.0f : scale * over);
       auto power = [&](float x) { return __builtin_amdgcn_exp2f((x - soft.m) * c); };
       if (lone >= 0) dz[lone] = from_f32<T>(gain * power(z_lone));
 #pragma unroll
       for (int u = 0; u < D; ++u) {
-        if (u * NT + (int)threadIdx.x < cut.chunks) {
+        if (has(u)) {
           float f[8];
           ch[u].widen(f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = gain * power(f[i]);
           Chunk<T> o;
           o.narrow(f);
-          o.store_stream(lane_at(out + u * NT * 8));
+          o.store_stream(
+              reinterpret_cast<T*>(reinterpret_cast<char*>(out + u * NT * 8) + lane_bytes));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -1261,7 +1282,7 @@ static hipError_t distill_rows(const VocabArgs& a, hipStream_t stream, bool& hel
   else if (v <= 16384) SWG_HELD(256, 8, 4);
   else if (v <= 32768) SWG_HELD(512, 8, 4);
   else if (v <= 65536) SWG_HELD(512, 16, 4);
-  else SWG_HELD(512, 32, 2);
+  else SWG_HELD(1024, 16, 4);
 #undef SWG_HELD
   return hipGetLastError();
 }
