@@ -30,9 +30,9 @@ struct RowCut {
     tail = (int)((V - head) & 7);
   }
   // the element index of the single element thread t takes, or -1
-  __device__ inline int64_t single(int t, int64_t V, bool first, bool last) const {
+  __device__ inline int single(int t, int64_t V, bool first, bool last) const {
     if (t < head) return first ? t : -1;
-    if (t >= 8 && t < 8 + tail) return last ? V - tail + (t - 8) : -1;
+    if (t >= 8 && t < 8 + tail) return last ? (int)V - tail + (t - 8) : -1;
     return -1;
   }
 };
@@ -389,36 +389,30 @@ template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n)
   __syncthreads();
 }
 
-// The thread's group j of a tile exists while its first chunk does.
-template <int NT, int U, int GU> __device__ inline bool group_exists(int j, int chunks) {
-  return j * (NT * (GU == 1 ? 1 : U)) + (int)threadIdx.x < chunks;
-}
-// element j NT + thread of `gmax` is the maximum of the thread's group j
-template <int NT, int U, int GU, int NS>
-__device__ inline void load_groups(const float* gmax, int64_t chunks, float (&gv)[NS]) {
-#pragma unroll
-  for (int j = 0; j < NS; ++j)
-    gv[j] = group_exists<NT, U, GU>(j, (int)chunks) ? gmax[j * NT + threadIdx.x] : neg_inf();
-}
-
 // the candidates of one tile: chunks [t0, t1) of `body`, whose first element is entry `first`
-// of the row; groups of GU chunks, NT apart.  gv[j] is the maximum of the thread's group j, -inf
-// for none; the histogram is clear.
+// of the row; groups of GU chunks, NT apart.  Element j NT + thread of `gmax` (LDS) is the maximum
+// of the thread's group j, written by itself; the histogram is clear.  Group j exists while its
+// first chunk does.
 template <typename T, int NT, int U, int GU, int SLOTS>
-__device__ inline void collect_tile(const TopState<NT>& w, const float (&gv)[SLOTS / NT],
-                                    const T* body, int64_t first, int64_t t0, int64_t t1) {
+__device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, const T* body,
+                                    int64_t first, int64_t t0, int64_t t1) {
   constexpr int NS = SLOTS / NT;
   const int k = w.k, most = top_groups(k);
   const int chunks = (int)(t1 - t0);
-  auto exists = [&](int j) { return group_exists<NT, U, GU>(j, chunks); };
+  auto exists = [&](int j) {
+    return j * (NT * (GU == 1 ? 1 : U)) + (int)threadIdx.x < chunks;
+  };
+  // read from LDS where it is used: 16 of them in registers take a wave a SIMD
+  auto gv = [&](int j) { return exists(j) ? gmax[j * NT + threadIdx.x] : neg_inf(); };
   const int groups = GU == 1 ? chunks
                              : chunks / (NT * U) * NT +
                                    (chunks % (NT * U) < NT ? chunks % (NT * U) : NT);
   float least = __builtin_inff(), largest = neg_inf();
-#pragma unroll
+#pragma unroll 4
   for (int j = 0; j < NS; ++j) {
-    largest = max2(largest, gv[j]);
-    if (exists(j)) least = __builtin_fminf(least, gv[j]);
+    const float v = gv(j);
+    largest = max2(largest, v);
+    if (exists(j)) least = __builtin_fminf(least, v);
   }
   // between the smallest of the threads' largest maxima (of all where k is above NT) and the
   // largest lie at least k; threads with nothing but masked entries do not count
@@ -434,9 +428,9 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float (&gv)[SLO
   if (groups > most) {
     int reach = 0;
     if (bins.usable(lo)) {
-#pragma unroll
+#pragma unroll 4
       for (int j = 0; j < NS; ++j)
-        if (exists(j) && gv[j] >= lo) bins.add(w.hist, gv[j]);
+        if (exists(j) && gv(j) >= lo) bins.add(w.hist, gv(j));
       __syncthreads();
       reach = hist_bound(w.hist, k, limit);
     }
@@ -444,8 +438,8 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float (&gv)[SLO
     if (!by_value) {
       reach = bisect<NT, uint32_t>([&](uint32_t x) {
         int c = 0;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) c += __popcll(__ballot(exists(j) && value_key(gv[j]) >= x));
+#pragma unroll 4
+        for (int j = 0; j < NS; ++j) c += __popcll(__ballot(exists(j) && value_key(gv(j)) >= x));
         return c;
       }, groups, k, most, value_key(hi) + 1, w.count, bound);
       ties = reach > most;   // too many groups at the bound itself
@@ -456,8 +450,8 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float (&gv)[SLO
     return by_value ? v >= lo && bins.at(v) < limit : value_key(v) >= from;
   };
   uint32_t mine = 0;
-#pragma unroll
-  for (int j = 0; j < NS; ++j) mine |= (uint32_t)(exists(j) && passes(gv[j])) << j;
+#pragma unroll 4
+  for (int j = 0; j < NS; ++j) mine |= (uint32_t)(exists(j) && passes(gv(j))) << j;
   if (mine) {
     int at = atomicAdd(&w.count[1], __popc(mine));
     do {
@@ -686,6 +680,16 @@ extern __shared__ __attribute__((aligned(16))) char swg_vocab_lds[];
 // is worked on.
 template <typename T> struct Pass { static constexpr int U = sizeof(T) == 2 ? 4 : 2; };
 
+// The thread's chunk of those that start at p, an address that all threads share: it stays in
+// scalar registers and the thread adds 32 bits.
+template <typename T> __device__ inline const T* lane_at(const T* p) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) +
+                                    threadIdx.x * (uint32_t)(8 * sizeof(T)));
+}
+template <typename T> __device__ inline T* lane_at(T* p) {
+  return const_cast<T*>(lane_at<T>(static_cast<const T*>(p)));
+}
+
 // What a workgroup does about the top entries: nothing, their selection, or, where it has a
 // segment of the row only, leaving the group maxima to join_kernel.
 enum { kNoTop = 0, kTop = 1, kTopLater = 2 };
@@ -738,22 +742,23 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, S
     const RowCut cut(z, a.V);
     const T* body = z + cut.head;
     const int64_t c0 = part_i * seg, c1 = c0 + seg < cut.chunks ? c0 + seg : cut.chunks;
-    const int64_t lone = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
+    const int lone = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
     Entry mine{-1, neg_inf()};
     if (split == 1) mine = row_entry<MODE>(a, r);
     float z_lone = lone >= 0 ? to_f32(z[lone]) : neg_inf();
     // one pass: U chunks of the thread, from `base` on, before t1
     auto load = [&](Chunk<T>* ch, int64_t base, int64_t t1) {
-      if (base + PASS <= t1) {
+      const T* p = body + base * 8;
+      const int64_t left = t1 - base;
+      if (left >= PASS) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          ch[u].load_stream(body + (base + u * NT + threadIdx.x) * 8);
+        for (int u = 0; u < U; ++u) ch[u].load_stream(lane_at<T>(p + u * NT * 8));
       } else {
+        const int n = (int)left;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int64_t q = base + u * NT + threadIdx.x;
           fill_masked(ch[u]);
-          if (q < t1) ch[u].load_stream(body + q * 8);
+          if ((int)threadIdx.x < n - u * NT) ch[u].load_stream(lane_at<T>(p + u * NT * 8));
         }
       }
     };
@@ -807,9 +812,7 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, S
         for (int u = 0; u < U; ++u) cur[u] = next[u];
       }
       if constexpr (TOP == kTop) {
-        float gv[SLOTS / NT];
-        load_groups<NT, U, GU>(gmax, t1 - t0, gv);   // the thread's own writes
-        collect_tile<T, NT, U, GU, SLOTS>(w, gv, body, cut.head, t0, t1);
+        collect_tile<T, NT, U, GU, SLOTS>(w, gmax, body, cut.head, t0, t1);
         if (t1 < c1) {   // the best so far are the next tile's first candidates
           keep_best<NT>(w);
           load(cur, t1, t1 + TILE < c1 ? t1 + TILE : c1);
@@ -858,6 +861,7 @@ __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, co
   constexpr int64_t TILE = RowShape<T, NT, GU, SLOTS>::TILE;
   __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
   __shared__ int count[TopCount<NT>::N];
+  __shared__ float gmax[TOP == kTop ? SLOTS : 1];
   const float c = a.inv_t * kLog2e;
   TopState<NT> w;
   const int k = (int)a.top;
@@ -876,12 +880,18 @@ __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, co
     if constexpr (TOP == kTop) {
       constexpr int U = Pass<T>::U;
       const RowCut cut(z, a.V);
-      const int64_t lone = cut.single(threadIdx.x, a.V, true, true);
+      const int lone = cut.single(threadIdx.x, a.V, true, true);
       const float* maxima = part_max + r * row_max;
       const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
-      // all loads of the row's start together
-      float gv[SLOTS / NT];
-      load_groups<NT, U, GU>(maxima, cut.chunks < TILE ? cut.chunks : TILE, gv);
+      // the thread's own groups; past the row's end the workspace holds them up to row_max only
+      auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int j = 0; j < SLOTS / NT; ++j) {
+          const int64_t i = t0 / GU + j * NT + threadIdx.x;
+          if (i < row_max) gmax[j * NT + threadIdx.x] = maxima[i];
+        }
+      };
+      fetch(0);
       if (mine.id >= 0) z_mine = to_f32(z[mine.id]);
       __syncthreads();   // LDS of the row before
       if (threadIdx.x == 0) count[0] = 0;
@@ -892,9 +902,9 @@ __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, co
         const int64_t t1 = t0 + TILE < cut.chunks ? t0 + TILE : cut.chunks;
         if (t0 > 0) {
           keep_best<NT>(w);
-          load_groups<NT, U, GU>(maxima + t0 / GU, t1 - t0, gv);
+          fetch(t0);
         }
-        collect_tile<T, NT, U, GU, SLOTS>(w, gv, z + cut.head, cut.head, t0, t1);
+        collect_tile<T, NT, U, GU, SLOTS>(w, gmax, z + cut.head, cut.head, t0, t1);
       }
       order_top<NT>(w, count[0]);
     } else {
@@ -982,7 +992,7 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
     T* out = dz + cut.head;
     const int64_t c0 = part_i * seg < cut.chunks ? part_i * seg : cut.chunks;
     const int64_t c1 = c0 + seg < cut.chunks ? c0 + seg : cut.chunks;
-    const int64_t lone = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
+    const int lone = cut.single(threadIdx.x, a.V, part_i == 0, part_i == split - 1);
     const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
     Entry mine{-1, neg_inf()};
     if constexpr (MODE == kDistill) mine = load_entry(a, r, threadIdx.x);
@@ -1109,22 +1119,19 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
     const RowCut cut(dz, a.V);
     const T* body = z + cut.head;
     T* out = dz + cut.head;
-    const int64_t lone = cut.single(threadIdx.x, a.V, true, true);
+    const int lone = cut.single(threadIdx.x, a.V, true, true);
     const Entry mine = load_entry(a, r, threadIdx.x);
     const float wgt = a.dloss[r];
     const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
-    // Chunk u of the thread, if the row has it.  A row-wide address or number and the thread's
-    // 32-bit offset: chunks differ in scalar registers only.
+    // chunk u of the thread, if the row has it
     const int chunks = (int)cut.chunks;
     auto has = [&](int u) { return (int)threadIdx.x < chunks - u * NT; };
-    const uint32_t lane_bytes = threadIdx.x * (uint32_t)(8 * sizeof(T));
     Chunk<T> ch[D];
 #pragma unroll
     for (int u = 0; u < D; ++u) {
       fill_masked(ch[u]);
       if (has(u))
-        ch[u].load_stream(reinterpret_cast<const T*>(
-            reinterpret_cast<const char*>(body + u * NT * 8) + lane_bytes));
+        ch[u].load_stream(lane_at<T>(body + u * NT * 8));
     }
     const float z_mine = mine.id >= 0 ? to_f32(z[mine.id]) : 0.0f;
     Teacher t = teacher_softmax<NT>(a, r, mine, red);
@@ -1197,8 +1204,7 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
           for (int i = 0; i < 8; ++i) f[i] = gain * power(f[i]);
           Chunk<T> o;
           o.narrow(f);
-          o.store_stream(
-              reinterpret_cast<T*>(reinterpret_cast<char*>(out + u * NT * 8) + lane_bytes));
+          o.store_stream(lane_at<T>(out + u * NT * 8));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
