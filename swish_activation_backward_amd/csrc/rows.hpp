@@ -130,7 +130,7 @@ typedef unsigned long long u64;
 __device__ inline uint32_t value_key(float v) {
   v = v == v ? v + 0.0f : neg_inf();
   const uint32_t b = __float_as_uint(v);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ inline float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);

@@ -240,7 +240,8 @@ template <int NT> struct TopState {
   int* count;        // TopCount<NT>::N
   int k;
 };
-// [0] candidates, [1] groups or chosen keys, then the waves' counts and bounds, twice
+// [0] candidates, [1] chosen groups, [2] the least key of their maxima, then the waves' counts
+// and bounds, twice
 template <int NT> struct TopCount { static constexpr int N = 4 + 4 * (NT / 64); };
 
 // the sum of the waves' counts; successive calls alternate `half`
@@ -418,19 +419,24 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
   // largest lie at least k; threads with nothing but masked entries do not count
   float hi = largest, lo = k <= NT ? largest : least;
   if (lo == neg_inf()) lo = __builtin_inff();
-  if (threadIdx.x == 0) w.count[1] = 0;
+  if (threadIdx.x == 0) {
+    w.count[1] = 0;
+    w.count[2] = -1;
+  }
   block_bounds<NT>(lo, hi, w.count);
   const int before = w.count[0];
   const Bins bins(lo, hi);
-  uint32_t from = 0, bound = 0;   // least keys of the candidates and of the groups
+  uint32_t bound = 0;   // least key of the groups
   float limit = __builtin_inff();
   bool by_value = false, ties = false;
   if (groups > most) {
     int reach = 0;
     if (bins.usable(lo)) {
 #pragma unroll 4
-      for (int j = 0; j < NS; ++j)
-        if (exists(j) && gv(j) >= lo) bins.add(w.hist, gv(j));
+      for (int j = 0; j < NS; ++j) {
+        const float v = gv(j);
+        if (exists(j) && v >= lo) bins.add(w.hist, v);
+      }
       __syncthreads();
       reach = hist_bound(w.hist, k, limit);
     }
@@ -438,76 +444,78 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
     if (!by_value) {
       reach = bisect<NT, uint32_t>([&](uint32_t x) {
         int c = 0;
-#pragma unroll 4
+#pragma unroll 1
         for (int j = 0; j < NS; ++j) c += __popcll(__ballot(exists(j) && value_key(gv(j)) >= x));
         return c;
       }, groups, k, most, value_key(hi) + 1, w.count, bound);
       ties = reach > most;   // too many groups at the bound itself
-      from = bound + ties;
+      bound = bound == 0 ? value_key(neg_inf()) : bound;
     }
   }
-  auto passes = [&](float v) {
-    return by_value ? v >= lo && bins.at(v) < limit : value_key(v) >= from;
-  };
-  uint32_t mine = 0;
-#pragma unroll 4
-  for (int j = 0; j < NS; ++j) mine |= (uint32_t)(exists(j) && passes(gv(j))) << j;
-  if (mine) {
-    int at = atomicAdd(&w.count[1], __popc(mine));
-    do {
-      w.glist[at++] = (uint32_t)((__builtin_ctz(mine)) * NT + threadIdx.x);
-      mine &= mine - 1;
-    } while (mine);
+#pragma unroll 2
+  for (int j = 0; j < NS; ++j) {
+    const float v = gv(j);
+    if (!exists(j)) break;
+    if (by_value ? v >= lo && bins.at(v) < limit : value_key(v) >= bound + ties) {
+      w.glist[atomicAdd(&w.count[1], 1)] = (uint32_t)(j * NT + threadIdx.x);
+      if (by_value) atomicMin(reinterpret_cast<uint32_t*>(&w.count[2]), value_key(v));
+    }
   }
   __syncthreads();
+  // an entry is a candidate from the bound on, with ties from the next value on; a NaN ranks with
+  // -inf: it passes, or with ties comes in the scan
+  const float cut = key_value(by_value ? (uint32_t)w.count[2]
+                                       : groups > most ? bound : value_key(neg_inf()));
+  const float next = ties ? key_value(value_key(cut) + 1) : cut;
+  auto passes = [&](float v) { return !(v < next); };
   const int chosen = w.count[1];
   auto each_chunk = [&](auto use) {   // of the chosen groups
     for (int i = threadIdx.x; i < chosen * GU; i += NT) {
       const int g = (int)w.glist[i / GU], u = i % GU;
-      const int64_t q = GU == 1 ? t0 + g : t0 + (int64_t)(g / NT) * (NT * U) + u * NT + g % NT;
-      if (q >= t1) continue;
+      const int q = GU == 1 ? g : (g / NT) * (NT * U) + u * NT + g % NT;
+      if (q >= chunks) continue;
       Chunk<T> c;
-      c.load(body + q * 8);
+      c.load(body + (t0 + q) * 8);
       float f[8];
       c.widen(f);
-      use(f, (uint32_t)(first + q * 8));
+      use(f, (uint32_t)(first + (t0 + q) * 8));
     }
   };
   const int room = before + k + kSlack;
-  each_chunk([&](const float* f, uint32_t id) {
-    uint32_t hits = 0;
+  u64 lowest = 0;
+  for (;;) {
+    each_chunk([&](const float* f, uint32_t id) {
+      uint32_t hits = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) hits |= (uint32_t)passes(f[e]) << e;
-    if (hits == 0) return;
-    int at = atomicAdd(&w.count[0], __popc(hits));
+      for (int e = 0; e < 8; ++e) hits |= (uint32_t)passes(f[e]) << e;
+      if (ties || lowest != 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (hits >> e & 1) {
-        if (at < room) w.cand[at] = entry_key(f[e], id + e);
-        ++at;
+        for (int e = 0; e < 8; ++e)
+          if ((ties && f[e] != f[e]) || entry_key(f[e], id + e) < lowest) hits &= ~(1u << e);
       }
-    }
-  });
-  __syncthreads();
-  if (w.count[0] > room) {
-    u64 lowest;
+      if (hits == 0) return;
+      int at = atomicAdd(&w.count[0], __popc(hits));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (hits >> e & 1) {
+          if (at < room) w.cand[at] = entry_key(f[e], id + e);
+          ++at;
+        }
+      }
+    });
+    __syncthreads();
+    const int have = w.count[0];
+    if (have <= room) break;
     bisect<NT, u64>([&](u64 x) {
       int c = 0;
       each_chunk([&](const float* f, uint32_t id) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c += passes(f[e]) && entry_key(f[e], id + e) >= x;
+        for (int e = 0; e < 8; ++e)
+          c += passes(f[e]) && !(ties && f[e] != f[e]) && entry_key(f[e], id + e) >= x;
       });
       return (int)lanes_sum<64>((float)c);
-    }, w.count[0] - before, k, k + kSlack, ~0ull, w.count, lowest);
+    }, have - before, k, k + kSlack, ~0ull, w.count, lowest);
     if (threadIdx.x == 0) w.count[0] = before;
-    __syncthreads();
-    each_chunk([&](const float* f, uint32_t id) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const u64 key = entry_key(f[e], id + e);
-        if (passes(f[e]) && key >= lowest) w.cand[atomicAdd(&w.count[0], 1)] = key;
-      }
-    });
     __syncthreads();
   }
   if (!ties) return;
@@ -554,14 +562,13 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
   __syncthreads();
 }
 
-// the best k candidates become the only ones, and the histogram is clear
+// the n = min(k, candidates) best become the only candidates, and the histogram is clear
 template <int NT> __device__ inline void keep_best(const TopState<NT>& w) {
   const int n = w.count[0] < w.k ? w.count[0] : w.k;
-  order_top<NT>(w, w.count[0]);
   for (int i = threadIdx.x; i < n; i += NT) w.cand[i] = w.best[i];
   for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
-  if (threadIdx.x == 0) w.count[0] = n;
   __syncthreads();
+  if (threadIdx.x == 0) w.count[0] = n;
 }
 
 // ------------------------------------------------------------------ the teacher's entries
@@ -813,6 +820,7 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, S
       }
       if constexpr (TOP == kTop) {
         collect_tile<T, NT, U, GU, SLOTS>(w, gmax, body, cut.head, t0, t1);
+        order_top<NT>(w, count[0]);
         if (t1 < c1) {   // the best so far are the next tile's first candidates
           keep_best<NT>(w);
           load(cur, t1, t1 + TILE < c1 ? t1 + TILE : c1);
@@ -844,8 +852,10 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, S
       if (threadIdx.x == 0) part[r * split + part_i] = soft;
     } else {
       if constexpr (TOP == kTop) {
-        if constexpr (NT == 64) __syncthreads();
-        order_top<NT>(w, count[0]);
+        if (c1 == 0) {   // a row of single elements
+          __syncthreads();
+          order_top<NT>(w, count[0]);
+        }
       }
       finish_row<T, NT, MODE>(a, r, soft, TOP == kTop ? w.best : nullptr, mine, z_mine, red);
     }
@@ -885,11 +895,10 @@ __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, co
       const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
       // the thread's own groups; past the row's end the workspace holds them up to row_max only
       auto fetch = [&](int64_t t0) {
-#pragma unroll
-        for (int j = 0; j < SLOTS / NT; ++j) {
-          const int64_t i = t0 / GU + j * NT + threadIdx.x;
-          if (i < row_max) gmax[j * NT + threadIdx.x] = maxima[i];
-        }
+        const float* from = maxima + t0 / GU;
+        const int n = (int)(row_max - t0 / GU < SLOTS ? row_max - t0 / GU : SLOTS);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += NT) gmax[i] = from[i];
       };
       fetch(0);
       if (mine.id >= 0) z_mine = to_f32(z[mine.id]);
@@ -898,15 +907,15 @@ __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, co
       for (int i = threadIdx.x; i < kBins; i += NT) w.hist[i] = 0;
       __syncthreads();
       if (lone >= 0) w.cand[atomicAdd(&count[0], 1)] = entry_key(z_lone, (uint32_t)lone);
-      for (int64_t t0 = 0; t0 < cut.chunks; t0 += TILE) {
+      for (int64_t t0 = 0;;) {   // a split row has chunks
         const int64_t t1 = t0 + TILE < cut.chunks ? t0 + TILE : cut.chunks;
-        if (t0 > 0) {
-          keep_best<NT>(w);
-          fetch(t0);
-        }
         collect_tile<T, NT, U, GU, SLOTS>(w, gmax, z + cut.head, cut.head, t0, t1);
+        order_top<NT>(w, count[0]);
+        if (t1 >= cut.chunks) break;
+        keep_best<NT>(w);
+        t0 = t1;
+        fetch(t0);
       }
-      order_top<NT>(w, count[0]);
     } else {
       if (mine.id >= 0) z_mine = to_f32(z[mine.id]);
     }
