@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -447,8 +448,34 @@ MAX_TOP = 128          # SWG_MAX_TOP
 MAX_TEACHER = 1024     # SWG_MAX_TEACHER
 
 
-# The checks below test everything at once and leave it to the slow ones to say what is wrong:
-# a call on one row is bound by the host.
+# A call on few rows is bound by the host, so the checks below test everything at once and leave
+# it to the slow ones to say what is wrong, outputs that nobody gave are made in one go, and the
+# device is switched only where it is not the current one.
+def _gpu(device):
+    if device.type != "cuda":
+        raise ValueError(f"tensor on {device}: the library computes on the GPU only "
+                         f"(move inputs and outputs to a cuda device)")
+
+
+def _call(name, fn, device, *args):
+    """Calls an entry point on the tensors' device and torch's current stream there.  A call
+    given a stream makes it the current one first, so that what it allocates belongs to it."""
+    index = device.index
+    handle = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != 0:
+        raise SwgError(name, st, load_library())
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(query, *args):
+    return int(getattr(load_library(), query)(*args))
+
+
 def _rows(name, t, dtype, shape, device):
     """Checks a matrix whose rows are contiguous (any row stride that keeps them apart) and
     returns the row stride."""
@@ -514,22 +541,24 @@ def layer_norm_fwd(x, w, b, y=None, mean=None, rstd=None, eps=1e-5, stream=None)
     """Layer norm over the rows of x [M, N]: y = (x - mean) rstd w + b.  ``w`` and ``b`` [N] (or
     None) have x's dtype or fp32.  Returns y [M, N], and the fp32 mean and rstd [M] that
     ``layer_norm_bwd`` takes; outputs that are not given are allocated."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_fwd(x, w, b, y, mean, rstd, eps)
     lib = load_library()
-    M, N = _matrix("x", x)
+    shape = _matrix("x", x)
+    M, N = shape
     dt, dev = x.dtype, x.device
     code = _dtype_code(x)
-    ldx = _rows("x", x, dt, (M, N), dev)
+    ldx = _rows("x", x, dt, shape, dev)
     wdt = _affine(dt, N, dev, w=w, b=b)
-    with _on_device(dev):
-        if y is None:
-            y = torch.empty((M, N), dtype=dt, device=dev)
-        ldy = _rows("y", y, dt, (M, N), dev)
-        mean = _out("mean", mean, torch.float32, (M,), dev)
-        rstd = _out("rstd", rstd, torch.float32, (M,), dev)
-        st = lib.layer_norm_fwd(_addr(x), ldx, _addr(w), _addr(b), _addr(y), ldy, _addr(mean),
-                                _addr(rstd), M, N, eps, code, DTYPE_CODE[wdt],
-                                _stream(stream, dev))
-    _check("layer_norm_fwd", st, lib)
+    _gpu(dev)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    ldy = _rows("y", y, dt, shape, dev)
+    mean = _out("mean", mean, torch.float32, (M,), dev)
+    rstd = _out("rstd", rstd, torch.float32, (M,), dev)
+    _call("layer_norm_fwd", lib.layer_norm_fwd, dev, x.data_ptr(), ldx, _addr(w), _addr(b),
+          y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), M, N, eps, code, DTYPE_CODE[wdt])
     return y, mean, rstd
 
 
@@ -541,25 +570,28 @@ def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace
                    stream=None):
     """Gradients of ``layer_norm_fwd``: writes dx [M, N], dw and db [N] (each may be None);
     with ``accumulate`` dw and db are added to (+=)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate, workspace)
     lib = load_library()
-    M, N = _matrix("dy", dy)
+    shape = _matrix("dy", dy)
+    M, N = shape
     dt, dev = dy.dtype, dy.device
     code = _dtype_code(dy)
-    lddy = _rows("dy", dy, dt, (M, N), dev)
-    ldx = _rows("x", x, dt, (M, N), dev)
-    lddx = N if dx is None else _rows("dx", dx, dt, (M, N), dev)
+    lddy = _rows("dy", dy, dt, shape, dev)
+    ldx = _rows("x", x, dt, shape, dev)
+    lddx = N if dx is None else _rows("dx", dx, dt, shape, dev)
     wdt = _affine(dt, N, dev, w=w, dw=dw, db=db)
-    _packed("mean", mean, torch.float32, (M,), dev)
-    _packed("rstd", rstd, torch.float32, (M,), dev)
-    with _on_device(dev):
-        ws = workspace
-        if dw is not None or db is not None:
-            nbytes = int(lib.layer_norm_bwd_workspace_size(M, N, code))
-            ws = _workspace(nbytes, workspace, dev, stream)
-        st = lib.layer_norm_bwd(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(mean), _addr(rstd),
-                                _addr(dx), lddx, _addr(dw), _addr(db), int(accumulate), M, N, code,
-                                DTYPE_CODE[wdt], _addr(ws), _size(ws), _stream(stream, dev))
-    _check("layer_norm_bwd", st, lib)
+    mean_at = _packed("mean", mean, torch.float32, (M,), dev)
+    rstd_at = _packed("rstd", rstd, torch.float32, (M,), dev)
+    _gpu(dev)
+    ws = workspace
+    if dw is not None or db is not None:
+        ws = _workspace(_workspace_bytes("layer_norm_bwd_workspace_size", M, N, code), workspace,
+                        dev, None)
+    _call("layer_norm_bwd", lib.layer_norm_bwd, dev, dy.data_ptr(), lddy, x.data_ptr(),
+          ldx, _addr(w), mean_at, rstd_at, _addr(dx), lddx, _addr(dw), _addr(db), int(accumulate),
+          M, N, code, DTYPE_CODE[wdt], _addr(ws), _size(ws))
 
 
 class TokenLogprobs(NamedTuple):
@@ -570,6 +602,9 @@ class TokenLogprobs(NamedTuple):
     lse: torch.Tensor
     top_logprob: Optional[torch.Tensor]
     top_id: Optional[torch.Tensor]
+
+
+_NOTHING = TokenLogprobs(None, None, None, None, None)
 
 
 def token_logprobs_workspace_size(R: int, V: int, top: int, dtype) -> int:
@@ -583,31 +618,35 @@ def token_logprobs(logits, targets=None, top=0, temperature=1.0, ignore_index=-1
     (likeliest first, ties by rising id) with their log probabilities.  Returns
     ``TokenLogprobs``; ``out`` may hand back an earlier result of the same shape to be
     overwritten."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprobs(logits, targets, top, temperature, ignore_index, out, workspace)
     lib = load_library()
-    R, V = _matrix("logits", logits)
+    shape = _matrix("logits", logits)
+    R, V = shape
     dt, dev = logits.dtype, logits.device
     code = _dtype_code(logits)
-    ld = _rows("logits", logits, dt, (R, V), dev)
+    ld = _rows("logits", logits, dt, shape, dev)
     if targets is not None:
         _packed("targets", targets, torch.int64, (R,), dev)
     if out is None:
-        out = TokenLogprobs(None, None, None, None, None)
-    with _on_device(dev):
-        f32 = torch.float32
-        entropy = _out("out.entropy", out.entropy, f32, (R,), dev)
-        lse = _out("out.lse", out.lse, f32, (R,), dev)
-        logprob = top_lp = top_id = None
-        if targets is not None:
-            logprob = _out("out.logprob", out.logprob, f32, (R,), dev)
-        if top > 0:
-            top_lp = _out("out.top_logprob", out.top_logprob, f32, (R, top), dev)
-            top_id = _out("out.top_id", out.top_id, torch.int64, (R, top), dev)
-        ws = _workspace(int(lib.token_logprobs_workspace_size(R, V, top, code)), workspace, dev,
-                        stream)
-        st = lib.token_logprobs(_addr(logits), ld, _addr(targets), _addr(logprob), _addr(entropy),
-                                _addr(lse), _addr(top_lp), _addr(top_id), top, R, V, temperature,
-                                ignore_index, code, _addr(ws), _size(ws), _stream(stream, dev))
-    _check("token_logprobs", st, lib)
+        out = _NOTHING
+    _gpu(dev)
+    f32 = torch.float32
+    entropy = _out("out.entropy", out.entropy, f32, (R,), dev)
+    lse = torch.empty_like(entropy) if out.lse is None else _out("out.lse", out.lse, f32, (R,), dev)
+    logprob = top_lp = top_id = None
+    if targets is not None:
+        logprob = torch.empty_like(entropy) if out.logprob is None else _out(
+            "out.logprob", out.logprob, f32, (R,), dev)
+    if top > 0:
+        top_lp = _out("out.top_logprob", out.top_logprob, f32, (R, top), dev)
+        top_id = _out("out.top_id", out.top_id, torch.int64, (R, top), dev)
+    ws = _workspace(_workspace_bytes("token_logprobs_workspace_size", R, V, top, code), workspace,
+                    dev, None)
+    _call("token_logprobs", lib.token_logprobs, dev, logits.data_ptr(), ld,
+          _addr(targets), _addr(logprob), entropy.data_ptr(), lse.data_ptr(), _addr(top_lp),
+          _addr(top_id), top, R, V, temperature, ignore_index, code, _addr(ws), _size(ws))
     return TokenLogprobs(logprob, entropy, lse, top_lp, top_id)
 
 
@@ -616,25 +655,29 @@ def token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogit
     """Gradient of ``token_logprobs``'s logprob and entropy with respect to the logits, from
     dlogprob and dentropy [R] (fp32; either may be None, targets with dlogprob and entropy
     with dentropy).  ``dlogits`` [R, V] may be ``logits`` itself; it is returned."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogits,
+                                      temperature, ignore_index)
     lib = load_library()
-    R, V = _matrix("logits", logits)
+    shape = _matrix("logits", logits)
+    R, V = shape
     dt, dev = logits.dtype, logits.device
     code = _dtype_code(logits)
-    ld = _rows("logits", logits, dt, (R, V), dev)
+    ld = _rows("logits", logits, dt, shape, dev)
     if targets is not None:
         _packed("targets", targets, torch.int64, (R,), dev)
     for name, t in (("lse", lse), ("entropy", entropy), ("dlogprob", dlogprob),
                     ("dentropy", dentropy)):
         if t is not None or name == "lse":
             _packed(name, t, torch.float32, (R,), dev)
-    with _on_device(dev):
-        if dlogits is None:
-            dlogits = torch.empty((R, V), dtype=dt, device=dev)
-        ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
-        st = lib.token_logprobs_bwd(_addr(logits), ld, _addr(targets), _addr(lse), _addr(entropy),
-                                    _addr(dlogprob), _addr(dentropy), _addr(dlogits), ldd, R, V,
-                                    temperature, ignore_index, code, _stream(stream, dev))
-    _check("token_logprobs_bwd", st, lib)
+    _gpu(dev)
+    if dlogits is None:
+        dlogits = torch.empty(shape, dtype=dt, device=dev)
+    ldd = _rows("dlogits", dlogits, dt, shape, dev)
+    _call("token_logprobs_bwd", lib.token_logprobs_bwd, dev, logits.data_ptr(), ld,
+          _addr(targets), _addr(lse), _addr(entropy), _addr(dlogprob), _addr(dentropy),
+          dlogits.data_ptr(), ldd, R, V, temperature, ignore_index, code)
     return dlogits
 
 
@@ -650,48 +693,59 @@ def distill_workspace_size(R: int, V: int, k: int, dtype) -> int:
     return int(load_library().distill_workspace_size(R, V, k, DTYPE_CODE[dtype]))
 
 
+def _loss_and_lse(loss, lse, R, dev):
+    loss = _out("loss", loss, torch.float32, (R,), dev)
+    lse = torch.empty_like(loss) if lse is None else _out("lse", lse, torch.float32, (R,), dev)
+    return loss, lse
+
+
 def distill_fwd(logits, top, top_ids, temperature=1.0, loss=None, lse=None, workspace=None,
                 stream=None):
     """Distillation loss of logits [R, V] against a teacher's entries: values ``top`` [R, k]
     (logits or log probabilities, bf16, fp16 or fp32) at ``top_ids`` [R, k] (int64; ids
     outside [0, V) are padding).  Returns the fp32 loss [R] (T^2 times the divergence from
     the teacher's renormalised distribution) and the lse [R] ``distill_bwd`` takes."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return distill_fwd(logits, top, top_ids, temperature, loss, lse, workspace)
     lib = load_library()
-    R, V = _matrix("logits", logits)
+    shape = _matrix("logits", logits)
+    R, V = shape
     dt, dev = logits.dtype, logits.device
     code = _dtype_code(logits)
-    ld = _rows("logits", logits, dt, (R, V), dev)
+    ld = _rows("logits", logits, dt, shape, dev)
     k, top_code = _teacher(top, top_ids, R, dev)
-    with _on_device(dev):
-        loss = _out("loss", loss, torch.float32, (R,), dev)
-        lse = _out("lse", lse, torch.float32, (R,), dev)
-        ws = _workspace(int(lib.distill_workspace_size(R, V, k, code)), workspace, dev, stream)
-        st = lib.distill_fwd(_addr(logits), ld, _addr(top), _addr(top_ids), k, _addr(loss), _addr(lse),
-                             R, V, temperature, code, top_code, _addr(ws), _size(ws),
-                             _stream(stream, dev))
-    _check("distill_fwd", st, lib)
+    _gpu(dev)
+    loss, lse = _loss_and_lse(loss, lse, R, dev)
+    ws = _workspace(_workspace_bytes("distill_workspace_size", R, V, k, code), workspace, dev, None)
+    _call("distill_fwd", lib.distill_fwd, dev, logits.data_ptr(), ld, top.data_ptr(),
+          top_ids.data_ptr(), k, loss.data_ptr(), lse.data_ptr(), R, V, temperature, code,
+          top_code, _addr(ws), _size(ws))
     return loss, lse
 
 
 def distill_bwd(logits, top, top_ids, lse, dloss, dlogits=None, temperature=1.0, stream=None):
     """Gradient of ``distill_fwd``'s loss with respect to the logits, from dloss [R] (fp32; 0
     for a masked row).  ``dlogits`` [R, V] may be ``logits`` itself; it is returned."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return distill_bwd(logits, top, top_ids, lse, dloss, dlogits, temperature)
     lib = load_library()
-    R, V = _matrix("logits", logits)
+    shape = _matrix("logits", logits)
+    R, V = shape
     dt, dev = logits.dtype, logits.device
     code = _dtype_code(logits)
-    ld = _rows("logits", logits, dt, (R, V), dev)
+    ld = _rows("logits", logits, dt, shape, dev)
     k, top_code = _teacher(top, top_ids, R, dev)
-    _packed("lse", lse, torch.float32, (R,), dev)
-    _packed("dloss", dloss, torch.float32, (R,), dev)
-    with _on_device(dev):
-        if dlogits is None:
-            dlogits = torch.empty((R, V), dtype=dt, device=dev)
-        ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
-        st = lib.distill_bwd(_addr(logits), ld, _addr(top), _addr(top_ids), k, _addr(lse),
-                             _addr(dloss), _addr(dlogits), ldd, R, V, temperature, code, top_code,
-                             _stream(stream, dev))
-    _check("distill_bwd", st, lib)
+    lse_at = _packed("lse", lse, torch.float32, (R,), dev)
+    dloss_at = _packed("dloss", dloss, torch.float32, (R,), dev)
+    _gpu(dev)
+    if dlogits is None:
+        dlogits = torch.empty(shape, dtype=dt, device=dev)
+    ldd = _rows("dlogits", dlogits, dt, shape, dev)
+    _call("distill_bwd", lib.distill_bwd, dev, logits.data_ptr(), ld, top.data_ptr(),
+          top_ids.data_ptr(), k, lse_at, dloss_at, dlogits.data_ptr(), ldd, R, V, temperature,
+          code, top_code)
     return dlogits
 
 
@@ -700,22 +754,25 @@ def distill_fwd_bwd(logits, top, top_ids, dloss, dlogits=None, temperature=1.0, 
     """``distill_fwd`` and ``distill_bwd`` in one call, for a training step that knows the row
     weights ``dloss`` [R] beforehand.  ``dlogits`` may be ``logits`` itself.  Returns
     (loss, lse, dlogits)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return distill_fwd_bwd(logits, top, top_ids, dloss, dlogits, temperature, loss, lse,
+                                   workspace)
     lib = load_library()
-    R, V = _matrix("logits", logits)
+    shape = _matrix("logits", logits)
+    R, V = shape
     dt, dev = logits.dtype, logits.device
     code = _dtype_code(logits)
-    ld = _rows("logits", logits, dt, (R, V), dev)
+    ld = _rows("logits", logits, dt, shape, dev)
     k, top_code = _teacher(top, top_ids, R, dev)
-    _packed("dloss", dloss, torch.float32, (R,), dev)
-    with _on_device(dev):
-        loss = _out("loss", loss, torch.float32, (R,), dev)
-        lse = _out("lse", lse, torch.float32, (R,), dev)
-        if dlogits is None:
-            dlogits = torch.empty((R, V), dtype=dt, device=dev)
-        ldd = _rows("dlogits", dlogits, dt, (R, V), dev)
-        ws = _workspace(int(lib.distill_workspace_size(R, V, k, code)), workspace, dev, stream)
-        st = lib.distill_fwd_bwd(_addr(logits), ld, _addr(top), _addr(top_ids), k, _addr(dloss),
-                                 _addr(loss), _addr(lse), _addr(dlogits), ldd, R, V, temperature,
-                                 code, top_code, _addr(ws), _size(ws), _stream(stream, dev))
-    _check("distill_fwd_bwd", st, lib)
+    dloss_at = _packed("dloss", dloss, torch.float32, (R,), dev)
+    _gpu(dev)
+    loss, lse = _loss_and_lse(loss, lse, R, dev)
+    if dlogits is None:
+        dlogits = torch.empty(shape, dtype=dt, device=dev)
+    ldd = _rows("dlogits", dlogits, dt, shape, dev)
+    ws = _workspace(_workspace_bytes("distill_workspace_size", R, V, k, code), workspace, dev, None)
+    _call("distill_fwd_bwd", lib.distill_fwd_bwd, dev, logits.data_ptr(), ld,
+          top.data_ptr(), top_ids.data_ptr(), k, dloss_at, loss.data_ptr(), lse.data_ptr(),
+          dlogits.data_ptr(), ldd, R, V, temperature, code, top_code, _addr(ws), _size(ws))
     return loss, lse, dlogits
