@@ -143,6 +143,11 @@ __device__ inline void load_affine(const W* w, int64_t c, float absent, float* f
   }
 }
 
+// 1 / sqrt(v): the hardware's reciprocal root (1 ulp), which takes no subnormal
+__device__ inline float inv_root(float v) {
+  return v < 1.17549435e-38f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
+}
+
 template <typename T, typename W, int G, int EC>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, const W* w,
                                                        const W* b, T* y, int64_t ldy,
@@ -153,6 +158,12 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
   const int lane = threadIdx.x % G;
   const RowMap<G, EC> map(lane, N);
   const float inv_n = 1.0f / (float)N;
+  // of one chunk w and b stay in registers, of more they are read again (from cache)
+  float wv[EC == 1 ? 8 : 1], bv[EC == 1 ? 8 : 1];
+  if constexpr (EC == 1) {
+    load_affine(w, map.col[0], 1.0f, wv);
+    load_affine(b, map.col[0], 0.0f, bv);
+  }
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
   Chunk<T> cur[EC], next[EC];
@@ -179,7 +190,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
       drop(g, map.skip[j]);
       s += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
     }
-    const float mu = row_sum<G>(s, red[0], (threadIdx.x / G) * (G / 64)) / (float)N;
+    const float mu = row_sum<G>(s, red[0], (threadIdx.x / G) * (G / 64)) * inv_n;
     s = 0.0f;
 #pragma unroll
     for (int j = 0; j < EC; ++j) {
@@ -192,15 +203,20 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
       for (int i = 0; i < 8; ++i) q = __builtin_fmaf(g[i], g[i], q);
       s += q;
     }
-    const float var = row_sum<G>(s, red[1], (threadIdx.x / G) * (G / 64)) / (float)N;
-    const float rs = 1.0f / __builtin_sqrtf(var + eps);
+    const float var = row_sum<G>(s, red[1], (threadIdx.x / G) * (G / 64)) * inv_n;
+    const float rs = inv_root(var + eps);
     if (r < M) {
 #pragma unroll
       for (int j = 0; j < EC; ++j) {
         if (!map.has(j)) continue;
         float g[8], h[8];
-        load_affine(w, map.col[j], 1.0f, g);
-        load_affine(b, map.col[j], 0.0f, h);
+        if constexpr (EC == 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = wv[i], h[i] = bv[i];
+        } else {
+          load_affine(w, map.col[j], 1.0f, g);
+          load_affine(b, map.col[j], 0.0f, h);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = __builtin_fmaf(f[j][i] * rs, g[i], h[i]);
         Chunk<T> o;
@@ -240,6 +256,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
 #pragma unroll
     for (int i = 0; i < 8; ++i) sw[j][i] = sb[j][i] = 0.0f;
   }
+  const float inv_n = 1.0f / (float)a.N;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t r = (int64_t)blockIdx.x * ROWS + grp;
   int half = 0;
@@ -289,7 +306,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
         }
         half ^= 1;
       }
-      const float c1 = s1 / (float)a.N, c2 = s2 / (float)a.N;
+      const float c1 = s1 * inv_n, c2 = s2 * inv_n;
       if (live) {
 #pragma unroll
         for (int j = 0; j < EC; ++j) {
