@@ -143,6 +143,13 @@ __device__ inline void load_affine(const W* w, int64_t c, float absent, float* f
   }
 }
 
+// The thread's row group; groups of whole waves in a scalar register, and with it the row's
+// addresses and statistics.
+template <int G> __device__ inline int row_group() {
+  const int g = (int)(threadIdx.x / G);
+  return G < 64 ? g : __builtin_amdgcn_readfirstlane(g);
+}
+
 // 1 / sqrt(v): the hardware's reciprocal root (1 ulp), which takes no subnormal
 __device__ inline float inv_root(float v) {
   return v < 1.17549435e-38f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
@@ -165,7 +172,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
     load_affine(b, map.col[0], 0.0f, bv);
   }
   const int64_t step = (int64_t)gridDim.x * ROWS;
-  int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
+  const int grp = row_group<G>();
+  int64_t r = (int64_t)blockIdx.x * ROWS + grp;
   Chunk<T> cur[EC], next[EC];
 #pragma unroll
   for (int j = 0; j < EC; ++j) {
@@ -190,7 +198,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
       drop(g, map.skip[j]);
       s += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
     }
-    const float mu = row_sum<G>(s, red[0], (threadIdx.x / G) * (G / 64)) * inv_n;
+    const float mu = row_sum<G>(s, red[0], grp * (G / 64)) * inv_n;
     s = 0.0f;
 #pragma unroll
     for (int j = 0; j < EC; ++j) {
@@ -203,7 +211,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, 
       for (int i = 0; i < 8; ++i) q = __builtin_fmaf(g[i], g[i], q);
       s += q;
     }
-    const float var = row_sum<G>(s, red[1], (threadIdx.x / G) * (G / 64)) * inv_n;
+    const float var = row_sum<G>(s, red[1], grp * (G / 64)) * inv_n;
     const float rs = inv_root(var + eps);
     if (r < M) {
 #pragma unroll
@@ -242,7 +250,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
   constexpr int ROWS = 1024 / G;
   __shared__ float red[2][2][16];
   __shared__ float sums[ROWS > 1 ? 1024 * EC * 8 : 1];
-  const int lane = threadIdx.x % G, grp = threadIdx.x / G, wave0 = grp * (G / 64);
+  const int lane = threadIdx.x % G, grp = row_group<G>(), wave0 = grp * (G / 64);
   const RowMap<G, EC> map(lane, a.N);
   const T* dy = static_cast<const T*>(a.dy);
   const T* x = static_cast<const T*>(a.x);
