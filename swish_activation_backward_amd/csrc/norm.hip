@@ -268,18 +268,25 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t r = (int64_t)blockIdx.x * ROWS + grp;
   int half = 0;
-  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.M; base += step, r += step) {
-    Chunk<T> cd[EC], cx[EC];
-    const bool live = r < a.M;
+  auto load = [&](Chunk<T>* d, Chunk<T>* f, int64_t row) {
 #pragma unroll
     for (int j = 0; j < EC; ++j) {
-      cd[j].zero();
-      cx[j].zero();
-      if (map.has(j) && live) {
-        cd[j].load_stream(dy + r * a.lddy + map.col[j]);
-        cx[j].load_stream(x + r * a.ldx + map.col[j]);
+      d[j].zero();
+      f[j].zero();
+      if (map.has(j) && row < a.M) {
+        d[j].load_stream(dy + row * a.lddy + map.col[j]);
+        f[j].load_stream(x + row * a.ldx + map.col[j]);
       }
     }
+  };
+  // one chunk a thread leaves registers for the next row's loads
+  constexpr bool AHEAD = EC == 1;
+  Chunk<T> cd[EC], cx[EC], nd[EC], nx[EC];
+  if (AHEAD) load(cd, cx, r);
+  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.M; base += step, r += step) {
+    const bool live = r < a.M;
+    if (AHEAD) load(nd, nx, r + step);
+    else load(cd, cx, r);
     const float mu = live ? a.mean[r] : 0.0f, rs = live ? a.rstd[r] : 0.0f;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -341,6 +348,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
           o.store_stream(dx + r * a.lddx + map.col[j]);
         }
       }
+    }
+    if (AHEAD) {
+#pragma unroll
+      for (int j = 0; j < EC; ++j) cd[j] = nd[j], cx[j] = nx[j];
     }
   }
   if (!a.dw && !a.db) return;
