@@ -11,12 +11,16 @@ otherwise ``swiglu_bwd_w`` (dW) or ``swiglu_bwd_x`` (dx).  The pattern is a cust
 kernel (the Ascend C custom-backward page, "突破自动微分瓶颈: 基于 Ascend C 的高性能自定义反向传播
 算子实战", section 4.2, Python-side registration); the weight layout [K, N] is the SwiGLU
 page's.  Leading dimensions of x are flattened into M.
+
+Around the gate, in the same manner: ``layer_norm`` / ``LayerNorm``, ``token_logprobs`` (log
+probability of given tokens and entropy) and ``distill_loss`` (a teacher's top logits).
 """
 from __future__ import annotations
 
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -96,3 +100,131 @@ class SwiGLU(torch.nn.Module):
 
     def forward(self, x):
         return swiglu(x, self.w_g, self.w_fc, self.b_g, self.b_fc)
+
+
+def _rows_of(x):
+    """x [..., N] as a matrix of contiguous rows (a view where its layout allows)."""
+    x2 = x.reshape(-1, x.shape[-1])
+    R, C = x2.shape
+    if (C > 1 and x2.stride(1) != 1) or (R > 1 and x2.stride(0) < C):
+        x2 = x2.contiguous()
+    return x2
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """x [M, N], w / b [N] or None -> y [M, N]."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        y, mean, rstd = _lib.layer_norm_fwd(x, w, b, eps=eps)
+        ctx.save_for_backward(x, w, mean, rstd)
+        ctx.wdtype = next((t.dtype for t in (w, b) if t is not None), x.dtype)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, mean, rstd = ctx.saved_tensors
+        dy = _rows_of(dy)
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        N, dev = x.shape[1], x.device
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_x else None
+        dw = torch.empty(N, dtype=ctx.wdtype, device=dev) if need_w else None
+        db = torch.empty(N, dtype=ctx.wdtype, device=dev) if need_b else None
+        _lib.layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db)
+        return dx, dw, db, None
+
+
+def layer_norm(x, w=None, b=None, eps=1e-5):
+    """Layer norm over the last dimension of x (any leading shape); ``w`` and ``b`` have x's
+    dtype or fp32."""
+    return LayerNormFunction.apply(_rows_of(x), w, b, eps).view(x.shape)
+
+
+class LayerNorm(torch.nn.Module):
+    """Parameters w (ones) and b (zeros, optional) [features], of ``dtype`` (fp32 goes with any
+    activations); forward(x) norms [..., features]."""
+
+    def __init__(self, features, eps=1e-5, bias=True, device=None, dtype=torch.float32):
+        super().__init__()
+        self.eps = eps
+        self.w = torch.nn.Parameter(torch.ones(features, device=device, dtype=dtype))
+        if bias:
+            self.b = torch.nn.Parameter(torch.zeros(features, device=device, dtype=dtype))
+        else:
+            self.register_parameter("b", None)
+
+    def forward(self, x):
+        return layer_norm(x, self.w, self.b, self.eps)
+
+
+class TokenLogprobsFunction(torch.autograd.Function):
+    """logits [R, V], targets [R] (int64) -> logprob [R], entropy [R] (fp32)."""
+
+    @staticmethod
+    def forward(ctx, logits, targets, temperature, ignore_index):
+        r = _lib.token_logprobs(logits, targets, temperature=temperature,
+                                ignore_index=ignore_index)
+        ctx.save_for_backward(logits, targets, r.lse, r.entropy)
+        ctx.temperature, ctx.ignore_index = temperature, ignore_index
+        ctx.set_materialize_grads(False)
+        return r.logprob, r.entropy
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogprob, dentropy):
+        if not ctx.needs_input_grad[0] or (dlogprob is None and dentropy is None):
+            return None, None, None, None
+        logits, targets, lse, entropy = ctx.saved_tensors
+        dlogits = _lib.token_logprobs_bwd(
+            logits, None if dlogprob is None else targets, lse,
+            None if dentropy is None else entropy,
+            None if dlogprob is None else dlogprob.contiguous(),
+            None if dentropy is None else dentropy.contiguous(),
+            torch.empty(logits.shape, dtype=logits.dtype, device=logits.device),
+            temperature=ctx.temperature, ignore_index=ctx.ignore_index)
+        return dlogits, None, None, None
+
+
+def token_logprobs(logits, targets, temperature=1.0, ignore_index=-100):
+    """Log probability of each of the ``targets`` [...] (int64) under
+    softmax(logits / temperature), logits [..., V], and the entropy, both fp32 of shape [...]
+    and differentiable with respect to the logits."""
+    lp, ent = TokenLogprobsFunction.apply(_rows_of(logits), targets.reshape(-1).contiguous(),
+                                          temperature, ignore_index)
+    return lp.view(targets.shape), ent.view(targets.shape)
+
+
+class DistillFunction(torch.autograd.Function):
+    """logits [R, V], top and top_ids [R, k] -> loss [R] (fp32)."""
+
+    @staticmethod
+    def forward(ctx, logits, top, top_ids, temperature):
+        loss, lse = _lib.distill_fwd(logits, top, top_ids, temperature=temperature)
+        ctx.save_for_backward(logits, top, top_ids, lse)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss):
+        if not ctx.needs_input_grad[0]:
+            return None, None, None, None
+        logits, top, top_ids, lse = ctx.saved_tensors
+        dlogits = _lib.distill_bwd(
+            logits, top, top_ids, lse, dloss.contiguous(),
+            torch.empty(logits.shape, dtype=logits.dtype, device=logits.device),
+            temperature=ctx.temperature)
+        return dlogits, None, None, None
+
+
+def distill_loss(logits, top, top_ids, temperature=1.0):
+    """Distillation loss [...] (fp32) of logits [..., V] against a teacher's entries ``top``
+    and ``top_ids`` [..., k], e.g. what ``token_logprobs`` of the binding returned for the
+    teacher's logits; differentiable with respect to the logits (the teacher's entries are
+    constants).  ``distill_fwd_bwd`` of the binding forms the same loss with its gradient in
+    one pass where the row weights are known beforehand."""
+    k = top.shape[-1]
+    loss = DistillFunction.apply(_rows_of(logits), top.detach().reshape(-1, k).contiguous(),
+                                 top_ids.reshape(-1, k).contiguous(), temperature)
+    return loss.view(logits.shape[:-1])

@@ -741,7 +741,7 @@ size_t distill_workspace_size(int64_t R, int64_t V, int64_t k, swg_dtype dtype) 
   if (!dtype_ok(dtype) || !row_dims_ok(R, V) || R == 0 || V == 0 || k < 1 ||
       k > SWG_MAX_TEACHER)
     return 0;
-  return plan_vocab(R, V, 0, dtype).ws_bytes;
+  return distill_ws_bytes(plan_vocab(R, V, 0, dtype), R, V, dtype);
 }
 
 swg_status distill_fwd(const void* logits, int64_t ld, const void* top, const int64_t* top_ids,
@@ -817,7 +817,7 @@ swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
   const int64_t es = elem_size(dtype);
   if (!aligned(dlogits, (size_t)es)) return SWG_ERR_INVALID;
   const VocabPlan p = plan_vocab(R, V, 0, dtype);
-  const size_t need = p.ws_bytes;
+  const size_t need = distill_ws_bytes(p, R, V, dtype);
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   const Span outs[] = {{dlogits, rows_bytes(R, V, ldd, es)}, {loss, 4 * R}, {lse, 4 * R},
@@ -833,6 +833,8 @@ swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
   VocabArgs a = vocab_args(logits, ld, R, V, temperature);
   a.teacher = top; a.teacher_dtype = top_dtype; a.ids = top_ids; a.k = k; a.dloss = dloss;
   a.loss = loss; a.lse = lse; a.dz = dlogits; a.lddz = ldd;
+  if (!distill_held(R, V, dtype))
+    a.stat = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.stat_at);
   return hip_status(launch_distill_fwd_bwd(dtype, a, p, workspace, as_stream(stream)));
 }
 

@@ -150,6 +150,7 @@ struct VocabArgs {
   int64_t k;
   float* loss;
   const float* dloss;
+  float* stat;              // [R, 2]: m and ln sum exp(a - m), between the two kernels of a call
 };
 hipError_t launch_logprobs(int dtype, const VocabArgs& a, const VocabPlan& p, void* ws,
                            hipStream_t stream);

@@ -334,8 +334,18 @@ struct VocabPlan {
   int64_t seg;
   int64_t row_max;
   size_t max_at;
+  size_t stat_at;    // of the distillation's two-kernel form, past ws_bytes of the forward
   size_t ws_bytes;
 };
+
+// Rows that a workgroup can hold in registers (in 16-bit units), and rows enough for that to pay:
+// the distillation loss with its gradient reads such logits once.  Otherwise the call's two
+// kernels hand 8 bytes a row on through the workspace.
+constexpr int64_t kHeldRow = 131072;
+constexpr int64_t kHeldRows = 256;
+inline bool distill_held(int64_t R, int64_t V, int dtype) {
+  return R >= kHeldRows && V * (dtype == 2 ? 2 : 1) <= kHeldRow;
+}
 
 inline VocabPlan plan_vocab(int64_t R, int64_t V, int64_t top, int dtype) {
   VocabPlan p{};
@@ -353,7 +363,12 @@ inline VocabPlan plan_vocab(int64_t R, int64_t V, int64_t top, int dtype) {
     p.max_at = (size_t)ceil_div(R * p.split * 12, 16) * 16;
     p.ws_bytes = p.max_at + (top > 0 ? (size_t)(R * p.row_max) * 4 : 0);
   }
+  p.stat_at = (p.ws_bytes + 15) / 16 * 16;
   return p;
+}
+
+inline size_t distill_ws_bytes(const VocabPlan& p, int64_t R, int64_t V, int dtype) {
+  return distill_held(R, V, dtype) ? p.ws_bytes : p.stat_at + (size_t)R * 8;
 }
 
 }  // namespace swg

@@ -663,6 +663,10 @@ __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum
     if (threadIdx.x == 0) {
       a.loss[r] = a.t * a.t * kl;
       if (a.lse) a.lse[r] = st.lse;
+      if (a.stat) {
+        a.stat[2 * r] = st.empty ? 0.0f : st.m;
+        a.stat[2 * r + 1] = st.empty ? 0.0f : st.ls;
+      }
     }
   }
 }
@@ -1005,7 +1009,10 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
     const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
     Entry mine{-1, neg_inf()};
     if constexpr (MODE == kDistill) mine = load_entry(a, r, threadIdx.x);
-    const float lse_in = a.lse_in[r];
+    // log p = (z - m) / T - ls; with only lse, which rounds ls off beside a large m / T, m = 0
+    const bool has_stat = MODE == kDistill && a.stat != nullptr;
+    const float m = has_stat ? a.stat[2 * r] : 0.0f;
+    const float ls_in = has_stat ? a.stat[2 * r + 1] : a.lse_in[r];
     // the segment's columns
     const int64_t from = part_i == 0 ? 0 : cut.head + c0 * 8;
     const int64_t to = part_i == split - 1 ? a.V : cut.head + c1 * 8;
@@ -1022,7 +1029,7 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
         c0 - (int64_t)((reinterpret_cast<uintptr_t>(out + c0 * 8) & 127) / (8 * sizeof(T)));
     Chunk<T> ch[U], next[U];
     load(ch, start);
-    const float lse = lse_in == neg_inf() ? 0.0f : lse_in;   // a row of masked entries: p = 0
+    const float ls = ls_in == neg_inf() ? 0.0f : ls_in;   // a row of masked entries: p = 0
 
     float scale = 0.0f, gain = 0.0f, A = 0.0f, g = 0.0f, h = 0.0f, H = 0.0f;
     int64_t id = -1;
@@ -1057,7 +1064,7 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
       __syncthreads();   // all entries' logits are read
     }
     auto value = [&](float x) {   // log p
-      return __builtin_fmaf(x, a.inv_t, -lse);
+      return __builtin_fmaf(x - m, a.inv_t, -ls);
     };
     auto prob = [&](float x) { return __builtin_amdgcn_exp2f(value(x) * kLog2e); };
     auto at_target = [&](float x) {
@@ -1291,7 +1298,7 @@ static hipError_t distill_rows(const VocabArgs& a, hipStream_t stream, bool& hel
 #define SWG_HELD(NT, D, WAVES)                                                               \
   SWG_LAUNCH((distill_kernel<T, NT, D * 2 / (int)sizeof(T), WAVES>), dim3(row_grid(a.R)),    \
              dim3(NT), lds, stream, a)
-  if (a.R < 256 || v > 131072) held = false;
+  if (a.stat) held = false;
   else if (v <= 2048) SWG_HELD(64, 4, 4);
   else if (v <= 8192) SWG_HELD(256, 4, 4);
   else if (v <= 16384) SWG_HELD(256, 8, 4);
