@@ -365,9 +365,10 @@ swg_status distill_bwd(const void* logits, int64_t ld, const void* top,
 /*
  * Both in one call, for a training step that knows its row weights dloss beforehand (such
  * as 1 / rows): loss and lse as distill_fwd, dlogits as distill_bwd, to within rounding (and
- * with p that sum to 1 in every row).  Reads the logits once from 256 rows on, up to
- * 131072 16-bit or 65536 fp32 logits a row.  lse may not be NULL.  dlogits may be exactly
- * logits.  workspace as distill_fwd.
+ * with p that sum to 1 in every row).  Reads the logits once where a workgroup can hold a row,
+ * up to 131072 16-bit or 65536 fp32 logits (and, of rows over a quarter of that, where there
+ * are enough of them).  lse may not be NULL.  dlogits may be exactly logits.  workspace as
+ * distill_fwd.
  */
 swg_status distill_fwd_bwd(const void* logits, int64_t ld, const void* top,
                            const int64_t* top_ids, int64_t k, const float* dloss,

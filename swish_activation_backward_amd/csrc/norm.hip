@@ -156,12 +156,11 @@ __device__ inline float inv_root(float v) {
 }
 
 template <typename T, typename W, int G, int EC>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(const T* x, int64_t ldx, const W* w,
-                                                       const W* b, T* y, int64_t ldy,
-                                                       float* mean, float* rstd, int64_t M,
-                                                       int64_t N, float eps) {
-  constexpr int ROWS = 256 / G;
-  __shared__ float red[2][4];
+__global__ __launch_bounds__(G > 256 ? G : 256) void norm_fwd_kernel(
+    const T* x, int64_t ldx, const W* w, const W* b, T* y, int64_t ldy, float* mean, float* rstd,
+    int64_t M, int64_t N, float eps) {
+  constexpr int ROWS = G > 256 ? 1 : 256 / G;
+  __shared__ float red[2][G > 256 ? G / 64 : 4];
   const int lane = threadIdx.x % G;
   const RowMap<G, EC> map(lane, N);
   const float inv_n = 1.0f / (float)N;
@@ -399,6 +398,16 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
   float* pw = part + (int64_t)blockIdx.x * 2 * Np;
 #pragma unroll
   for (int j = 0; j < EC; ++j) {
+    if (gridDim.x > 1 && map.skip[j] == 0) {   // a whole chunk: columns 8 n, 16-byte aligned
+      f32x4* w4 = reinterpret_cast<f32x4*>(pw + map.col[j]);
+      f32x4* b4 = reinterpret_cast<f32x4*>(pw + Np + map.col[j]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w4[i] = f32x4{sw[j][4 * i], sw[j][4 * i + 1], sw[j][4 * i + 2], sw[j][4 * i + 3]};
+        b4[i] = f32x4{sb[j][4 * i], sb[j][4 * i + 1], sb[j][4 * i + 2], sb[j][4 * i + 3]};
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i < map.skip[j]) continue;
@@ -414,28 +423,31 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part,
   }
 }
 
-// Sums the partial rows: 16 columns to a workgroup, 64 threads a column group of 4, each over
-// every 64th partial row, then those in order.
-template <typename W>
+// Sums the partial rows: Q groups of 4 columns to a workgroup, 256 / Q threads a group, each over
+// every (256 / Q)-th partial row, then those in order.  Q = 4 gives narrow norms workgroups, 16
+// reads whole lines of wide ones.
+template <typename W, int Q>
 __global__ __launch_bounds__(256) void norm_finalize_kernel(const float* part, int64_t nparts,
                                                             W* dw, W* db, int64_t N, int64_t Np,
                                                             int acc) {
-  __shared__ f32x4 red[64][4];
-  const int q = threadIdx.x & 3, lane = threadIdx.x >> 2;
-  const int64_t c = ((int64_t)blockIdx.x * 4 + q) * 4;   // column of the 2 Np
+  constexpr int P = 256 / Q;
+  __shared__ f32x4 red[P][Q];
+  const int q = threadIdx.x % Q, lane = threadIdx.x / Q;
+  const int64_t c = ((int64_t)blockIdx.x * Q + q) * 4;   // column of the 2 Np
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < 2 * Np) {
-    for (int64_t p = lane; p < nparts; p += 64)
+#pragma unroll 4
+    for (int64_t p = lane; p < nparts; p += P)
       s += *reinterpret_cast<const f32x4*>(part + p * 2 * Np + c);
   }
   red[lane][q] = s;
   __syncthreads();
-  for (int n = 32; n > 0; n >>= 1) {
+  for (int n = P / 2; n > 0; n >>= 1) {
     if (lane < n) red[lane][q] += red[lane + n][q];
     __syncthreads();
   }
-  if (threadIdx.x >= 16) return;
-  const int64_t e = (int64_t)blockIdx.x * 16 + threadIdx.x;
+  if (threadIdx.x >= 4 * Q) return;
+  const int64_t e = (int64_t)blockIdx.x * 4 * Q + threadIdx.x;
   const int64_t col = e < Np ? e : e - Np;
   W* dst = e < Np ? dw : db;
   if (e >= 2 * Np || col >= N || dst == nullptr) return;
@@ -458,8 +470,9 @@ static hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
   T* y = static_cast<T*>(a.y);
 #define SWG_FWD(G, EC)                                                                        \
   SWG_TRY(SWG_LAUNCH((norm_fwd_kernel<T, W, G, EC>),                                          \
-                     dim3(norm_fwd_grid(a.M, 256 / G)), dim3(256), 0, stream, x, a.ldx, w, b, \
-                     y, a.ldy, a.mean, a.rstd, a.M, a.N, a.eps))
+                     dim3(norm_fwd_grid(a.M, G > 256 ? 1 : 256 / G, G > 256 ? G : 256)),      \
+                     dim3(G > 256 ? G : 256), 0, stream, x, a.ldx, w, b, y, a.ldy,            \
+                     a.mean, a.rstd, a.M, a.N, a.eps))
   if (a.N < 8 || a.N > 16384) {
     SWG_TRY(SWG_LAUNCH((norm_fwd_any_kernel<T, W>), dim3(row_grid(a.M)), dim3(256), 0, stream, x,
                        a.ldx, w, b, y, a.ldy, a.mean, a.rstd, a.M, a.N, a.eps));
@@ -470,8 +483,8 @@ static hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
   else if (a.N <= 1024) SWG_FWD(64, 2);
   else if (a.N <= 2048) SWG_FWD(256, 1);
   else if (a.N <= 4096) SWG_FWD(256, 2);
-  else if (a.N <= 8192) SWG_FWD(256, 4);
-  else SWG_FWD(256, 8);
+  else if (a.N <= 8192) SWG_FWD(512, 2);
+  else SWG_FWD(1024, 2);
 #undef SWG_FWD
   return hipSuccess;
 }
@@ -515,9 +528,15 @@ static hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, float* part,
   }
   // M = 0: no partial rows, the empty sums
   const int64_t np = a.M > 0 ? p.np : ceil_div(a.N, 4) * 4;
-  SWG_TRY(SWG_LAUNCH((norm_finalize_kernel<W>), dim3((unsigned)ceil_div(2 * np, 16)), dim3(256),
-                     0, stream, part, a.M > 0 ? p.parts : 0, static_cast<W*>(a.dw),
-                     static_cast<W*>(a.db), a.N, np, a.accumulate));
+  const int64_t parts = a.M > 0 ? p.parts : 0;
+  if (np < 2048)
+    SWG_TRY(SWG_LAUNCH((norm_finalize_kernel<W, 4>), dim3((unsigned)ceil_div(2 * np, 16)),
+                       dim3(256), 0, stream, part, parts, static_cast<W*>(a.dw),
+                       static_cast<W*>(a.db), a.N, np, a.accumulate));
+  else
+    SWG_TRY(SWG_LAUNCH((norm_finalize_kernel<W, 16>), dim3((unsigned)ceil_div(2 * np, 64)),
+                       dim3(256), 0, stream, part, parts, static_cast<W*>(a.dw),
+                       static_cast<W*>(a.db), a.N, np, a.accumulate));
   return hipSuccess;
 }
 

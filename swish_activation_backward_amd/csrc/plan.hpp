@@ -285,9 +285,9 @@ inline unsigned row_grid(int64_t rows) {
 
 // Workgroups of the norm's forward pass, `rows` rows at a time each: all resident at once, so
 // that each walks over its rows with the next ones' loads in flight.
-inline unsigned norm_fwd_grid(int64_t M, int rows) {
-  const int64_t n = ceil_div(M, rows);
-  return (unsigned)(n < 2048 ? n : 2048);
+inline unsigned norm_fwd_grid(int64_t M, int rows, int threads) {
+  const int64_t n = ceil_div(M, rows), all = 2048 * 256 / threads;
+  return (unsigned)(n < all ? n : all);
 }
 
 // Layer norm's backward pass.  Rows of 8 to 16384 elements: `group` threads hold a row, `chunks`
@@ -338,13 +338,14 @@ struct VocabPlan {
   size_t ws_bytes;
 };
 
-// Rows that a workgroup can hold in registers (in 16-bit units), and rows enough for that to pay:
-// the distillation loss with its gradient reads such logits once.  Otherwise the call's two
-// kernels hand 8 bytes a row on through the workspace.
-constexpr int64_t kHeldRow = 131072;
-constexpr int64_t kHeldRows = 256;
+// The distillation loss with its gradient reads the logits once where a workgroup can hold a row
+// in registers (64 to 256 KiB of them) and, for the longer rows, there are enough rows: one row
+// of 131072 bf16 takes 23 us so and 13 us split over the two kernels, 128 of them 24 and 31 us;
+// of 65536, 16 rows 15.6 and 14.6, 80 rows 16.9 and 17.8 us.  The two kernels hand 8 bytes a row
+// on through the workspace.
 inline bool distill_held(int64_t R, int64_t V, int dtype) {
-  return R >= kHeldRows && V * (dtype == 2 ? 2 : 1) <= kHeldRow;
+  const int64_t v = V * (dtype == 2 ? 2 : 1);   // in 16-bit units
+  return v <= 32768 || (v <= 131072 && R * 1024 >= v);
 }
 
 inline VocabPlan plan_vocab(int64_t R, int64_t V, int64_t top, int dtype) {

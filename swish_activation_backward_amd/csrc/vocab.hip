@@ -1132,7 +1132,7 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
     const T* z = static_cast<const T*>(a.z) + r * a.ld;
     T* dz = static_cast<T*>(a.dz) + r * a.lddz;
-    const RowCut cut(dz, a.V);
+    const RowCut cut(z, a.V);   // by the logits: the sums do not depend on where dz lies
     const T* body = z + cut.head;
     T* out = dz + cut.head;
     const int lone = cut.single(threadIdx.x, a.V, true, true);
