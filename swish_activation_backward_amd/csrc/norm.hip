@@ -13,67 +13,70 @@
 namespace swg {
 
 // ------------------------------------------------------------------ rows of any length
+// Rows under 8 or over 16384 elements: a workgroup a row, one element at a time; the second and
+// third pass over a row come from cache.
 template <typename T, typename W>
 __global__ __launch_bounds__(256) void norm_fwd_any_kernel(const T* x, int64_t ldx, const W* w,
-                                                       const W* b, T* y, int64_t ldy,
-                                                       float* mean, float* rstd, int64_t M,
-                                                       int64_t N, float eps) {
+                                                           const W* b, T* y, int64_t ldy,
+                                                           float* mean, float* rstd, int64_t M,
+                                                           int64_t N, float eps) {
   __shared__ float red[4];
   for (int64_t r = blockIdx.x; r < M; r += gridDim.x) {
-  const T* xr = x + r * ldx;
-  float s = 0.0f;
-  for (int64_t c = threadIdx.x; c < N; c += 256) s += to_f32(xr[c]);
-  const float mu = block_sum<256>(s, red) / (float)N;
-  s = 0.0f;
-  for (int64_t c = threadIdx.x; c < N; c += 256) {
-    const float d = to_f32(xr[c]) - mu;
-    s = __builtin_fmaf(d, d, s);
-  }
-  const float rs = 1.0f / __builtin_sqrtf(block_sum<256>(s, red) / (float)N + eps);
-  for (int64_t c = threadIdx.x; c < N; c += 256) {
-    float v = (to_f32(xr[c]) - mu) * rs;
-    if (w) v *= to_f32(w[c]);
-    if (b) v += to_f32(b[c]);
-    y[r * ldy + c] = from_f32<T>(v);
-  }
-  if (threadIdx.x == 0) {
-    if (mean) mean[r] = mu;
-    if (rstd) rstd[r] = rs;
-  }
+    const T* xr = x + r * ldx;
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x; c < N; c += 256) s += to_f32(xr[c]);
+    const float mu = block_sum<256>(s, red) / (float)N;
+    s = 0.0f;
+    for (int64_t c = threadIdx.x; c < N; c += 256) {
+      const float d = to_f32(xr[c]) - mu;
+      s = __builtin_fmaf(d, d, s);
+    }
+    const float rs = 1.0f / __builtin_sqrtf(block_sum<256>(s, red) / (float)N + eps);
+    for (int64_t c = threadIdx.x; c < N; c += 256) {
+      float v = (to_f32(xr[c]) - mu) * rs;
+      if (w) v *= to_f32(w[c]);
+      if (b) v += to_f32(b[c]);
+      y[r * ldy + c] = from_f32<T>(v);
+    }
+    if (threadIdx.x == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
   }
 }
 
 template <typename T, typename W>
 __global__ __launch_bounds__(256) void norm_dx_any_kernel(const T* dy, int64_t lddy, const T* x,
-                                                      int64_t ldx, const W* w,
-                                                      const float* mean, const float* rstd,
-                                                      T* dx, int64_t lddx, int64_t M,
-                                                      int64_t N) {
+                                                          int64_t ldx, const W* w,
+                                                          const float* mean, const float* rstd,
+                                                          T* dx, int64_t lddx, int64_t M,
+                                                          int64_t N) {
   __shared__ float red[4];
   for (int64_t r = blockIdx.x; r < M; r += gridDim.x) {
-  const float mu = mean[r], rs = rstd[r];
-  float s1 = 0.0f, s2 = 0.0f;
-  for (int64_t c = threadIdx.x; c < N; c += 256) {
-    const float h = to_f32(dy[r * lddy + c]) * (w ? to_f32(w[c]) : 1.0f);
-    s1 += h;
-    s2 = __builtin_fmaf(h, (to_f32(x[r * ldx + c]) - mu) * rs, s2);
-  }
-  const float c1 = block_sum<256>(s1, red) / (float)N;
-  const float c2 = block_sum<256>(s2, red) / (float)N;
-  for (int64_t c = threadIdx.x; c < N; c += 256) {
-    const float h = to_f32(dy[r * lddy + c]) * (w ? to_f32(w[c]) : 1.0f);
-    const float xh = (to_f32(x[r * ldx + c]) - mu) * rs;
-    dx[r * lddx + c] = from_f32<T>(rs * (h - c1 - xh * c2));
-  }
+    const float mu = mean[r], rs = rstd[r];
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int64_t c = threadIdx.x; c < N; c += 256) {
+      const float h = to_f32(dy[r * lddy + c]) * (w ? to_f32(w[c]) : 1.0f);
+      s1 += h;
+      s2 = __builtin_fmaf(h, (to_f32(x[r * ldx + c]) - mu) * rs, s2);
+    }
+    const float c1 = block_sum<256>(s1, red) / (float)N;
+    const float c2 = block_sum<256>(s2, red) / (float)N;
+    for (int64_t c = threadIdx.x; c < N; c += 256) {
+      const float h = to_f32(dy[r * lddy + c]) * (w ? to_f32(w[c]) : 1.0f);
+      const float xh = (to_f32(x[r * ldx + c]) - mu) * rs;
+      dx[r * lddx + c] = from_f32<T>(rs * (h - c1 - xh * c2));
+    }
   }
 }
 
 // one partial row [dw | db] of fp32 per block of rows
 template <typename T>
 __global__ __launch_bounds__(256) void norm_cols_any_kernel(const T* dy, int64_t lddy, const T* x,
-                                                        int64_t ldx, const float* mean,
-                                                        const float* rstd, float* part,
-                                                        int64_t M, int64_t N, int64_t Np, int64_t rows) {
+                                                            int64_t ldx, const float* mean,
+                                                            const float* rstd, float* part,
+                                                            int64_t M, int64_t N, int64_t Np,
+                                                            int64_t rows) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= N) return;
   const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = r0 + rows < M ? r0 + rows : M;
@@ -155,6 +158,14 @@ __device__ inline float inv_root(float v) {
   return v < 1.17549435e-38f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
 }
 
+// Forward: the row is read once; the variance is the mean of squared differences from the mean,
+// both over registers.  All workgroups are resident and walk over the rows with the next row's
+// loads in flight.  Bound by memory, and closely behind by the arithmetic around the two
+// reductions (a wave takes about 200 instructions a row of 512): [220000, 512] bf16, 450 MB,
+// 84 us = 5.4 TB/s (469 us with one element at a time in three passes; 90 us with w and b read
+// again for every row and IEEE divisions); one row of 4096 under 5 us, most of it the launch.
+// Rows above 1024 columns are spread over waves (one barrier a reduction): with 4 or 8 chunks a
+// thread instead of 2, one row of 14336 bf16 takes 8.0 us, not 5.5.
 template <typename T, typename W, int G, int EC>
 __global__ __launch_bounds__(G > 256 ? G : 256) void norm_fwd_kernel(
     const T* x, int64_t ldx, const W* w, const W* b, T* y, int64_t ldy, float* mean, float* rstd,
@@ -243,7 +254,12 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_fwd_kernel(
 // Backward: one pass over dy and x.  A workgroup of 1024 threads walks its share of the rows,
 // 1024 / G at a time; each thread keeps the sums dy xh and dy of its own columns in registers,
 // and the row groups of the workgroup add theirs through LDS at the end, in a fixed order, to
-// one partial row [dw | db] (dw and db themselves where there is one workgroup).
+// one partial row [dw | db] (dw and db themselves where there is one workgroup).  Bound by
+// memory: [220000, 512] bf16, 676 MB, 117 us = 5.8 TB/s, of it 4 us for the partial rows' sums
+// (963 us as two passes of single elements); [16384, 4096] fp16 with fp32 w 77 us = 5.2 TB/s;
+// [8191, 1023] fp32, rows at any 4-byte boundary, 28 us.  One workgroup a CU keeps the partial
+// rows few: they cost 8 N bytes a workgroup twice, which shows where rows are few and wide
+// ([1000, 8192] bf16: 25 us with dw and db, 11 us without).
 template <typename T, typename W, int G, int EC>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part, int64_t Np) {
   constexpr int ROWS = 1024 / G;

@@ -730,6 +730,14 @@ template <typename T, int NT, int GU, int SLOTS> struct RowShape {
 // One row, or one segment of it (blockIdx.y of gridDim.y, `seg` chunks each, whole passes), by a
 // workgroup of NT threads.  A segment leaves its sums in the workspace; join_kernel finishes the
 // row.
+//
+// 4096 x 131072 bf16 (1.07 GB): 165 us = 6.5 TB/s without top entries, bound by memory with the
+// arithmetic (36 issue cycles an element and wave, 16 of them the exponential) at three quarters
+// of that; 202 us with 64.  The selection is latency: barriers, a second read of the chosen
+// groups, and their order, about 10 us a row behind 25 us of stream, so four rows share a CU (256
+// threads a row; two rows of 512 threads take 223 us, a fifth row costs spills: 238 us).  1021 x
+// 50021 fp32 with 5: 48 us = 4.2 TB/s.  Keeping the k best by insertion or by repeated maxima
+// instead reads the row k times: 36.8 ms.
 template <typename T, int NT, int GU, int SLOTS, int MODE, int TOP, bool ENT>
 __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, Soft* part,
                                                      float* part_max, int64_t row_max) {
@@ -867,7 +875,9 @@ __global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, S
 }
 
 // Joins a row's segments (at most 64) and selects its top entries from the group maxima they
-// left (`row_max` a row).
+// left (`row_max` a row).  One row of 131072 bf16 with 20 entries: 4.4 us for the segments and
+// 12 us here, most of it code that is fetched for the first time and waits for four loads in a
+// row; with a selection in each segment and the join of their best 27 us together.
 template <typename T, int GU, int SLOTS, int MODE, int TOP>
 __global__ __launch_bounds__(256, 4) void join_kernel(VocabArgs a, int split, const Soft* part,
                                                       const float* part_max, int64_t row_max) {
@@ -988,7 +998,11 @@ __device__ inline void teacher_store(const TeacherLds& l, const VocabArgs& a, T*
   }
 }
 
-// A workgroup forms one of `split` segments of a row, `seg` chunks each.
+// A workgroup forms one of `split` segments of a row, `seg` chunks each.  Bound by memory:
+// [2048, 65536] bf16 log probabilities, 537 MB, 89 us = 6.0 TB/s; [2047, 50021] bf16 with 32
+// teacher entries into rows that start anywhere, 410 MB, 86 us = 4.8 TB/s (82 us where both
+// rows start at lines; 102 us without the passes' start at a line and the loads ahead, 2.9 ms
+// with a search of the entries for every column).
 template <typename T, int NT, int MODE>
 __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_t seg) {
   constexpr int U = Pass<T>::U;
@@ -1123,7 +1137,13 @@ __device__ inline float uniform(float v) {
 
 // ------------------------------------------------------------------ distillation in one pass
 // Loss, lse and gradient of a row that a workgroup holds in registers, D chunks a thread: the
-// logits are read once.
+// logits are read once.  4096 x 131072 bf16 with 64 teacher entries (2.15 GB): 457 us = 4.7 TB/s,
+// against 532 us for the two kernels that read them twice.  A row of that length takes a CU's
+// registers (1024 threads, 16 chunks each, beside 64 registers for the rest), so its load, its
+// sums and its stores follow each other, and memory rests while the sums are formed; loading the
+// next row behind the stores, or forming its sums there as well, came to 455 and 494 us (a wait
+// for a load waits for the stores before it too).  Rows of half the length share a CU:
+// 2500 x 65536 132 us = 5.0 TB/s, 177 us for the two kernels.
 template <typename T, int NT, int D, int WAVES>
 __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
   __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
