@@ -232,6 +232,14 @@ __host__ __device__ inline int top_groups(int k) { return k + k / 8 + 8; }
 // a tile's, the best k so far and the row's single elements
 __host__ __device__ inline int top_candidates(int k) { return 2 * k + kSlack + 16; }
 
+// The thread's number as a value the compiler cannot compute ahead: what the selection derives
+// from it would otherwise wait in registers through the stream of every row.
+__device__ inline int late_thread() {
+  int t = (int)threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 template <int NT> struct TopState {
   uint32_t* glist;   // chosen groups
   u64* cand;         // candidates
@@ -259,13 +267,14 @@ template <int NT> __device__ inline int block_count(int wave_count, int* count, 
 
 // smallest and largest over the workgroup; a barrier
 template <int NT> __device__ inline void block_bounds(float& lo, float& hi, int* count) {
+  const int tid = late_thread();
   lo = -wave_max(-lo);
   hi = wave_max(hi);
   if constexpr (NT > 64) {
     float* c = reinterpret_cast<float*>(count + 4 + 2 * (NT / 64));
-    if ((threadIdx.x & 63) == 0) {
-      c[(threadIdx.x >> 6) * 2] = lo;
-      c[(threadIdx.x >> 6) * 2 + 1] = hi;
+    if ((tid & 63) == 0) {
+      c[(tid >> 6) * 2] = lo;
+      c[(tid >> 6) * 2 + 1] = hi;
     }
     __syncthreads();
 #pragma unroll
@@ -298,8 +307,9 @@ struct Bins {
 // them if bins.at(v) < limit); returns how many they hold, 0 if all together hold fewer.  Every
 // wave scans by itself, kBins / 64 bins to a lane.
 __device__ inline int hist_bound(const uint32_t* hist, int k, float& limit) {
+  const int tid = late_thread();
   constexpr int PER = kBins / 64;
-  const int lane = threadIdx.x & 63;
+  const int lane = tid & 63;
   int c[PER], sum = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -356,12 +366,13 @@ __device__ inline int bisect(F count_from, int n, int k, int most, K hi, int* co
 // with one.  The rank of a key is the number of larger ones: a wave takes 64 keys against a
 // share of all of them.
 template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n) {
+  const int tid = late_thread();
   constexpr int WAVES = NT / 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = tid & 63, wave = tid >> 6;
   const int blocks = (n + 63) / 64;
   const int parts = blocks > 0 && blocks <= WAVES ? WAVES / blocks : 1;
   if (parts == 1) {
-    for (int i = threadIdx.x; i < n; i += NT) {
+    for (int i = tid; i < n; i += NT) {
       const u64 key = w.cand[i];
       int rank = 0;
 #pragma unroll 8
@@ -397,14 +408,15 @@ template <int NT> __device__ inline void order_top(const TopState<NT>& w, int n)
 template <typename T, int NT, int U, int GU, int SLOTS>
 __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, const T* body,
                                     int64_t first, int64_t t0, int64_t t1) {
+  const int tid = late_thread();
   constexpr int NS = SLOTS / NT;
   const int k = w.k, most = top_groups(k);
   const int chunks = (int)(t1 - t0);
   auto exists = [&](int j) {
-    return j * (NT * (GU == 1 ? 1 : U)) + (int)threadIdx.x < chunks;
+    return j * (NT * (GU == 1 ? 1 : U)) + tid < chunks;
   };
   // read from LDS where it is used: 16 of them in registers take a wave a SIMD
-  auto gv = [&](int j) { return exists(j) ? gmax[j * NT + threadIdx.x] : neg_inf(); };
+  auto gv = [&](int j) { return exists(j) ? gmax[j * NT + tid] : neg_inf(); };
   const int groups = GU == 1 ? chunks
                              : chunks / (NT * U) * NT +
                                    (chunks % (NT * U) < NT ? chunks % (NT * U) : NT);
@@ -419,7 +431,7 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
   // largest lie at least k; threads with nothing but masked entries do not count
   float hi = largest, lo = k <= NT ? largest : least;
   if (lo == neg_inf()) lo = __builtin_inff();
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     w.count[1] = 0;
     w.count[2] = -1;
   }
@@ -457,7 +469,7 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
     const float v = gv(j);
     if (!exists(j)) break;
     if (by_value ? v >= lo && bins.at(v) < limit : value_key(v) >= bound + ties) {
-      w.glist[atomicAdd(&w.count[1], 1)] = (uint32_t)(j * NT + threadIdx.x);
+      w.glist[atomicAdd(&w.count[1], 1)] = (uint32_t)(j * NT + tid);
       if (by_value) atomicMin(reinterpret_cast<uint32_t*>(&w.count[2]), value_key(v));
     }
   }
@@ -470,7 +482,7 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
   auto passes = [&](float v) { return !(v < next); };
   const int chosen = w.count[1];
   auto each_chunk = [&](auto use) {   // of the chosen groups
-    for (int i = threadIdx.x; i < chosen * GU; i += NT) {
+    for (int i = tid; i < chosen * GU; i += NT) {
       const int g = (int)w.glist[i / GU], u = i % GU;
       const int q = GU == 1 ? g : (g / NT) * (NT * U) + u * NT + g % NT;
       if (q >= chunks) continue;
@@ -515,7 +527,7 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
       });
       return (int)lanes_sum<64>((float)c);
     }, have - before, k, k + kSlack, ~0ull, w.count, lowest);
-    if (threadIdx.x == 0) w.count[0] = before;
+    if (tid == 0) w.count[0] = before;
     __syncthreads();
   }
   if (!ties) return;
@@ -523,7 +535,7 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
   int need = k - (w.count[0] - before);
   int half = 0;
   for (int64_t base = t0; base < t1 && need > 0; base += NT) {
-    const int64_t q = base + threadIdx.x;
+    const int64_t q = base + tid;
     float f[8];
     int equal = 0;
     if (q < t1) {
@@ -538,14 +550,14 @@ __device__ inline void collect_tile(const TopState<NT>& w, const float* gmax, co
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(incl, d);
-      if ((int)(threadIdx.x & 63) >= d) incl += o;
+      if ((tid & 63) >= d) incl += o;
     }
     const int wave_total = __shfl(incl, 63);
     const int total = block_count<NT>(wave_total, w.count, half);
     int rank = incl - equal;
     if constexpr (NT > 64) {
       const int* c = w.count + 4 + (half ^ 1) * (NT / 64);
-      for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) rank += c[i];
+      for (int i = 0; i < (tid >> 6); ++i) rank += c[i];
     }
     if (q < t1 && equal) {
 #pragma unroll
@@ -733,13 +745,13 @@ template <typename T, int NT, int GU, int SLOTS> struct RowShape {
 //
 // 4096 x 131072 bf16 (1.07 GB): 165 us = 6.5 TB/s without top entries, bound by memory with the
 // arithmetic (36 issue cycles an element and wave, 16 of them the exponential) at three quarters
-// of that; 202 us with 64.  The selection is latency: barriers, a second read of the chosen
-// groups, and their order, about 10 us a row behind 25 us of stream, so four rows share a CU (256
-// threads a row; two rows of 512 threads take 223 us, a fifth row costs spills: 238 us).  1021 x
+// of that; 201 us with 64.  The selection is latency: barriers, a second read of the chosen
+// groups, and their order, about 10 us a row behind 30 us of stream, so five rows share a CU (256
+// threads a row; two rows of 512 threads take 223 us, four of 256 204 us).  1021 x
 // 50021 fp32 with 5: 48 us = 4.2 TB/s.  Keeping the k best by insertion or by repeated maxima
 // instead reads the row k times: 36.8 ms.
 template <typename T, int NT, int GU, int SLOTS, int MODE, int TOP, bool ENT>
-__global__ __launch_bounds__(NT, 4) void rows_kernel(VocabArgs a, int64_t seg, Soft* part,
+__global__ __launch_bounds__(NT, 5) void rows_kernel(VocabArgs a, int64_t seg, Soft* part,
                                                      float* part_max, int64_t row_max) {
   using Shape = RowShape<T, NT, GU, SLOTS>;
   constexpr int U = Shape::U;
