@@ -641,6 +641,8 @@ __device__ inline float kl_term(const Teacher& t, const RowStat& st, float u, fl
 // ------------------------------------------------------------------ forward
 enum { kLogprobs = 0, kDistill = 1 };
 
+constexpr int64_t kIgnored = -2;
+
 // The results of one row from its sums and, in falling order, its k best keys (null for none).
 template <typename T, int NT, int MODE>
 __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum,
@@ -652,9 +654,8 @@ __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum
       if (a.lse) a.lse[r] = st.lse;
       if (a.entropy) a.entropy[r] = st.entropy;
       if (a.target) {
-        // mine.id: the target, -1 where it lies outside the vocabulary
         float lp = __builtin_nanf("");
-        if (a.target[r] == a.ignore) lp = 0.0f;
+        if (mine.id == kIgnored) lp = 0.0f;
         else if (mine.id >= 0) lp = log_prob(st, z_mine, a.inv_t);
         a.logprob[r] = lp;
       }
@@ -683,13 +684,15 @@ __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum
   }
 }
 
-// what a thread reads of a row ahead of the stream: the target, or its first teacher entry
+// what a thread reads of a row ahead of the stream: the target (-1 outside the vocabulary,
+// kIgnored), or its first teacher entry
 template <int MODE> __device__ inline Entry row_entry(const VocabArgs& a, int64_t r) {
   if constexpr (MODE == kLogprobs) {
     Entry e{-1, neg_inf()};
     if (a.target && threadIdx.x == 0) {
       const int64_t id = a.target[r];
       if (id >= 0 && id < a.V) e.id = id;
+      if (id == a.ignore) e.id = kIgnored;
     }
     return e;
   } else {
