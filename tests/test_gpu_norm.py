@@ -233,3 +233,24 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         for a, c in zip(got, (y, mean, rstd, dx, dw, db)):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("N", [5, 24])
+def test_more_rows_than_workgroups(N):
+    """More than 2^20 rows, repeating with an odd period."""
+    period, M = 1009, (1 << 20) + 5000
+    note(f"layer norm rows {M} N={N}")
+    x1, dy1, w, b = make(period, N, BF16, FP32, seed=8)
+    i = torch.arange(M, device=x1.device) % period
+    x, dy = x1[i], dy1[i]
+    y1, m1, r1 = swg.layer_norm_fwd(x1, w, b, eps=EPS)
+    check_fwd(x1, w, b, y1, m1, r1)
+    y, m, r = swg.layer_norm_fwd(x, w, b, eps=EPS)
+    assert torch.equal(y, y1[i]) and torch.equal(m, m1[i]) and torch.equal(r, r1[i])
+    dx1, dx = torch.empty_like(x1), torch.empty_like(x)
+    dw, db = torch.empty_like(w), torch.empty_like(b)
+    swg.layer_norm_bwd(dy1, x1, w, m1, r1, dx1, None, None)
+    check_bwd(dy1, x1, w, m1, r1, dx1, None, None)
+    swg.layer_norm_bwd(dy, x, w, m, r, dx, dw, db)
+    assert torch.equal(dx, dx1[i])
+    check_bwd(dy, x, w, m, r, None, dw, db)

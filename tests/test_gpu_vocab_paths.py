@@ -208,3 +208,33 @@ def test_gradients_of_segments(rows, V, dt):
     loss, lse = swg.distill_fwd(z, u, ids)
     dz = swg.distill_bwd(z, u, ids, lse, c)
     check_distill(z, u, ids, 1.0, loss=loss, lse_out=lse, lse_in=lse, c=c, dz=dz, rows=sel)
+
+
+def test_more_rows_than_workgroups():
+    """A launch holds 2^20 workgroups; the rows repeat with an odd period, so a row that a
+    wrapped workgroup took for another would show.  Rows of 20 bf16 start at every other 8 bytes,
+    and the order of a row's sums goes by that: two periods are compared with."""
+    period, V, k = 1009, 20, 3
+    rows = (1 << 20) + 5000
+    note(f"rows {rows}")
+    z1, t1 = logits(period, V, BF16, seed=46), targets_for(period, V)
+    u1, ids1 = teacher(period, V, k)
+    c1 = torch.rand(period, device=z1.device) + 0.5
+    z1, t1, u1, ids1, c1 = (torch.cat((a, a)) for a in (z1, t1, u1, ids1, c1))
+    i = torch.arange(rows, device=z1.device) % (2 * period)
+    z, t, u, ids, c = (a[i].contiguous() for a in (z1, t1, u1, ids1, c1))
+    r1, r = (swg.token_logprobs(a, b, top=k) for a, b in ((z1, t1), (z, t)))
+    check_logprobs(z1, t1, r1, 1.0, k)
+    for a, b in zip(r, r1):
+        assert torch.equal(a, b[i])
+    g1, h1 = torch.randn(2, 2 * period, device=z.device)
+    d1 = swg.token_logprobs_bwd(z1, t1, r1.lse, r1.entropy, g1, h1)
+    d = swg.token_logprobs_bwd(z, t, r.lse, r.entropy, g1[i], h1[i])
+    assert torch.equal(d, d1[i])
+    one, many = (swg.distill_fwd_bwd(*a) for a in ((z1, u1, ids1, c1), (z, u, ids, c)))
+    check_distill(z1, u1, ids1, 1.0, loss=one[0], lse_out=one[1], lse_in=one[1], c=c1, dz=one[2])
+    for a, b in zip(many, one):
+        assert torch.equal(a, b[i])
+    d1 = swg.distill_bwd(z1, u1, ids1, one[1], c1)
+    d = swg.distill_bwd(z, u, ids, many[1], c)
+    assert torch.equal(d, d1[i])
