@@ -310,7 +310,9 @@ inline NormPlan plan_norm_bwd(int64_t M, int64_t N) {
   NormPlan p{};
   p.np = ceil_div(N, 4) * 4;
   if (N < 8 || N > 16384) {
-    p.rows = M > 256 * 64 ? ceil_div(M, 256) : 64;
+    // one thread walks a block of narrow rows: many short blocks
+    const int64_t least = N < 8 ? 16 : 64, blocks = N < 8 ? 8192 : 256;
+    p.rows = M > blocks * least ? ceil_div(M, blocks) : least;
     p.parts = ceil_div(M, p.rows);
     p.ws_bytes = (size_t)p.parts * 2 * (size_t)p.np * sizeof(float);
     return p;
