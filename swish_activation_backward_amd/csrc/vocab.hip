@@ -143,7 +143,9 @@ __device__ inline void run_single(Run& a, float x, float c) {
   a.m = __builtin_fmaxf(a.m, x);
   const float top = x * c;
   if (top - a.b > kLift) run_move(a, top);
-  const float d = top - a.b, e = __builtin_amdgcn_exp2f(d);
+  // not top - b: the product's rounding, half a unit of the last place of top, would stay in d
+  // here and not in the chunks' d
+  const float d = __builtin_fmaf(x, c, -a.b), e = __builtin_amdgcn_exp2f(d);
   a.s += e;
   a.t = __builtin_fmaf(bound_d(d), e, a.t);
 }
