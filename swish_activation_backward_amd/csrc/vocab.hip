@@ -83,11 +83,16 @@ struct Run {
   float b, m, s, t;
 };
 constexpr float kLift = 4.0f;
-constexpr float kNoRef = -1e30f;
-// z c has to stay far from overflow and from kNoRef: otherwise the row's sums are formed again
-// in the differences z - m
+// b is a rounded product, and the rounding, up to half a unit of its last place, remains in the d
+// of the element it comes from: harmless while it is a few units, as the sums are relative to b
+// as it is.  At -1e10 it reaches 512, where 2^d is infinite or 0.  So a value far below (a finite
+// mask) takes no part in the reference: its chunk leaves b where it was, at least kNoRef = -2^28
+// (2^d <= 2^8 there), and adds 0.  A row whose maximum has |m c| >= kRange = 2^26 (all of it
+// masked, or T tiny) has its sums formed again in the differences z - m.
+constexpr float kNoRef = -268435456.0f;
+constexpr float kRange = 67108864.0f;
 __device__ inline bool run_in_range(float m, float c) {
-  return __builtin_fabsf(m * c) < 1e29f || __builtin_fabsf(m) == __builtin_inff();
+  return __builtin_fabsf(m * c) < kRange || __builtin_fabsf(m) == __builtin_inff();
 }
 
 __device__ inline void run_move(Run& a, float b) {

@@ -1,5 +1,8 @@
-"""Logits far from the ordinary range."""
+"""Logits far from the ordinary range: large finite masks, rows of large values, tiny
+temperatures."""
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -7,7 +10,7 @@ import torch
 import swish_activation_backward_amd as swg
 from gpu_util import device, note
 from logit_range_models import check_forward, check_loss
-from test_gpu_vocab import BF16, FP32, teacher
+from test_gpu_vocab import BF16, DTYPES, FP32, logits, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +35,66 @@ def test_rows_of_large_equal_values(value, dt):
             c = torch.ones(3, device=z.device)
             loss, lse, dz = swg.distill_fwd_bwd(z, u, ids, c)
             check_loss(z, u, ids, 1.0, loss, lse, c, dz)
+
+
+# ------------------------------------------------------------------ large finite masks
+MASKS = [(-1e8, 1.0), (-1e9, 1.0), (-1e9, 0.1), (-1e10, 1.0), (-1e10, 2.0), (-1e12, 1.0),
+         (-1e15, 2.0), (-1e20, 1.0), (-1e20, 0.1), (-1e25, 1.0), (-1e30, 2.0), (-1e30, 0.1)]
+# one workgroup a row, segments, rows held in registers, two tiles
+FORMS = [(3000, 7), (20000, 7), (20000, 518), (131072, 7), (131072, 518), (140001, 518)]
+
+
+def masked_kinds(V, dt, mask, seed=0):
+    """Seven rows: the first third masked, the last third, everything, everything but one entry,
+    every second entry, every second chunk, and masked entries beside -inf."""
+    z = logits(7, V, dt, seed=seed).clone()
+    i = torch.arange(V, device=z.device)
+    z[0, : V // 3] = mask
+    z[1, V - V // 3:] = mask
+    z[2] = mask
+    z[3] = mask
+    z[3, V // 2] = 1.5
+    z[4, i % 2 == 0] = mask
+    z[5, i // 8 % 2 == 0] = mask
+    z[6] = -math.inf
+    z[6, : V // 2] = mask
+    return z
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("V,rows", FORMS)
+def test_large_finite_masks(V, rows, dt):
+    top, k = 20, 6
+    for mask, T in MASKS if V < 100000 else MASKS[2:4] + MASKS[7:11:3]:
+        note(f"mask {mask} T={T} V={V} rows={rows} {dt}")
+        kinds = masked_kinds(V, dt, mask)
+        i = torch.arange(rows, device=kinds.device) % 7
+        z = kinds[i].contiguous()
+        t = torch.tensor([1, V - 2, 3, V // 2, 5, 9, 4], device=z.device)
+        r = swg.token_logprobs(z, t[i], top=top, temperature=T)
+        check_forward(kinds, t, swg.TokenLogprobs(*(v[:7] for v in r)), T, top)
+        u, ids = teacher(7, V, k, pads=False)
+        c = torch.rand(7, device=z.device) + 0.5
+        loss, lse = swg.distill_fwd(z, u[i], ids[i], temperature=T)
+        check_loss(kinds, u, ids, T, loss[:7], lse[:7])
+        both = swg.distill_fwd_bwd(z, u[i], ids[i], c[i], temperature=T)
+        check_loss(kinds, u, ids, T, both[0][:7], both[1][:7], c, both[2][:7])
+        for a in (*r, loss, lse, *both):
+            assert not bool(torch.isnan(a).any())
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T", [1e-3, 1e-6, 1e-9, 1e-30])
+@pytest.mark.parametrize("V,rows", [(3000, 5), (20000, 5), (20000, 518), (140001, 5)])
+def test_tiny_temperatures(V, rows, dt, T):
+    """Ordinary logits: almost all of a row's probability lies on its largest entries."""
+    note(f"temperature {T} V={V} rows={rows} {dt}")
+    z = logits(rows, V, dt, seed=50)
+    t = z.float().argmax(1)
+    r = swg.token_logprobs(z, t, top=9, temperature=T)
+    check_forward(z[:5], t[:5], swg.TokenLogprobs(*(v[:5] for v in r)), T, 9)
+    # a teacher of one entry (loss = -T^2 log p) and weights that keep T^2 and c T in range
+    u = torch.zeros(rows, 1, device=z.device)
+    c = torch.full((rows,), min(1.0 / T, 1e30), device=z.device)
+    both = swg.distill_fwd_bwd(z, u, t[:, None].contiguous(), c, temperature=T)
+    check_loss(z[:5], u[:5], t[:5, None], T, both[0][:5], both[1][:5], c[:5], both[2][:5])
