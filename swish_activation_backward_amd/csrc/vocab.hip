@@ -300,8 +300,10 @@ struct Bins {
   __device__ inline Bins(float lo, float hi_) : hi(hi_) {
     scale = (float)(kBins - 1) / (hi - lo);
   }
+  // scale is 0 where hi - lo leaves fp32: values then have no bin
   __device__ inline bool usable(float lo) const {
-    return lo > neg_inf() && lo < hi && hi < __builtin_inff() && scale < __builtin_inff();
+    return lo > neg_inf() && lo < hi && hi < __builtin_inff() && scale > 0.0f &&
+           scale < __builtin_inff();
   }
   __device__ inline float at(float v) const { return (hi - v) * scale; }
   __device__ inline void add(uint32_t* hist, float v) const {

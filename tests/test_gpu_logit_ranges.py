@@ -1,15 +1,18 @@
 """Logits far from the ordinary range: large finite masks, rows of large values, tiny
-temperatures."""
+temperatures, values whose difference leaves fp32."""
 from __future__ import annotations
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
+import oracle.ref as R
 import swish_activation_backward_amd as swg
 from gpu_util import device, note
 from logit_range_models import check_forward, check_loss
+from parity import to64
 from test_gpu_vocab import BF16, DTYPES, FP32, logits, teacher
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +101,25 @@ def test_tiny_temperatures(V, rows, dt, T):
     c = torch.full((rows,), min(1.0 / T, 1e30), device=z.device)
     both = swg.distill_fwd_bwd(z, u, t[:, None].contiguous(), c, temperature=T)
     check_loss(z[:5], u[:5], t[:5, None], T, both[0][:5], both[1][:5], c[:5], both[2][:5])
+
+
+# ------------------------------------------------------------------ selections
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("V,rows", [(131072, 3), (131072, 515), (30000, 515), (20000, 3)])
+def test_selection_over_a_range_beyond_fp32(V, rows, dt):
+    """The largest entry less the type's lowest value leaves fp32; few groups hold any entry
+    that is not masked."""
+    top, n = 20, 26
+    low = torch.finfo(dt).min
+    z = torch.full((rows, V), -math.inf, dtype=dt, device=device())
+    at = torch.arange(n, device=z.device) * (V // n) + 3 * torch.arange(n, device=z.device)
+    z[:, at] = low
+    z[:, at[5::10]] = 3e38
+    z[1] = -math.inf          # other ids than the rows around it
+    z[1, at + 1] = low
+    z[1, at[2::9] + 1] = 2e38
+    note(f"selection range V={V} rows={rows} {dt}")
+    got = swg.token_logprobs(z, None, top=top).top_id.cpu().numpy()
+    want = R.top_ref(to64(z[:3]), top)
+    assert np.array_equal(got[:3], want)
+    assert np.array_equal(got[3:], np.broadcast_to(want[0], got[3:].shape))
