@@ -751,6 +751,33 @@ template <typename T, int NT, int GU, int SLOTS> struct RowShape {
   static constexpr int64_t TILE = ITERS * PASS;
 };
 
+// The thread's group maxima over chunks [t0, t1) of `body`, in their places from `out` on, by
+// comparisons that pass over NaN.
+template <typename T, int NT, int U, int GU>
+__device__ inline void remake_groups(float* out, const T* body, int64_t t0, int64_t t1) {
+  const int tid = late_thread(), chunks = (int)(t1 - t0);
+#pragma unroll 1
+  for (int base = 0; base < chunks; base += NT * U) {
+    float group = neg_inf();
+#pragma unroll 1
+    for (int u = 0; u < U; ++u) {
+      float gm = neg_inf();
+      const int q = base + u * NT + tid;
+      if (q < chunks) {
+        Chunk<T> c;
+        c.load(body + (t0 + q) * 8);
+        float f[8];
+        c.widen(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gm = f[i] > gm ? f[i] : gm;
+      }
+      if constexpr (GU == 1) out[q] = gm;
+      group = gm > group ? gm : group;
+    }
+    if constexpr (GU > 1) out[base / U + tid] = group;
+  }
+}
+
 // One row, or one segment of it (blockIdx.y of gridDim.y, `seg` chunks each, whole passes), by a
 // workgroup of NT threads.  A segment leaves its sums in the workspace; join_kernel finishes the
 // row.
@@ -836,7 +863,7 @@ __global__ __launch_bounds__(NT, 5) void rows_kernel(VocabArgs a, int64_t seg, S
           cur[u].widen(f);
           float gm = max8(f);
           if constexpr (TOP != kNoTop) {
-            // only a signaling NaN or 8 NaN come out as NaN; of the others the largest counts
+            // 8 NaN come out as NaN; what others may hide is looked for behind the loop
             if (gm != gm) {
               gm = neg_inf();
 #pragma unroll
@@ -853,6 +880,14 @@ __global__ __launch_bounds__(NT, 5) void rows_kernel(VocabArgs a, int64_t seg, S
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) cur[u] = next[u];
+      }
+      if constexpr (TOP != kNoTop) {
+        // A NaN may have hidden others of its chunk from max8 (the maximum with a signaling NaN is
+        // NaN, the next one drops it).  It is in the thread's sum, and the groups are formed again.
+        if (sum.s != sum.s) {
+          float* out = TOP == kTop ? gmax : part_max + r * row_max + t0 / GU;
+          remake_groups<T, NT, U, GU>(out, body, t0, t1);
+        }
       }
       if constexpr (TOP == kTop) {
         collect_tile<T, NT, U, GU, SLOTS>(w, gmax, body, cut.head, t0, t1);

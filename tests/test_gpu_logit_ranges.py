@@ -1,5 +1,5 @@
 """Logits far from the ordinary range: large finite masks, rows of large values, tiny
-temperatures, values whose difference leaves fp32."""
+temperatures, values whose difference leaves fp32, signaling NaN."""
 from __future__ import annotations
 
 import math
@@ -13,7 +13,7 @@ import swish_activation_backward_amd as swg
 from gpu_util import device, note
 from logit_range_models import check_forward, check_loss
 from parity import to64
-from test_gpu_vocab import BF16, DTYPES, FP32, logits, teacher
+from test_gpu_vocab import BF16, DTYPES, FP16, FP32, logits, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,25 @@ def test_selection_over_a_range_beyond_fp32(V, rows, dt):
     want = R.top_ref(to64(z[:3]), top)
     assert np.array_equal(got[:3], want)
     assert np.array_equal(got[3:], np.broadcast_to(want[0], got[3:].shape))
+
+
+SIGNALING = {BF16: (torch.int16, 0x7F81), FP16: (torch.int16, 0x7C01),
+             FP32: (torch.int32, 0x7F800001)}
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("V,rows", [(3000, 4), (20000, 4), (20000, 515), (140001, 4)])
+def test_signaling_nan_among_the_best(V, rows, dt):
+    """Any NaN ranks with -inf; the entries around it keep their order."""
+    top = 12
+    z = logits(rows, V, dt, seed=53)
+    itype, bits = SIGNALING[dt]
+    i = torch.arange(0, V - 16, V // 9, device=z.device) // 8 * 8
+    for e in range(8):   # the best entries beside a NaN, in every place of a chunk
+        z[0, i[e] + torch.arange(8, device=z.device)] = 20.0 + e
+        z.view(itype)[0, i[e] + e] = bits
+        z.view(itype)[2, i[e] + (e + 3) % 8] = bits
+        z[2, i[e] + e] = 30.0 - e
+    note(f"signaling nan V={V} rows={rows} {dt}")
+    ids = swg.token_logprobs(z, None, top=top).top_id[:4].cpu().numpy()
+    assert np.array_equal(ids, R.top_ref(to64(z[:4]), top))
