@@ -319,9 +319,9 @@ size_t token_logprobs_workspace_size(int64_t R, int64_t V, int64_t top, swg_dtyp
  * for g = dlogprob[r] (0 where t = ignore_index; a row whose t is any other id outside
  * [0, V) gets NaN), h = dentropy[r].  targets and dlogprob may both be NULL (g = 0), entropy
  * and dentropy may both be NULL (h = 0).  Masked entries (p = 0) get 0, or g at the target.
- * p = exp(a - lse) from the fp32 lse: where |a| is so large that lse has no room beside it for
- * log sum exp (a - max a), as in a row of nothing but the lowest finite number, the p of a row
- * do not sum to 1.  dlogits: dtype, row stride ldd, overwritten; it may be exactly logits (same
+ * p = exp(min(a - lse, 0)) from the fp32 lse: where |a| is so large that lse has no room beside
+ * it for log sum exp (a - max a), as in a row of nothing but a large finite mask or at a tiny
+ * temperature, each p stays in [0, 1] but the p of a row do not sum to 1.  dlogits: dtype, row stride ldd, overwritten; it may be exactly logits (same
  * pointer and stride).
  */
 swg_status token_logprobs_bwd(const void* logits, int64_t ld, const int64_t* targets,

@@ -1136,8 +1136,10 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
       teacher_fill<T, NT>(lds, a, r, z, t, mine, z_mine, from, to);
       __syncthreads();   // all entries' logits are read
     }
-    auto value = [&](float x) {   // log p
-      return __builtin_fmaf(x - m, a.inv_t, -ls);
+    // log p: at most 0, also where lse is too coarse beside a large |x| / T, so that p stays a
+    // probability.  A NaN stays one.
+    auto value = [&](float x) {
+      return __builtin_elementwise_minimum(__builtin_fmaf(x - m, a.inv_t, -ls), 0.0f);
     };
     auto prob = [&](float x) { return __builtin_amdgcn_exp2f(value(x) * kLog2e); };
     auto at_target = [&](float x) {

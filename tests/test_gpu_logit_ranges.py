@@ -1,5 +1,6 @@
 """Logits far from the ordinary range: large finite masks, rows of large values, tiny
-temperatures, values whose difference leaves fp32, signaling NaN."""
+temperatures, values whose difference leaves fp32, signaling NaN, and gradients
+from an lse that is too coarse for them."""
 from __future__ import annotations
 
 import math
@@ -145,3 +146,55 @@ def test_signaling_nan_among_the_best(V, rows, dt):
     note(f"signaling nan V={V} rows={rows} {dt}")
     ids = swg.token_logprobs(z, None, top=top).top_id[:4].cpu().numpy()
     assert np.array_equal(ids, R.top_ref(to64(z[:4]), top))
+
+
+# ------------------------------------------------------------------ gradients from the fp32 lse
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("T", [1e-9, 0.1, 0.7, 1.0])
+@pytest.mark.parametrize("V,rows", [(700, 6), (20000, 6), (70001, 6)])
+def test_gradients_stay_bounded(V, rows, dt, T):
+    """Beside a large |a| the fp32 lse has no room for log sum exp (a - max a): a probability
+    may be off, but it stays in [0, 1] and the gradients with it."""
+    note(f"bounded gradients T={T} V={V} {dt}")
+    z = logits(rows, V, dt, seed=51)
+    z[1] = -1e10
+    z[2] = -1e20
+    z[3] = 3e9
+    z[4] = z[4] * 1e8
+    t = torch.arange(rows, device=z.device)
+    r = swg.token_logprobs(z, t, temperature=T)
+    g = torch.ones(rows, device=z.device)
+    one = 1.0 + 2 * torch.finfo(dt).eps
+    # -p / T away from the target, (1 - p) / T at it
+    dz = swg.token_logprobs_bwd(z, t, r.lse, None, g, None, temperature=T).double() * T
+    at = torch.zeros(rows, V, dtype=torch.bool, device=z.device)
+    at[t, t] = True
+    assert float(dz[~at].max()) <= 0 and float(dz[~at].min()) >= -one
+    assert float(dz[at].min()) >= 0 and float(dz[at].max()) <= one
+    # -p (log p + H) / T with log p <= 0 and p (-log p) <= 1 / e
+    de = swg.token_logprobs_bwd(z, None, r.lse, r.entropy, None, g, temperature=T).double() * T
+    assert float(de.abs().max()) <= (math.log(V) + 1.0) * one
+    u = torch.zeros(rows, 1, device=z.device)
+    c = torch.full((rows,), 1.0 / T, device=z.device)
+    d = swg.distill_bwd(z, u, t[:, None].contiguous(), r.lse, c, temperature=T).double()
+    assert float(d[~at].min()) >= 0 and float(d.abs().max()) <= one
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("V", [40, 5000])
+def test_nan_logits_keep_their_gradient_nan(V, dt):
+    """A NaN logit beside a finite lse, and a NaN lse beside finite logits."""
+    z = logits(2, V, dt, seed=52)
+    t = torch.tensor([0, 1], device=z.device)
+    r = swg.token_logprobs(z, t)
+    at = [1, 9, V - 1]
+    z[0, at] = math.nan
+    lse = r.lse.clone()
+    lse[1] = math.nan
+    g = torch.ones(2, device=z.device)
+    u = torch.zeros(2, 1, device=z.device)
+    for dz in (swg.token_logprobs_bwd(z, t, lse, None, g, None),
+               swg.token_logprobs_bwd(z, None, lse, r.entropy, None, g),
+               swg.distill_bwd(z, u, t[:, None].contiguous(), lse, g)):
+        bad = torch.isnan(dz)
+        assert bad[0].nonzero()[:, 0].tolist() == at and bool(bad[1].all())
