@@ -600,10 +600,10 @@ __device__ inline float teacher_value(const VocabArgs& a, int64_t r, int64_t j, 
   if (a.teacher_dtype == 0) u = to_f32(static_cast<const bf16*>(a.teacher)[i]);
   else if (a.teacher_dtype == 1) u = to_f32(static_cast<const fp16*>(a.teacher)[i]);
   else u = static_cast<const float*>(a.teacher)[i];
-  return u * a.inv_t;
+  return u;
 }
 
-// An entry as the thread that reads it keeps it: id (-1: does not count) and u / T.
+// An entry as the thread that reads it keeps it: id (-1: does not count) and u.
 struct Entry {
   int64_t id;
   float u;
@@ -618,13 +618,17 @@ __device__ inline Entry load_entry(const VocabArgs& a, int64_t r, int64_t j) {
   return e;
 }
 
-// softmax over the entries: log q = u - um - lus.  `mine` is the thread's first entry, entry
-// threadIdx.x; those from NT on are read again.
+// softmax over the entries: log q = d - lus, d = (u - um) / T, from the differences, which neither
+// overflow at the type's lowest value nor lose digits beside a large one.  `mine` is the thread's
+// first entry, entry threadIdx.x, whose u becomes its d; those from NT on are read again.
 struct Teacher {
   float um, us, lus;
 };
+__device__ inline float teacher_d(const Teacher& t, const VocabArgs& a, float u) {
+  return (u - t.um) * a.inv_t;
+}
 template <int NT>
-__device__ inline Teacher teacher_softmax(const VocabArgs& a, int64_t r, const Entry& mine,
+__device__ inline Teacher teacher_softmax(const VocabArgs& a, int64_t r, Entry& mine,
                                           float* red) {
   Teacher t;
   float m = mine.u;
@@ -632,19 +636,21 @@ __device__ inline Teacher teacher_softmax(const VocabArgs& a, int64_t r, const E
     m = __builtin_fmaxf(m, load_entry(a, r, j).u);
   m = block_max<NT>(m, red);
   t.um = m == neg_inf() ? 0.0f : m;
-  float s = expf(mine.u - t.um);
-  for (int64_t j = threadIdx.x + NT; j < a.k; j += NT) s += expf(load_entry(a, r, j).u - t.um);
+  mine.u = teacher_d(t, a, mine.u);
+  float s = expf(mine.u);
+  for (int64_t j = threadIdx.x + NT; j < a.k; j += NT)
+    s += expf(teacher_d(t, a, load_entry(a, r, j).u));
   t.us = block_sum<NT>(s, red);
   t.lus = logf(t.us);
   return t;
 }
 
 // q (log q - log p) of one entry
-__device__ inline float kl_term(const Teacher& t, const RowStat& st, float u, float z,
+__device__ inline float kl_term(const Teacher& t, const RowStat& st, float d, float z,
                                 float inv_t) {
-  const float lq = u - t.um, q = expf(lq) / t.us;
+  const float q = expf(d) / t.us;
   if (t.us == 0.0f || q == 0.0f) return 0.0f;
-  return q * (lq - t.lus - log_prob(st, z, inv_t));
+  return q * (d - t.lus - log_prob(st, z, inv_t));
 }
 
 // ------------------------------------------------------------------ forward
@@ -655,7 +661,7 @@ constexpr int64_t kIgnored = -2;
 // The results of one row from its sums and, in falling order, its k best keys (null for none).
 template <typename T, int NT, int MODE>
 __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum,
-                                  const u64* best, const Entry& mine, float z_mine, float* red) {
+                                  const u64* best, Entry mine, float z_mine, float* red) {
   const T* z = static_cast<const T*>(a.z) + r * a.ld;
   const RowStat st = row_stat(sum, a.inv_t);
   if constexpr (MODE == kLogprobs) {
@@ -679,7 +685,7 @@ __device__ inline void finish_row(const VocabArgs& a, int64_t r, const Soft& sum
     float kl = mine.id >= 0 ? kl_term(t, st, mine.u, z_mine, a.inv_t) : 0.0f;
     for (int64_t j = threadIdx.x + NT; j < a.k; j += NT) {
       const Entry e = load_entry(a, r, j);
-      if (e.id >= 0) kl += kl_term(t, st, e.u, to_f32(z[e.id]), a.inv_t);
+      if (e.id >= 0) kl += kl_term(t, st, teacher_d(t, a, e.u), to_f32(z[e.id]), a.inv_t);
     }
     kl = block_sum<NT>(kl, red);
     if (threadIdx.x == 0) {
@@ -1030,11 +1036,12 @@ __device__ inline void teacher_fill(const TeacherLds& l, const VocabArgs& a, int
   for (int64_t j = threadIdx.x; j < a.k; j += NT) {
     if (j >= NT) {
       e = load_entry(a, r, j);
+      e.u = teacher_d(t, a, e.u);
       x = e.id >= from && e.id < to ? to_f32(z[e.id]) : 0.0f;
     }
     const bool counts = e.id >= 0 && t.us != 0.0f;
     l.id[j] = counts ? (int)e.id : -1;
-    l.share[j] = counts ? expf(e.u - t.um) / t.us : 0.0f;
+    l.share[j] = counts ? expf(e.u) / t.us : 0.0f;
     l.z[j] = x;
   }
 }
@@ -1217,7 +1224,10 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
     const T* body = z + cut.head;
     T* out = dz + cut.head;
     const int lone = cut.single(threadIdx.x, a.V, true, true);
-    const Entry mine = load_entry(a, r, threadIdx.x);
+    Entry mine = load_entry(a, r, threadIdx.x);
+    // waited for ahead of the row's loads: 4096 x 131072 takes 469 us where the wait comes behind
+    // them, 457 so; shorter rows are 2 to 4 % faster without
+    if constexpr (NT == 1024) asm volatile("" : "+v"(mine.u));
     const float wgt = a.dloss[r];
     const float z_lone = lone >= 0 ? to_f32(z[lone]) : 0.0f;
     // chunk u of the thread, if the row has it
@@ -1274,7 +1284,8 @@ __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
     float kl = 0.0f;
     for (int j = threadIdx.x; j < (int)a.k; j += NT)
       if (lds.id[j] >= 0)
-        kl += kl_term(t, st, j < NT ? mine.u : load_entry(a, r, j).u, lds.z[j], a.inv_t);
+        kl += kl_term(t, st, j < NT ? mine.u : teacher_d(t, a, load_entry(a, r, j).u), lds.z[j],
+                      a.inv_t);
     if constexpr (NT > 64) __syncthreads();
     kl = block_sum<NT>(kl, red);
     if (threadIdx.x == 0) {

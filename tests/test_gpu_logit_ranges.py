@@ -1,6 +1,6 @@
 """Logits far from the ordinary range: large finite masks, rows of large values, tiny
 temperatures, values whose difference leaves fp32, signaling NaN, and gradients
-from an lse that is too coarse for them."""
+from an lse that is too coarse for them; the same of a teacher's values."""
 from __future__ import annotations
 
 import math
@@ -14,6 +14,7 @@ import swish_activation_backward_amd as swg
 from gpu_util import device, note
 from logit_range_models import check_forward, check_loss
 from parity import to64
+from row_models import U
 from test_gpu_vocab import BF16, DTYPES, FP16, FP32, logits, teacher
 
 pytestmark = pytest.mark.gpu
@@ -198,3 +199,34 @@ def test_nan_logits_keep_their_gradient_nan(V, dt):
                swg.distill_bwd(z, u, t[:, None].contiguous(), lse, g)):
         bad = torch.isnan(dz)
         assert bad[0].nonzero()[:, 0].tolist() == at and bool(bad[1].all())
+
+
+# ------------------------------------------------------------------ the teacher's range
+@pytest.mark.parametrize("udt", DTYPES)
+@pytest.mark.parametrize("T", [0.5, 1.0, 4.0])
+@pytest.mark.parametrize("V", [500, 40000, 140000])
+def test_teacher_values_far_from_zero(V, T, udt):
+    """Entries of the type's lowest value (all, some) and its largest, and large values whose
+    differences count: q goes by the differences."""
+    rows, k = 6, 5
+    z = logits(rows, V, BF16, seed=54)
+    u, ids = teacher(rows, V, k, udt, pads=False)
+    ids[:] = torch.arange(k, device=z.device) * 7
+    info = torch.finfo(udt)
+    u[0] = info.min
+    u[1, 2:] = info.min
+    u[2] = info.max
+    u[3] = torch.tensor([4096.0, 4096, 4064, 4064, 4032], device=z.device).to(udt) * (
+        1 if udt == FP16 else 256)
+    u[4] = -u[3]
+    c = torch.rand(rows, device=z.device) + 0.5
+    note(f"teacher range V={V} T={T} {udt}")
+    loss, lse = swg.distill_fwd(z, u, ids, temperature=T)
+    check_loss(z, u, ids, T, loss, lse)
+    both = swg.distill_fwd_bwd(z, u, ids, c, temperature=T)
+    check_loss(z, u, ids, T, both[0], both[1], c, both[2])
+    dz = swg.distill_bwd(z, u, ids, lse, c, temperature=T)
+    # the same gradient to within the roundings of p from lse (|a| and lse below 64) and of dz
+    a, b = dz.double(), both[2].double()
+    step = torch.finfo(BF16).eps
+    assert bool(((a - b).abs() <= step * b.abs() + 512 * U * c[:, None] * T).all())
