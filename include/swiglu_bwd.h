@@ -289,7 +289,8 @@ size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
 
 /*
  * Log probabilities over rows of logits z [R, V] (dtype, row stride ld) at a temperature
- * (finite, > 0): a = z / temperature, lse = log sum exp a, p = exp(a - lse).
+ * (finite, > 0, and large enough, above 4.24e-39, that log2(e) / temperature is finite in
+ * fp32; SWG_ERR_INVALID otherwise): a = z / temperature, lse = log sum exp a, p = exp(a - lse).
  *   logprob[r] = a_t - lse for t = targets[r]; 0 for t = ignore_index; NaN for any other
  *                t outside [0, V)
  *   entropy[r] = - sum p (a - lse)

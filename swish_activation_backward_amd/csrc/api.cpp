@@ -539,10 +539,11 @@ swg_status norm_types(int dtype, int wdtype) {
   return wdtype == dtype || wdtype == SWG_FP32 ? SWG_OK : SWG_ERR_UNSUPPORTED;
 }
 
-// finite and above zero, and so is its inverse
+// finite and above zero, and so are its inverse and log2(e) / t, which the kernels multiply by
 bool temperature_ok(float t) {
   const float inv = 1.0f / t;
-  return t > 0.0f && t <= 3.4028234663852886e38f && inv > 0.0f && inv <= 3.4028234663852886e38f;
+  return t > 0.0f && t <= 3.4028234663852886e38f && inv > 0.0f &&
+         inv * 1.4426950408889634f <= 3.4028234663852886e38f;
 }
 
 // Checks shared by the operators on logits; `r0` tells that there is nothing to do.
