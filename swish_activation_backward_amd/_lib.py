@@ -156,13 +156,27 @@ def _on_device(device):
 _SAME_DEVICE = contextlib.nullcontext()
 
 
+def _check_stream(stream, device):
+    """A stream of another device cannot order work on the tensors' one."""
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device}, expected one of {device}")
+
+
 def _stream(stream, device):
     """The stream handle to launch on: ``stream``, else torch's current stream of the
     tensors' device."""
     if stream is None:
         # the handle itself: a torch.cuda.Stream object costs about a microsecond
         return torch._C._cuda_getCurrentRawStream(device.index)
+    _check_stream(stream, device)
     return stream.cuda_stream
+
+
+def _on_stream(stream, t):
+    """Context that makes ``stream`` torch's current one for a call on ``t``'s device."""
+    if isinstance(t, torch.Tensor) and t.device.type == "cuda":   # others are refused inside
+        _check_stream(stream, t.device)
+    return torch.cuda.stream(stream)
 
 
 def _check(call, status, lib):
@@ -542,7 +556,7 @@ def layer_norm_fwd(x, w, b, y=None, mean=None, rstd=None, eps=1e-5, stream=None)
     None) have x's dtype or fp32.  Returns y [M, N], and the fp32 mean and rstd [M] that
     ``layer_norm_bwd`` takes; outputs that are not given are allocated."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, x):
             return layer_norm_fwd(x, w, b, y, mean, rstd, eps)
     lib = load_library()
     shape = _matrix("x", x)
@@ -571,7 +585,7 @@ def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace
     """Gradients of ``layer_norm_fwd``: writes dx [M, N], dw and db [N] (each may be None);
     with ``accumulate`` dw and db are added to (+=)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dy):
             return layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate, workspace)
     lib = load_library()
     shape = _matrix("dy", dy)
@@ -619,7 +633,7 @@ def token_logprobs(logits, targets=None, top=0, temperature=1.0, ignore_index=-1
     ``TokenLogprobs``; ``out`` may hand back an earlier result of the same shape to be
     overwritten."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, logits):
             return token_logprobs(logits, targets, top, temperature, ignore_index, out, workspace)
     lib = load_library()
     shape = _matrix("logits", logits)
@@ -656,7 +670,7 @@ def token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogit
     dlogprob and dentropy [R] (fp32; either may be None, targets with dlogprob and entropy
     with dentropy).  ``dlogits`` [R, V] may be ``logits`` itself; it is returned."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, logits):
             return token_logprobs_bwd(logits, targets, lse, entropy, dlogprob, dentropy, dlogits,
                                       temperature, ignore_index)
     lib = load_library()
@@ -706,7 +720,7 @@ def distill_fwd(logits, top, top_ids, temperature=1.0, loss=None, lse=None, work
     outside [0, V) are padding).  Returns the fp32 loss [R] (T^2 times the divergence from
     the teacher's renormalised distribution) and the lse [R] ``distill_bwd`` takes."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, logits):
             return distill_fwd(logits, top, top_ids, temperature, loss, lse, workspace)
     lib = load_library()
     shape = _matrix("logits", logits)
@@ -728,7 +742,7 @@ def distill_bwd(logits, top, top_ids, lse, dloss, dlogits=None, temperature=1.0,
     """Gradient of ``distill_fwd``'s loss with respect to the logits, from dloss [R] (fp32; 0
     for a masked row).  ``dlogits`` [R, V] may be ``logits`` itself; it is returned."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, logits):
             return distill_bwd(logits, top, top_ids, lse, dloss, dlogits, temperature)
     lib = load_library()
     shape = _matrix("logits", logits)
@@ -755,7 +769,7 @@ def distill_fwd_bwd(logits, top, top_ids, dloss, dlogits=None, temperature=1.0, 
     weights ``dloss`` [R] beforehand.  ``dlogits`` may be ``logits`` itself.  Returns
     (loss, lse, dlogits)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, logits):
             return distill_fwd_bwd(logits, top, top_ids, dloss, dlogits, temperature, loss, lse,
                                    workspace)
     lib = load_library()
