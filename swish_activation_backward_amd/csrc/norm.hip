@@ -348,7 +348,8 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_fwd_kernel(
 // (963 us as two passes of single elements); [16384, 4096] fp16 with fp32 w 77 us = 5.2 TB/s;
 // [8191, 1023] fp32, rows at any 4-byte boundary, 28 us.  One workgroup a CU keeps the partial
 // rows few: they cost 8 N bytes a workgroup twice, which shows where rows are few and wide
-// ([1000, 8192] bf16: 25 us with dw and db, 11 us without).
+// ([1000, 8192] bf16: 25 us with dw and db, 11 us without).  Above 4096 columns the 128 registers
+// of 1024 threads do not hold everything: 12 to 32 bytes a lane spill.
 template <typename T, typename W, int G, int EC>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, float* part, int64_t Np) {
   constexpr int ROWS = 1024 / G;

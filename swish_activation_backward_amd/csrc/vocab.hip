@@ -133,7 +133,9 @@ template <bool ENT> __device__ inline void run_chunk(Run& a, const float* f, flo
     if constexpr (ENT) a.t = __builtin_fmaf(d, e, a.t);
   }
   if constexpr (ENT) {
-    if (a.t != a.t) {   // masked entries: -inf times 0
+    // masked entries, -inf times 0: the chunk's exponentials again, for the whole wave (1021 x
+    // 50021 fp32, every 16th entry masked, so every wave and chunk: 49.9 us, unmasked 48.3)
+    if (a.t != a.t) {
       a.t = t0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -788,13 +790,14 @@ __device__ inline void remake_groups(float* out, const T* body, int64_t t0, int6
 // workgroup of NT threads.  A segment leaves its sums in the workspace; join_kernel finishes the
 // row.
 //
-// 4096 x 131072 bf16 (1.07 GB): 165 us = 6.5 TB/s without top entries, bound by memory with the
+// 4096 x 131072 bf16 (1.07 GB): 166 us = 6.5 TB/s without top entries, bound by memory with the
 // arithmetic (36 issue cycles an element and wave, 16 of them the exponential) at three quarters
-// of that; 201 us with 64.  The selection is latency: barriers, a second read of the chosen
-// groups, and their order, about 10 us a row behind 30 us of stream, so five rows share a CU (256
-// threads a row; two rows of 512 threads take 223 us, four of 256 204 us).  1021 x
-// 50021 fp32 with 5: 48 us = 4.2 TB/s.  Keeping the k best by insertion or by repeated maxima
-// instead reads the row k times: 36.8 ms.
+// of that; 200 us with 64.  The selection is latency: barriers, a second read of the chosen
+// groups (130 MB of the pass's 1203 MB read), and their order, about 10 us a row behind 30 us of
+// stream, so five rows share a CU (256 threads a row; two rows of 512 threads take 223 us, four of
+// 256 204 us).  The 96 registers that five rows leave hold bf16; fp16 spills 12 bytes a lane (20
+// with 64 threads) and takes 204 us.  1021 x 50021 fp32 with 5: 48 us = 4.2 TB/s.  Keeping the k
+// best by insertion or by repeated maxima instead reads the row k times: 36.8 ms.
 template <typename T, int NT, int GU, int SLOTS, int MODE, int TOP, bool ENT>
 __global__ __launch_bounds__(NT, 5) void rows_kernel(VocabArgs a, int64_t seg, Soft* part,
                                                      float* part_max, int64_t row_max) {
@@ -1067,8 +1070,8 @@ __device__ inline void teacher_store(const TeacherLds& l, const VocabArgs& a, T*
 // A workgroup forms one of `split` segments of a row, `seg` chunks each.  Bound by memory:
 // [2048, 65536] bf16 log probabilities, 537 MB, 89 us = 6.0 TB/s; [2047, 50021] bf16 with 32
 // teacher entries into rows that start anywhere, 410 MB, 86 us = 4.8 TB/s (82 us where both
-// rows start at lines; 102 us without the passes' start at a line and the loads ahead, 2.9 ms
-// with a search of the entries for every column).
+// rows start at lines; temporal stores 77 us; 102 us without the passes' start at a line and the
+// loads ahead, 2.9 ms with a search of the entries for every column).
 template <typename T, int NT, int MODE>
 __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_t seg) {
   constexpr int U = Pass<T>::U;
@@ -1103,8 +1106,9 @@ __global__ __launch_bounds__(NT) void grad_kernel(VocabArgs a, int split, int64_
         if (q >= c0 && q < c1) ch[u].load_stream(body + q * 8);
       }
     };
-    // passes start at a 128-byte line of the output: waves that share one cost 7 % at rows of
-    // 50024 bf16
+    // passes start at a 128-byte line of the output: waves that share one cost 6 % at rows of
+    // 50024 bf16 (73.8 and 78.3 us).  Not so in fp32: 1024 x 65536, where rows start at lines
+    // anyway, takes 153 us with the offset and 122 without (107 with temporal stores)
     const int64_t start =
         c0 - (int64_t)((reinterpret_cast<uintptr_t>(out + c0 * 8) & 127) / (8 * sizeof(T)));
     Chunk<T> ch[U], next[U];
@@ -1207,11 +1211,11 @@ __device__ inline float uniform(float v) {
 // Loss, lse and gradient of a row that a workgroup holds in registers, D chunks a thread: the
 // logits are read once.  4096 x 131072 bf16 with 64 teacher entries (2.15 GB): 457 us = 4.7 TB/s,
 // against 532 us for the two kernels that read them twice.  A row of that length takes a CU's
-// registers (1024 threads, 16 chunks each, beside 64 registers for the rest), so its load, its
-// sums and its stores follow each other, and memory rests while the sums are formed; loading the
-// next row behind the stores, or forming its sums there as well, came to 455 and 494 us (a wait
-// for a load waits for the stores before it too).  Rows of half the length share a CU:
-// 2500 x 65536 132 us = 5.0 TB/s, 177 us for the two kernels.
+// registers (1024 threads, 16 chunks each, beside 64 registers for the rest, 12 bytes a lane
+// spilled), so its load, its sums and its stores follow each other, and memory rests while the
+// sums are formed; loading the next row behind the stores, or forming its sums there as well, came
+// to 455 and 494 us (a wait for a load waits for the stores before it too).  Rows of half the length share a CU:
+// 2500 x 65536 137 us = 4.8 TB/s, 177 us for the two kernels.
 template <typename T, int NT, int D, int WAVES>
 __global__ __launch_bounds__(NT, WAVES) void distill_kernel(VocabArgs a) {
   __shared__ __attribute__((aligned(16))) float red[NT / 64 * 4];
