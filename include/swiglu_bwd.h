@@ -319,11 +319,11 @@ size_t token_logprobs_workspace_size(int64_t R, int64_t V, int64_t top, swg_dtyp
  *   dlogits[v] = (g (1[v = t] - p_v) - h p_v (a_v - lse + entropy)) / temperature
  * for g = dlogprob[r] (0 where t = ignore_index; a row whose t is any other id outside
  * [0, V) gets NaN), h = dentropy[r].  targets and dlogprob may both be NULL (g = 0), entropy
- * and dentropy may both be NULL (h = 0).  Masked entries (p = 0) get 0, or g at the target.
- * p = exp(min(a - lse, 0)) from the fp32 lse: where |a| is so large that lse has no room beside
- * it for log sum exp (a - max a), as in a row of nothing but a large finite mask or at a tiny
- * temperature, each p stays in [0, 1] but the p of a row do not sum to 1.  dlogits: dtype, row stride ldd, overwritten; it may be exactly logits (same
- * pointer and stride).
+ * and dentropy may both be NULL (h = 0).  Masked entries (p = 0) get 0, or g / temperature at
+ * the target.  p = exp(min(a - lse, 0)) from the fp32 lse: where |a| is so large that lse has no
+ * room beside it for log sum exp (a - max a), as in a row of nothing but a large finite mask or
+ * at a tiny temperature, each p stays in [0, 1] but the p of a row do not sum to 1.  dlogits:
+ * dtype, row stride ldd, overwritten; it may be exactly logits (same pointer and stride).
  */
 swg_status token_logprobs_bwd(const void* logits, int64_t ld, const int64_t* targets,
                               const float* lse, const float* entropy,
@@ -354,8 +354,8 @@ size_t distill_workspace_size(int64_t R, int64_t V, int64_t k, swg_dtype dtype);
  * Its gradient with respect to the student's logits, with the forward's lse:
  *   dlogits[v] = dloss[r] temperature (Q p_v - sum_{j: id_j = v} q_j)
  * Q = 1, or 0 for a row without any entry above -inf.  p from lse as in token_logprobs_bwd.
- * dloss[r] = 0 gives exactly 0 whatever the row holds (masked rows).  dlogits: dtype, row stride ldd, overwritten; it may be
- * exactly logits (same pointer and stride).
+ * dloss[r] = 0 gives exactly 0 whatever the row holds (masked rows).  dlogits: dtype, row
+ * stride ldd, overwritten; it may be exactly logits (same pointer and stride).
  */
 swg_status distill_bwd(const void* logits, int64_t ld, const void* top,
                        const int64_t* top_ids, int64_t k, const float* lse,
