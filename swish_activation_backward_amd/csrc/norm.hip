@@ -247,6 +247,15 @@ __device__ inline float inv_root(float v) {
   return v < 1.17549435e-38f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
 }
 
+// s / n from 1 / n, with the remainder put back: the rounding of 1 / n would move the mean by up to
+// its last place, and a row of equal values far from 0 would be normed by nothing but that.  An
+// infinite s stays.
+__device__ inline float quotient(float s, float n, float inv_n) {
+  const float q = s * inv_n;
+  const float r = __builtin_fmaf(__builtin_fmaf(-q, n, s), inv_n, q);
+  return r == r ? r : q;
+}
+
 // Forward: the row is read once; the variance is the mean of squared differences from the mean,
 // both over registers.  All workgroups are resident and walk over the rows with the next row's
 // loads in flight.  Bound by memory, and closely behind by the arithmetic around the two
@@ -297,7 +306,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_fwd_kernel(
       drop(g, map.skip[j]);
       s += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
     }
-    const float mu = row_sum<G>(s, red[0], grp * (G / 64)) * inv_n;
+    const float mu = quotient(row_sum<G>(s, red[0], grp * (G / 64)), (float)N, inv_n);
     s = 0.0f;
 #pragma unroll
     for (int j = 0; j < EC; ++j) {
