@@ -1,6 +1,7 @@
 /*
  * swiglu_bwd.h — C ABI of the MI355X (gfx950) SwiGLU backward and Swish-gradient library, with
- * the operators around the gate: layer norm, token log probabilities, distillation.
+ * the operators around the gate: layer norm, residual norm, token log probabilities,
+ * distillation.
  *
  * Sources (web pages; cited by title and section):
  *   [SwiGLU page]  "PyPTO-Gym 实战: Fused SwiGLU 反向传播算子 (Ascend NPU 三 Kernel 融合实现)",
@@ -242,8 +243,9 @@ swg_status swish_grad_strided(const void* grad, const void* x, void* grad_x, int
                               swg_dtype dtype, const float* beta, void* stream);
 
 /*
- * Operators around the gate: the layer norm in front of it and, at the vocabulary end, token
- * log probabilities and distillation from a teacher's top logits.  They share these rules:
+ * Operators around the gate: the layer norm in front of it, the residual norm between blocks and,
+ * at the vocabulary end, token log probabilities and distillation from a teacher's top logits.
+ * They share these rules:
  *   - Matrices are rows of contiguous elements a row stride (ld*, in elements, at least the
  *     row length when there is more than one row) apart, so a slice of a wider buffer is
  *     taken as it is; every other buffer is contiguous.  Pointers need the alignment of
@@ -286,6 +288,62 @@ swg_status layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t l
                           int64_t M, int64_t N, swg_dtype dtype, swg_dtype wdtype,
                           void* workspace, size_t workspace_bytes, void* stream);
 size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
+
+/*
+ * Residual norm between two blocks, over the rows of y [M, N]: the root mean square norm after a
+ * block (post), its gate, the residual sum and the norm before the next block (pre), each part
+ * optional:
+ *   u = y rs w_post  (post != 0; otherwise u = y),    rs = 1 / sqrt(sum y^2 / N + eps)
+ *   out = residual + scale gate u
+ *   norm = out rp w_pre  (pre != 0),                  rp = 1 / sqrt(sum out^2 / N + eps)
+ * y, norm: dtype; residual (NULL: 0), out: rdtype = dtype or SWG_FP32; w_post, w_pre: [N] of
+ * wdtype = dtype or SWG_FP32, NULL: 1 (other types: SWG_ERR_UNSUPPORTED).  gate:
+ *   SWG_GATE_NONE     absent (1); ldg is not used
+ *   SWG_GATE_CHANNEL  [N] of wdtype, contiguous; ldg is not used
+ *   SWG_GATE_ROW      one value a row, of dtype, ldg elements apart
+ *   SWG_GATE_FULL     [M, N] of dtype, row stride ldg
+ * norm is formed from the fp32 value of out.  rstd_post = rs and rstd_pre = rp, [M], are for the
+ * backward pass; either may be NULL.  scale: finite; eps: finite, >= 0.  out may be exactly the
+ * residual (same pointer and stride).  What belongs to a part that is off is not touched.
+ */
+typedef enum {
+  SWG_GATE_NONE = 0,
+  SWG_GATE_CHANNEL = 1,
+  SWG_GATE_ROW = 2,
+  SWG_GATE_FULL = 3
+} swg_gate;
+swg_status residual_norm_fwd(const void* y, int64_t ldy, const void* residual, int64_t ldr,
+                             const void* w_post, const void* w_pre, const void* gate,
+                             int64_t ldg, swg_gate gate_kind, float scale, void* out, int64_t ldo,
+                             void* norm, int64_t ldn, float* rstd_post, float* rstd_pre, int post,
+                             int pre, int64_t M, int64_t N, float eps, swg_dtype dtype,
+                             swg_dtype rdtype, swg_dtype wdtype, void* stream);
+
+/*
+ * Its gradients, from dout (rdtype, of the stream's later use) and dnorm (dtype), either NULL for
+ * 0, and the forward's y, out and statistics (rstd_post, rstd_pre: NULL where the part was off),
+ * with xh = out rp, yh = y rs (y where post was off), h = dnorm w_pre:
+ *   D = dout + rp (h - xh sum(h xh) / N),  dresidual = D
+ *   v = scale gate D w_post,  dy = rs (v - yh sum(v yh) / N)     (dy = scale gate D without post)
+ *   dw_pre = sum_m dnorm xh,  dw_post = sum_m scale gate D yh
+ *   dgate = scale D u, summed over n for SWG_GATE_ROW, over m for SWG_GATE_CHANNEL
+ * Each of dy, dresidual, dw_post, dw_pre and dgate may be NULL (not wanted); out is read only with
+ * dnorm.  dgate has the gate's shape and type, row stride lddg.  accumulate = 0: dw_post, dw_pre
+ * and a channel gate's dgate are overwritten; otherwise the sums are added to their contents
+ * before the one rounding.  The other outputs are overwritten.  dresidual may be exactly dout.
+ * SWG_ERR_INVALID: a gradient of a part that was off.  workspace:
+ * residual_norm_bwd_workspace_size(M, N, dtype) bytes, 16-byte aligned.
+ */
+swg_status residual_norm_bwd(const void* dout, int64_t lddo, const void* dnorm, int64_t lddn,
+                             const void* y, int64_t ldy, const void* out, int64_t ldo,
+                             const void* w_post, const void* w_pre, const void* gate, int64_t ldg,
+                             swg_gate gate_kind, float scale, const float* rstd_post,
+                             const float* rstd_pre, void* dy, int64_t lddy, void* dresidual,
+                             int64_t lddr, void* dw_post, void* dw_pre, void* dgate, int64_t lddg,
+                             int accumulate, int64_t M, int64_t N, swg_dtype dtype,
+                             swg_dtype rdtype, swg_dtype wdtype, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t residual_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
 
 /*
  * Log probabilities over rows of logits z [R, V] (dtype, row stride ld) at a temperature

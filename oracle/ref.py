@@ -35,7 +35,7 @@ import numpy as np
 
 __all__ = ["sigmoid", "silu", "silu_grad", "swish_grad_ref", "b_ref", "w_ref",
            "x_ref", "swiglu_forward_ref", "swiglu_bwd_ref", "layer_norm_ref",
-           "layer_norm_bwd_ref", "log_softmax_ref", "entropy_ref", "top_ref",
+           "layer_norm_bwd_ref", "residual_norm_ref", "residual_norm_bwd_ref", "log_softmax_ref", "entropy_ref", "top_ref",
            "token_logprobs_bwd_ref", "teacher_ref", "distill_ref", "distill_bwd_ref"]
 
 
@@ -167,6 +167,59 @@ def layer_norm_bwd_ref(dy, x, w, mean, rstd):
     c1 = h.mean(1, keepdims=True)
     c2 = (h * xh).mean(1, keepdims=True)
     return rs * (h - c1 - xh * c2), (dy * xh).sum(0), dy.sum(0)
+
+
+def _times(a, w):
+    return a if w is None else a * _f64(w)
+
+
+def residual_norm_ref(y, residual, w_post, w_pre, gate, scale, eps, post=True, pre=True):
+    """out = residual + scale * gate * rms(y) w_post, norm = rms(out) w_pre; returns (out, norm,
+    rstd_post, rstd_pre).  Weights and gate None: 1, residual None: 0; the gate broadcasts."""
+    u = y = _f64(y)
+    rs = rp = norm = None
+    if post:
+        rs = 1.0 / np.sqrt((y * y).mean(1) + eps)
+        u = _times(y * rs[:, None], w_post)
+    out = scale * _times(u, gate)
+    if residual is not None:
+        out = out + _f64(residual)
+    if pre:
+        rp = 1.0 / np.sqrt((out * out).mean(1) + eps)
+        norm = _times(out * rp[:, None], w_pre)
+    return out, norm, rs, rp
+
+
+def residual_norm_bwd_ref(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, rstd_pre, scale):
+    """Gradients (dy, dresidual, dw_post, dw_pre, dgate) of residual_norm_ref with the statistics
+    given (None: that norm is off); dgate has the gate's shape."""
+    y = _f64(y)
+    D = np.zeros_like(y) if dout is None else _f64(dout)
+    dw_pre = dw_post = dgate = None
+    if rstd_pre is not None:
+        rp = _f64(rstd_pre)[:, None]
+        dn = np.zeros_like(y) if dnorm is None else _f64(dnorm)
+        xh = (np.zeros_like(y) if dnorm is None else _f64(out)) * rp
+        h = _times(dn, w_pre)
+        D = D + rp * (h - xh * (h * xh).mean(1, keepdims=True))
+        dw_pre = (dn * xh).sum(0)
+    u = yh = y
+    if rstd_post is not None:
+        yh = y * _f64(rstd_post)[:, None]
+        u = _times(yh, w_post)
+    du = scale * _times(D, gate)
+    if gate is not None:
+        dgate = scale * D * u
+        if np.ndim(gate) == 1:
+            dgate = dgate.sum(0)
+        elif np.shape(gate)[1] == 1:
+            dgate = dgate.sum(1, keepdims=True)
+    dy = du
+    if rstd_post is not None:
+        dw_post = (du * yh).sum(0)
+        v = _times(du, w_post)
+        dy = _f64(rstd_post)[:, None] * (v - yh * (v * yh).mean(1, keepdims=True))
+    return dy, D, dw_post, dw_pre, dgate
 
 
 def log_softmax_ref(z, t):

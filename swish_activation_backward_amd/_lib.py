@@ -23,7 +23,9 @@ __all__ = ["SwgError", "load_library", "library_path", "swish_grad", "swish_grad
            "swiglu_bwd_gemm_tile", "swg_set_gemm_tile", "DTYPE_CODE", "STATUS",
            "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size", "TokenLogprobs",
            "token_logprobs", "token_logprobs_bwd", "token_logprobs_workspace_size", "distill_fwd",
-           "distill_bwd", "distill_fwd_bwd", "distill_workspace_size", "MAX_TOP", "MAX_TEACHER"]
+           "distill_bwd", "distill_fwd_bwd", "distill_workspace_size", "MAX_TOP", "MAX_TEACHER",
+           "ResidualNorm", "residual_norm_fwd", "residual_norm_bwd",
+           "residual_norm_bwd_workspace_size"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libswiglu_bwd.so"
@@ -100,6 +102,15 @@ def load_library():
         lib.layer_norm_bwd.restype = i32
         lib.layer_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
         lib.layer_norm_bwd_workspace_size.restype = sz
+        lib.residual_norm_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i32, f32, vp, i64, vp,
+                                          i64, vp, vp, i32, i32, i64, i64, f32, i32, i32, i32, vp]
+        lib.residual_norm_fwd.restype = i32
+        lib.residual_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32,
+                                          f32, vp, vp, vp, i64, vp, i64, vp, vp, vp, i64, i32, i64,
+                                          i64, i32, i32, i32, vp, sz, vp]
+        lib.residual_norm_bwd.restype = i32
+        lib.residual_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
+        lib.residual_norm_bwd_workspace_size.restype = sz
         lib.token_logprobs.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32, i64,
                                        i32, vp, sz, vp]
         lib.token_logprobs.restype = i32
@@ -606,6 +617,154 @@ def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace
     _call("layer_norm_bwd", lib.layer_norm_bwd, dev, dy.data_ptr(), lddy, x.data_ptr(),
           ldx, _addr(w), mean_at, rstd_at, _addr(dx), lddx, _addr(dw), _addr(db), int(accumulate),
           M, N, code, DTYPE_CODE[wdt], _addr(ws), _size(ws))
+
+
+class ResidualNorm(NamedTuple):
+    """What ``residual_norm_fwd`` returns: the new residual stream out [M, N], its norm [M, N] (None
+    where ``pre`` is off) and the fp32 statistics [M] of the norms that are on."""
+    out: torch.Tensor
+    norm: Optional[torch.Tensor]
+    rstd_post: Optional[torch.Tensor]
+    rstd_pre: Optional[torch.Tensor]
+
+
+_GATE_NONE, _GATE_CHANNEL, _GATE_ROW, _GATE_FULL = range(4)
+
+
+def _gate(name, t, dtype, wdtype, shape, device):
+    """Kind and row stride of a gate: [N] (``wdtype``), [M, 1] or [M, N] (``dtype``)."""
+    if t is None:
+        return _GATE_NONE, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    M, N = shape
+    if t.dim() == 1:
+        _packed(name, t, wdtype, (N,), device)
+        return _GATE_CHANNEL, N
+    if t.shape == shape:
+        return _GATE_FULL, _rows(name, t, dtype, shape, device)
+    if t.shape != (M, 1):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(N,)}, {(M, 1)} or {(M, N)}")
+    return _GATE_ROW, _rows(name, t, dtype, (M, 1), device)
+
+
+def _vectors(gate):
+    """A gate of the columns is of the norm weights' type."""
+    return gate if isinstance(gate, torch.Tensor) and gate.dim() == 1 else None
+
+
+def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0, post=True,
+                      pre=True, out=None, norm=None, rstd_post=None, rstd_pre=None, eps=1e-5,
+                      stream=None):
+    """The root mean square norm after a block (``post``), its gate, the residual sum and the norm
+    before the next block (``pre``) over the rows of y [M, N]:
+
+        out = residual + scale * gate * (y rs w_post),  norm = out rp w_pre
+
+    ``residual`` [M, N] (None: 0) and ``out`` have y's dtype or fp32, ``w_post`` and ``w_pre`` [N]
+    (None: 1) y's dtype or fp32.  ``gate`` is None, [N] (of the weights' type), or [M, 1] or [M, N]
+    (of y's).  ``out`` may be ``residual``; outputs that are not given are allocated.  Returns
+    ``ResidualNorm``."""
+    if stream is not None:
+        with _on_stream(stream, y):
+            return residual_norm_fwd(y, residual, w_post, w_pre, gate, scale, post, pre, out, norm,
+                                     rstd_post, rstd_pre, eps)
+    lib = load_library()
+    shape = _matrix("y", y)
+    M, N = shape
+    dt, dev = y.dtype, y.device
+    code = _dtype_code(y)
+    ldy = _rows("y", y, dt, shape, dev)
+    wdt = _affine(dt, N, dev, w_post=w_post, w_pre=w_pre, gate=_vectors(gate))
+    kind, ldg = _gate("gate", gate, dt, wdt, shape, dev)
+    rdt, ldr = dt, N
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
+        rdt = residual.dtype
+        ldr = _rows("residual", residual, rdt, shape, dev)
+    elif out is not None:
+        rdt = out.dtype
+    _gpu(dev)
+    if out is None:
+        out = torch.empty(shape, dtype=rdt, device=dev)
+    ldo = _rows("out", out, rdt, shape, dev)
+    rcode = _dtype_code(out)
+    ldn = N
+    if pre:
+        if norm is None:
+            norm = torch.empty(shape, dtype=dt, device=dev)
+        ldn = _rows("norm", norm, dt, shape, dev)
+        rstd_pre = _out("rstd_pre", rstd_pre, torch.float32, (M,), dev)
+    else:
+        norm = rstd_pre = None
+    rstd_post = _out("rstd_post", rstd_post, torch.float32, (M,), dev) if post else None
+    _call("residual_norm_fwd", lib.residual_norm_fwd, dev, y.data_ptr(), ldy, _addr(residual), ldr,
+          _addr(w_post), _addr(w_pre), _addr(gate), ldg, kind, scale, out.data_ptr(), ldo,
+          _addr(norm), ldn, _addr(rstd_post), _addr(rstd_pre), int(post), int(pre), M, N, eps, code,
+          rcode, DTYPE_CODE[wdt])
+    return ResidualNorm(out, norm, rstd_post, rstd_pre)
+
+
+def residual_norm_bwd_workspace_size(M: int, N: int, dtype) -> int:
+    return int(load_library().residual_norm_bwd_workspace_size(M, N, DTYPE_CODE[dtype]))
+
+
+def residual_norm_bwd(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, rstd_pre, dy, dresidual,
+                      dw_post=None, dw_pre=None, dgate=None, scale=1.0, accumulate=False,
+                      workspace=None, stream=None):
+    """Gradients of ``residual_norm_fwd`` from ``dout`` and ``dnorm`` [M, N] (either None: 0) and the
+    forward's ``out``, ``rstd_post`` and ``rstd_pre`` (None where that norm was off): writes dy,
+    dresidual, dw_post, dw_pre and dgate (each may be None).  ``dresidual`` may be ``dout``; with
+    ``accumulate`` dw_post, dw_pre and the dgate of a gate [N] are added to (+=)."""
+    if stream is not None:
+        with _on_stream(stream, y):
+            return residual_norm_bwd(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, rstd_pre,
+                                     dy, dresidual, dw_post, dw_pre, dgate, scale, accumulate,
+                                     workspace)
+    lib = load_library()
+    shape = _matrix("y", y)
+    M, N = shape
+    dt, dev = y.dtype, y.device
+    code = _dtype_code(y)
+    ldy = _rows("y", y, dt, shape, dev)
+    wdt = _affine(dt, N, dev, w_post=w_post, w_pre=w_pre, dw_post=dw_post, dw_pre=dw_pre,
+                  gate=_vectors(gate), dgate=_vectors(dgate))
+    kind, ldg = _gate("gate", gate, dt, wdt, shape, dev)
+    lddg = 0
+    if dgate is not None:
+        if gate is None or dgate.shape != gate.shape:
+            raise ValueError("dgate must have the gate's shape")
+        lddg = _gate("dgate", dgate, dt, wdt, shape, dev)[1]
+    # the residual stream's type: of the first one given
+    rdt, lds = None, []
+    for name, t in (("dout", dout), ("out", out if dnorm is not None else None),
+                    ("dresidual", dresidual)):
+        if t is None:
+            lds.append(N)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        rdt = t.dtype if rdt is None else rdt
+        lds.append(_rows(name, t, rdt, shape, dev))
+    if dnorm is not None and (out is None or rstd_pre is None):
+        raise ValueError("dnorm needs out and rstd_pre")
+    rdt = dt if rdt is None else rdt
+    if rdt not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {rdt}")
+    lddn = N if dnorm is None else _rows("dnorm", dnorm, dt, shape, dev)
+    lddy = N if dy is None else _rows("dy", dy, dt, shape, dev)
+    for name, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
+        if t is not None:
+            _packed(name, t, torch.float32, (M,), dev)
+    _gpu(dev)
+    ws = _workspace(_workspace_bytes("residual_norm_bwd_workspace_size", M, N, code), workspace,
+                    dev, None)
+    _call("residual_norm_bwd", lib.residual_norm_bwd, dev, _addr(dout), lds[0], _addr(dnorm), lddn,
+          y.data_ptr(), ldy, _addr(out), lds[1], _addr(w_post), _addr(w_pre), _addr(gate), ldg, kind,
+          scale, _addr(rstd_post), _addr(rstd_pre), _addr(dy), lddy, _addr(dresidual), lds[2],
+          _addr(dw_post), _addr(dw_pre), _addr(dgate), lddg, int(accumulate), M, N, code,
+          DTYPE_CODE[rdt], DTYPE_CODE[wdt], _addr(ws), _size(ws))
 
 
 class TokenLogprobs(NamedTuple):

@@ -666,6 +666,153 @@ swg_status layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t l
                                     as_stream(stream)));
 }
 
+namespace {
+
+bool gate_ok(int kind) { return kind >= SWG_GATE_NONE && kind <= SWG_GATE_FULL; }
+bool is_finite(float v) { return v - v == 0.0f; }
+
+// elements, element size and rows of a gate (or of its gradient)
+struct GateView {
+  int64_t rows, cols, ld, es;
+};
+GateView gate_view(int kind, int64_t M, int64_t N, int64_t ld, int64_t es, int64_t ws) {
+  if (kind == SWG_GATE_CHANNEL) return {1, N, N, ws};
+  if (kind == SWG_GATE_ROW) return {M, 1, ld, es};
+  return {M, N, ld, es};
+}
+Span gate_span(const void* p, const GateView& g) {
+  return {p, p ? rows_bytes(g.rows, g.cols, g.ld, g.es) : 0};
+}
+
+swg_status residual_norm_types(int dtype, int rdtype, int wdtype, int kind) {
+  if (!dtype_ok(rdtype) || !gate_ok(kind)) return SWG_ERR_INVALID;
+  const swg_status st = norm_types(dtype, wdtype);
+  if (st != SWG_OK) return st;
+  return rdtype == dtype || rdtype == SWG_FP32 ? SWG_OK : SWG_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+swg_status residual_norm_fwd(const void* y, int64_t ldy, const void* residual, int64_t ldr,
+                             const void* w_post, const void* w_pre, const void* gate,
+                             int64_t ldg, swg_gate gate_kind, float scale, void* out, int64_t ldo,
+                             void* norm, int64_t ldn, float* rstd_post, float* rstd_pre, int post,
+                             int pre, int64_t M, int64_t N, float eps, swg_dtype dtype,
+                             swg_dtype rdtype, swg_dtype wdtype, void* stream) {
+  TimedCall timed_;
+  const swg_status st = residual_norm_types(dtype, rdtype, wdtype, gate_kind);
+  if (st != SWG_OK) return st;
+  if (!row_dims_ok(M, N) || !(eps >= 0.0f) || !is_finite(eps) || !is_finite(scale))
+    return SWG_ERR_INVALID;
+  const int64_t es = elem_size(dtype), rs = elem_size(rdtype), ws = elem_size(wdtype);
+  const GateView gv = gate_view(gate_kind, M, N, ldg, es, ws);
+  if (!stride_ok(M, N, ldy) || (residual && !stride_ok(M, N, ldr)) || !stride_ok(M, N, ldo) ||
+      (pre && !stride_ok(M, N, ldn)) || (gate_kind != SWG_GATE_NONE && !stride_ok(gv.rows, gv.cols, gv.ld)))
+    return SWG_ERR_INVALID;
+  if (M == 0) return SWG_OK;
+  if (N == 0) return SWG_ERR_INVALID;
+  if (!y || !out || (pre && !norm) || (gate_kind != SWG_GATE_NONE && !gate)) return SWG_ERR_NULLPTR;
+  // what the call does not use
+  if (!post) w_post = nullptr, rstd_post = nullptr;
+  if (!pre) w_pre = nullptr, rstd_pre = nullptr, norm = nullptr;
+  if (gate_kind == SWG_GATE_NONE) gate = nullptr;
+  if (!aligned(y, (size_t)es) || !aligned(norm, (size_t)es) || !aligned(gate, (size_t)gv.es) ||
+      !aligned(residual, (size_t)rs) || !aligned(out, (size_t)rs) || !aligned(w_post, (size_t)ws) ||
+      !aligned(w_pre, (size_t)ws) || !aligned(rstd_post, 4) || !aligned(rstd_pre, 4))
+    return SWG_ERR_INVALID;
+  // out may be exactly the residual
+  const bool in_place = out == residual && (ldo == ldr || M == 1);
+  const Span stream_in = {in_place ? nullptr : residual, residual ? rows_bytes(M, N, ldr, rs) : 0};
+  const Span outs[] = {{out, rows_bytes(M, N, ldo, rs)}, {norm, norm ? rows_bytes(M, N, ldn, es) : 0},
+                       {rstd_post, 4 * M}, {rstd_pre, 4 * M}};
+  const Span ins[] = {{y, rows_bytes(M, N, ldy, es)}, stream_in, {w_post, N * ws}, {w_pre, N * ws},
+                      gate_span(gate, gv)};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  ResidualNormArgs a{};
+  a.y = y; a.ldy = ldy; a.residual = residual; a.ldr = ldr; a.wp = w_post; a.wq = w_pre;
+  a.gate = gate; a.ldg = ldg; a.kind = gate_kind; a.scale = scale; a.out = out; a.ldo = ldo;
+  a.norm = norm; a.ldn = ldn; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  a.post = post != 0; a.pre = pre != 0; a.wide = wdtype == SWG_FP32; a.in_place = in_place;
+  a.M = M; a.N = N; a.eps = eps;
+  return hip_status(launch_residual_norm_fwd(dtype, rdtype, a, as_stream(stream)));
+}
+
+size_t residual_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype) {
+  if (!dtype_ok(dtype) || !row_dims_ok(M, N) || M == 0 || N == 0) return 0;
+  return plan_residual_norm_bwd(M, N).ws_bytes;
+}
+
+swg_status residual_norm_bwd(const void* dout, int64_t lddo, const void* dnorm, int64_t lddn,
+                             const void* y, int64_t ldy, const void* out, int64_t ldo,
+                             const void* w_post, const void* w_pre, const void* gate, int64_t ldg,
+                             swg_gate gate_kind, float scale, const float* rstd_post,
+                             const float* rstd_pre, void* dy, int64_t lddy, void* dresidual,
+                             int64_t lddr, void* dw_post, void* dw_pre, void* dgate, int64_t lddg,
+                             int accumulate, int64_t M, int64_t N, swg_dtype dtype,
+                             swg_dtype rdtype, swg_dtype wdtype, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  TimedCall timed_;
+  swg_status st = residual_norm_types(dtype, rdtype, wdtype, gate_kind);
+  if (st != SWG_OK) return st;
+  if (!row_dims_ok(M, N) || !is_finite(scale)) return SWG_ERR_INVALID;
+  const bool post = rstd_post != nullptr, pre = rstd_pre != nullptr;
+  // M = 0 has no statistics to say which norms there are
+  if (M > 0 && ((!post && dw_post) || (!pre && (dnorm || dw_pre)))) return SWG_ERR_INVALID;
+  if (gate_kind == SWG_GATE_NONE && dgate) return SWG_ERR_INVALID;
+  const int64_t es = elem_size(dtype), rs = elem_size(rdtype), ws = elem_size(wdtype);
+  const GateView gv = gate_view(gate_kind, M, N, ldg, es, ws);
+  const GateView dgv = gate_view(gate_kind, M, N, lddg, es, ws);
+  if (!stride_ok(M, N, ldy) || (dout && !stride_ok(M, N, lddo)) ||
+      (dnorm && (!stride_ok(M, N, lddn) || !stride_ok(M, N, ldo))) ||
+      (dy && !stride_ok(M, N, lddy)) || (dresidual && !stride_ok(M, N, lddr)) ||
+      (gate_kind != SWG_GATE_NONE && !stride_ok(gv.rows, gv.cols, gv.ld)) ||
+      (dgate && !stride_ok(dgv.rows, dgv.cols, dgv.ld)))
+    return SWG_ERR_INVALID;
+  if (M > 0 && N == 0) return SWG_ERR_INVALID;
+  const bool cols = dw_post || dw_pre || (dgate && gate_kind == SWG_GATE_CHANNEL);
+  if (N == 0 || (M == 0 && (accumulate || !cols)) || (!dy && !dresidual && !dgate && !cols))
+    return SWG_OK;
+  if (M > 0 && (!y || (dnorm && !out))) return SWG_ERR_NULLPTR;
+  if (M > 0 && gate_kind != SWG_GATE_NONE && !gate) return SWG_ERR_NULLPTR;
+  if (gate_kind == SWG_GATE_NONE) gate = nullptr;
+  if (!dnorm) out = nullptr;
+  for (const void* p : {y, dnorm, (const void*)dy})
+    if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
+  for (const void* p : {dout, out, (const void*)dresidual})
+    if (!aligned(p, (size_t)rs)) return SWG_ERR_INVALID;
+  for (const void* p : {w_post, w_pre, (const void*)dw_post, (const void*)dw_pre})
+    if (!aligned(p, (size_t)ws)) return SWG_ERR_INVALID;
+  if (!aligned(gate, (size_t)gv.es) || !aligned(dgate, (size_t)gv.es) || !aligned(rstd_post, 4) ||
+      !aligned(rstd_pre, 4))
+    return SWG_ERR_INVALID;
+  ResidualNormPlan p{};
+  if (M > 0) p = plan_residual_norm_bwd(M, N);
+  const size_t need = p.ws_bytes;
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  // dresidual may be exactly dout
+  const bool in_place = dresidual && dresidual == dout && (lddr == lddo || M == 1);
+  auto rows = [&](const void* q, int64_t ld, int64_t e) {
+    return Span{q, q ? rows_bytes(M, N, ld, e) : 0};
+  };
+  const Span outs[] = {rows(dy, lddy, es), rows(dresidual, lddr, rs), {dw_post, N * ws},
+                       {dw_pre, N * ws}, gate_span(dgate, dgv), {workspace, (int64_t)need}};
+  const Span ins[] = {rows(in_place ? nullptr : dout, lddo, rs), rows(dnorm, lddn, es),
+                      rows(y, ldy, es), rows(out, ldo, rs), {w_post, N * ws}, {w_pre, N * ws},
+                      gate_span(gate, gv), {rstd_post, 4 * M}, {rstd_pre, 4 * M}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  ResidualNormArgs a{};
+  a.dout = dout; a.lddo = lddo; a.dnorm = dnorm; a.lddn = lddn; a.y = y; a.ldy = ldy;
+  a.out = const_cast<void*>(out); a.ldo = ldo; a.wp = w_post; a.wq = w_pre; a.gate = gate;
+  a.ldg = ldg; a.kind = gate_kind; a.scale = scale;
+  a.rstd_post = const_cast<float*>(rstd_post); a.rstd_pre = const_cast<float*>(rstd_pre);
+  a.dy = dy; a.lddy = lddy; a.dresidual = dresidual; a.lddr = lddr; a.dwp = dw_post; a.dwq = dw_pre;
+  a.dgate = dgate; a.lddg = lddg; a.accumulate = accumulate != 0;
+  a.post = post; a.pre = pre; a.wide = wdtype == SWG_FP32; a.in_place = in_place; a.M = M; a.N = N;
+  return hip_status(launch_residual_norm_bwd(dtype, rdtype, a, p, static_cast<float*>(workspace),
+                                             as_stream(stream)));
+}
+
 size_t token_logprobs_workspace_size(int64_t R, int64_t V, int64_t top, swg_dtype dtype) {
   if (!dtype_ok(dtype) || !row_dims_ok(R, V) || R == 0 || V == 0 || top < 0 || top > V ||
       top > SWG_MAX_TOP)

@@ -119,6 +119,48 @@ hipError_t launch_norm_fwd(int dtype, int wdtype, const NormArgs& a, hipStream_t
 hipError_t launch_norm_bwd(int dtype, int wdtype, const NormArgs& a, const NormPlan& p,
                            float* part, hipStream_t stream);
 
+// Residual norm.  Row strides in elements; pointers that a call does not use are null.
+enum GateKind { kGateNone = 0, kGateChannel = 1, kGateRow = 2, kGateFull = 3 };
+struct ResidualNormArgs {
+  const void* y;
+  int64_t ldy;
+  const void* residual;
+  int64_t ldr;
+  const void* wp;           // of the norm after the block
+  const void* wq;           // of the norm before the next block
+  const void* gate;
+  int64_t ldg;
+  void* out;                // read by the backward pass
+  int64_t ldo;
+  void* norm;
+  int64_t ldn;
+  float* rstd_post;
+  float* rstd_pre;
+  const void* dout;
+  int64_t lddo;
+  const void* dnorm;
+  int64_t lddn;
+  void* dy;
+  int64_t lddy;
+  void* dresidual;
+  int64_t lddr;
+  void* dwp;
+  void* dwq;
+  void* dgate;
+  int64_t lddg;
+  int64_t M, N;
+  float scale, eps;
+  int kind;                 // GateKind
+  bool post, pre;
+  bool wide;                // wp, wq, a gate of the columns and their gradients are fp32
+  bool in_place;            // out is residual, or dresidual is dout
+  bool accumulate;
+};
+hipError_t launch_residual_norm_fwd(int dtype, int rdtype, const ResidualNormArgs& a,
+                                    hipStream_t stream);
+hipError_t launch_residual_norm_bwd(int dtype, int rdtype, const ResidualNormArgs& a,
+                                    const ResidualNormPlan& p, float* ws, hipStream_t stream);
+
 // Rows of logits [R, V] (row stride ld) with what the forward and backward of the token log
 // probabilities and of the distillation loss read and write; pointers that a call does not
 // use are null.

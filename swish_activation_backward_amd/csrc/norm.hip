@@ -20,31 +20,6 @@ namespace swg {
 // bf16 takes 46 us forward and 97 us backward (199 and 239 us by single elements), one row of
 // 65536 14 and 19 us.
 
-// use(column, elements) for the thread's parts of a row: 8 at a time, then one
-template <int NT, typename F> __device__ inline void each_part(int64_t N, F use) {
-  for (int64_t c = (int64_t)threadIdx.x * 8; c + 8 <= N; c += NT * 8)
-    use(c, std::integral_constant<int, 8>());
-  const int64_t c = (N & ~int64_t(7)) + threadIdx.x;
-  if (c < N) use(c, std::integral_constant<int, 1>());
-}
-template <int n, typename T> __device__ inline void load_part(const T* p, float* f) {
-  if constexpr (n == 8) {
-    Chunk<T> c;
-    c.load(p);
-    c.widen(f);
-  } else {
-    f[0] = to_f32(p[0]);
-  }
-}
-template <int n, typename T> __device__ inline void store_part(T* p, const float* f) {
-  if constexpr (n == 8) {
-    Chunk<T> c;
-    c.narrow(f);
-    c.store_stream(p);
-  } else {
-    p[0] = from_f32<T>(f[0]);
-  }
-}
 template <int n, typename W>
 __device__ inline void affine_part(const W* w, int64_t c, float absent, float* f) {
   if (w) {
@@ -181,47 +156,6 @@ __global__ __launch_bounds__(256) void norm_cols_any_kernel(const T* dy, int64_t
 }
 
 // ------------------------------------------------------------------ rows in registers
-// A row of 8 <= N <= 16384 elements is held by G threads, EC chunks of 8 elements each (chunk
-// j * G + lane starts at column 8 times that).  A row whose length is no multiple of 8 ends
-// with a chunk moved back to the row's end: its first `skip` elements belong to the chunk
-// before as well, count in no sum, and are written twice with the same value.
-template <int G, int EC> struct RowMap {
-  int col[EC];    // first column of the chunk
-  int skip[EC];   // duplicated elements; 8 where the thread has no chunk
-  __device__ inline RowMap(int lane, int64_t n) {
-    const int N = (int)n;
-#pragma unroll
-    for (int j = 0; j < EC; ++j) {
-      const int c = (j * G + lane) * 8;
-      col[j] = c + 8 <= N ? c : N - 8;
-      skip[j] = c >= N ? 8 : c - col[j];
-    }
-  }
-  __device__ inline bool has(int j) const { return skip[j] < 8; }
-};
-
-// the first `skip` elements become 0
-__device__ inline void drop(float* f, int skip) {
-  if (skip > 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < skip ? 0.0f : f[i];
-  }
-}
-
-// Sums over the G threads of a row: lanes of a wave, or waves through LDS (one barrier; two
-// successive calls use different halves of `red`, so a third may reuse the first's).
-template <int G> __device__ inline float row_sum(float v, float* red, int wave0) {
-  v = lanes_sum<(G < 64 ? G : 64)>(v);
-  if constexpr (G > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[wave0];
-#pragma unroll
-    for (int i = 1; i < G / 64; ++i) v += red[wave0 + i];
-  }
-  return v;
-}
-
 // w and b as fp32 (1 and 0 where absent)
 template <typename W>
 __device__ inline void load_affine(const W* w, int64_t c, float absent, float* f) {
@@ -233,18 +167,6 @@ __device__ inline void load_affine(const W* w, int64_t c, float absent, float* f
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = absent;
   }
-}
-
-// The thread's row group; groups of whole waves in a scalar register, and with it the row's
-// addresses and statistics.
-template <int G> __device__ inline int row_group() {
-  const int g = (int)(threadIdx.x / G);
-  return G < 64 ? g : __builtin_amdgcn_readfirstlane(g);
-}
-
-// 1 / sqrt(v): the hardware's reciprocal root (1 ulp), which takes no subnormal
-__device__ inline float inv_root(float v) {
-  return v < 1.17549435e-38f ? 1.0f / __builtin_sqrtf(v) : __builtin_amdgcn_rsqf(v);
 }
 
 // s / n from 1 / n, with the remainder put back: the rounding of 1 / n would move the mean by up to

@@ -326,6 +326,28 @@ inline NormPlan plan_norm_bwd(int64_t M, int64_t N) {
   return p;
 }
 
+// The residual norm's backward pass: two fp32 values a row, then `parts` partial rows of 2 np, one
+// for each block of `rows` rows.
+struct ResidualNormPlan {
+  int64_t rows;
+  int64_t parts;
+  int64_t np;
+  int64_t stat_floats;
+  size_t ws_bytes;
+};
+
+inline ResidualNormPlan plan_residual_norm_bwd(int64_t M, int64_t N) {
+  ResidualNormPlan p{};
+  p.np = ceil_div(N, 4) * 4;
+  // one thread walks a block of narrow rows: many short blocks
+  const int64_t least = N < 8 ? 16 : 64, blocks = N < 8 ? 8192 : 256;
+  p.rows = M > blocks * least ? ceil_div(M, blocks) : least;
+  p.parts = ceil_div(M, p.rows);
+  p.stat_floats = ceil_div(2 * M, 4) * 4;
+  p.ws_bytes = (size_t)(p.stat_floats + p.parts * 2 * p.np) * sizeof(float);
+  return p;
+}
+
 // Operators on logits [R, V]: a workgroup of `threads` reads a row, or one of `split` segments
 // of `seg` chunks (8 elements) where the rows alone do not fill the GPU.  Segments are whole
 // passes of 256 threads (64 bytes each); a split row leaves the segments' sums (12 bytes each)
