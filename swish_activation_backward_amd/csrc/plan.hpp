@@ -326,9 +326,12 @@ inline NormPlan plan_norm_bwd(int64_t M, int64_t N) {
   return p;
 }
 
-// The residual norm's backward pass: two fp32 values a row, then `parts` partial rows of 2 np, one
-// for each block of `rows` rows.
+// The residual norm's backward pass, as layer norm's: rows of 8 to 16384 elements are held by
+// `group` threads of `chunks` chunks each, and a workgroup (512 threads, 1024 above 8192 columns)
+// per CU leaves one fp32 partial row of 2 np.  Other lengths (group = 0) need two fp32 values a row
+// before those, and their partial rows are of blocks of `rows` rows.
 struct ResidualNormPlan {
+  int group, chunks;
   int64_t rows;
   int64_t parts;
   int64_t np;
@@ -339,11 +342,19 @@ struct ResidualNormPlan {
 inline ResidualNormPlan plan_residual_norm_bwd(int64_t M, int64_t N) {
   ResidualNormPlan p{};
   p.np = ceil_div(N, 4) * 4;
-  // one thread walks a block of narrow rows: many short blocks
-  const int64_t least = N < 8 ? 16 : 64, blocks = N < 8 ? 8192 : 256;
-  p.rows = M > blocks * least ? ceil_div(M, blocks) : least;
-  p.parts = ceil_div(M, p.rows);
-  p.stat_floats = ceil_div(2 * M, 4) * 4;
+  if (N < 8 || N > 16384) {
+    // one thread walks a block of narrow rows: many short blocks
+    const int64_t least = N < 8 ? 16 : 64, blocks = N < 8 ? 8192 : 256;
+    p.rows = M > blocks * least ? ceil_div(M, blocks) : least;
+    p.parts = ceil_div(M, p.rows);
+    p.stat_floats = ceil_div(2 * M, 4) * 4;
+  } else {
+    p.chunks = N <= 1024 ? 1 : 2;
+    p.group = 8;
+    while ((int64_t)p.group * 8 * p.chunks < N) p.group *= 2;
+    const int64_t n = ceil_div(M, p.group > 512 ? 1 : 512 / p.group);
+    p.parts = n < 256 ? n : 256;
+  }
   p.ws_bytes = (size_t)(p.stat_floats + p.parts * 2 * p.np) * sizeof(float);
   return p;
 }

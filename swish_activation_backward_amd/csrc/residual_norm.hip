@@ -248,6 +248,380 @@ __global__ __launch_bounds__(NT) void rnorm_apply_any_kernel(ResidualNormArgs a,
   }
 }
 
+// ------------------------------------------------------------------ rows in registers
+// 8 <= N <= 16384 (RowMap): every row is read once.
+
+// 8 elements of a row, all but the first `skip` if they must not be written twice
+template <typename T>
+__device__ inline void store_chunk(T* p, const float* f, int skip, bool once) {
+  if (once && skip > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= skip) p[i] = from_f32<T>(f[i]);
+    return;
+  }
+  Chunk<T> c;
+  c.narrow(f);
+  c.store_stream(p);
+}
+
+// Forward.  All workgroups are resident and walk over the rows with the next row's loads in
+// flight.  A row that is changed in place and whose end is held twice is written once: without a
+// norm no barrier orders the first write before the second read.
+template <typename T, typename R, bool FULL, int G, int EC>
+__global__ __launch_bounds__(G > 256 ? G : 256) void rnorm_fwd_kernel(ResidualNormArgs a) {
+  constexpr int ROWS = G > 256 ? 1 : 256 / G;
+  __shared__ float red[2][G > 256 ? G / 64 : 4];
+  const int lane = threadIdx.x % G, grp = row_group<G>(), wave0 = grp * (G / 64);
+  const RowMap<G, EC> map(lane, a.N);
+  const float inv_n = 1.0f / (float)a.N;
+  const T* y = static_cast<const T*>(a.y);
+  const R* res = static_cast<const R*>(a.residual);
+  const T* gate = static_cast<const T*>(a.gate);
+  // of one chunk the weights stay in registers, of more they are read again (from cache)
+  constexpr bool HELD = EC == 1;
+  float wp[HELD ? 8 : 1], wq[HELD ? 8 : 1];
+  auto gated = [&](int64_t c, float* f) {
+    load_weights<8, T>(a.post ? a.wp : nullptr, a.wide, c, 1.0f, f);
+    if (a.kind == kGateChannel) {
+      float g[8];
+      load_weights<8, T>(a.gate, a.wide, c, 1.0f, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= g[i];
+    }
+  };
+  if constexpr (HELD) {
+    gated(map.col[0], wp);
+    load_weights<8, T>(a.pre ? a.wq : nullptr, a.wide, map.col[0], 1.0f, wq);
+  }
+  struct Row {
+    Chunk<T> y[EC], g[FULL ? EC : 1];
+    Chunk<R> r[EC];
+  };
+  auto load = [&](Row& d, int64_t row) {
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      d.y[j].zero();
+      d.r[j].zero();
+      if constexpr (FULL) d.g[j].zero();
+      if (map.has(j) && row < a.M) {
+        d.y[j].load_stream(y + row * a.ldy + map.col[j]);
+        if (res) d.r[j].load_stream(res + row * a.ldr + map.col[j]);
+        if constexpr (FULL) d.g[j].load_stream(gate + row * a.ldg + map.col[j]);
+      }
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t r = (int64_t)blockIdx.x * ROWS + grp;
+  int half = 0;
+  auto root = [&](float s) {
+    s = row_sum<G>(s, red[half], wave0);
+    half ^= 1;
+    return inv_root(__builtin_fmaf(s, inv_n, a.eps));
+  };
+  Row cur, next;
+  load(cur, r);
+  // every thread of the workgroup makes the same number of passes (barriers)
+  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.M; base += step, r += step) {
+    load(next, r + step);
+    const bool live = r < a.M;
+    const float k = live ? row_scale<T>(a, r) : 0.0f;
+    float f[EC][8];
+    auto square = [&]() {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < EC; ++j) {
+        float g[8], q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = f[j][i];
+        drop(g, map.skip[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q = __builtin_fmaf(g[i], g[i], q);
+        s += q;
+      }
+      return s;
+    };
+#pragma unroll
+    for (int j = 0; j < EC; ++j) cur.y[j].widen(f[j]);
+    float rs = 1.0f, rp = 0.0f;
+    if (a.post) rs = root(square());
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      float e[8], h[8];
+      if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = wp[i];
+      } else {
+        gated(map.col[j], e);
+      }
+      if constexpr (FULL) {
+        cur.g[j].widen(h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] *= h[i];
+      }
+      cur.r[j].widen(h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j][i] = __builtin_fmaf(k * e[i], f[j][i] * rs, h[i]);
+    }
+    if (a.pre) rp = root(square());
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < EC; ++j) {
+        if (!map.has(j)) continue;
+        store_chunk(static_cast<R*>(a.out) + r * a.ldo + map.col[j], f[j], map.skip[j],
+                    a.in_place);
+        if (a.pre) {
+          float e[8];
+          if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = wq[i];
+          } else {
+            load_weights<8, T>(a.wq, a.wide, map.col[j], 1.0f, e);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e[i] *= f[j][i] * rp;
+          store_chunk(static_cast<T*>(a.norm) + r * a.ldn + map.col[j], e, map.skip[j], false);
+        }
+      }
+      if (lane == 0) {
+        if (a.post && a.rstd_post) a.rstd_post[r] = rs;
+        if (a.pre && a.rstd_pre) a.rstd_pre[r] = rp;
+      }
+    }
+    cur = next;
+  }
+}
+
+// Backward.  A workgroup of NT threads walks its share of the rows, NT / G at a time; each thread
+// keeps the sums dnorm xh and gate D yh of its own columns in registers, and the row groups add
+// theirs through LDS at the end, in a fixed order, to one partial row.
+template <typename T, typename R, bool FULL, int G, int EC>
+__global__ __launch_bounds__(G > 512 ? 1024 : 512) void rnorm_bwd_kernel(ResidualNormArgs a,
+                                                                        float* part, int64_t Np) {
+  constexpr int NT = G > 512 ? 1024 : 512, ROWS = NT / G;
+  __shared__ float red[2][3][NT / 64];
+  __shared__ float sums[ROWS > 1 ? NT * EC * 8 : 1];
+  const int lane = threadIdx.x % G, grp = row_group<G>(), wave0 = grp * (G / 64);
+  const RowMap<G, EC> map(lane, a.N);
+  constexpr bool HELD = NT == 512;   // weights in registers, the next row's loads ahead
+  float wp[HELD ? EC : 1][8], wq[HELD ? EC : 1][8], sq[EC][8], sp[EC][8];
+  auto gated = [&](int64_t c, float* f) {
+    load_weights<8, T>(a.post ? a.wp : nullptr, a.wide, c, 1.0f, f);
+    if (a.kind == kGateChannel) {
+      float g[8];
+      load_weights<8, T>(a.gate, a.wide, c, 1.0f, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= g[i];
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < EC; ++j) {
+    if constexpr (HELD) {
+      gated(map.col[j], wp[j]);
+      load_weights<8, T>(a.wq, a.wide, map.col[j], 1.0f, wq[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq[j][i] = sp[j][i] = 0.0f;
+  }
+  const float inv_n = 1.0f / (float)a.N;
+  struct Row {
+    Chunk<T> dn[EC], y[EC], g[FULL ? EC : 1];
+    Chunk<R> d[EC], o[EC];
+    float rs, rp, gr;
+  };
+  auto load = [&](Row& q, int64_t row) {
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      q.dn[j].zero();
+      q.y[j].zero();
+      q.d[j].zero();
+      q.o[j].zero();
+      if constexpr (FULL) q.g[j].zero();
+      if (map.has(j) && row < a.M) {
+        const int c = map.col[j];
+        if (a.dnorm) {
+          q.dn[j].load_stream(static_cast<const T*>(a.dnorm) + row * a.lddn + c);
+          q.o[j].load_stream(static_cast<const R*>(a.out) + row * a.ldo + c);
+        }
+        q.y[j].load_stream(static_cast<const T*>(a.y) + row * a.ldy + c);
+        if (a.dout) q.d[j].load_stream(static_cast<const R*>(a.dout) + row * a.lddo + c);
+        if constexpr (FULL)
+          q.g[j].load_stream(static_cast<const T*>(a.gate) + row * a.ldg + c);
+      }
+    }
+    const bool live = row < a.M;
+    q.rs = live && a.post ? a.rstd_post[row] : 1.0f;
+    q.rp = live && a.dnorm ? a.rstd_pre[row] : 0.0f;
+    q.gr = live && a.kind == kGateRow ? to_f32(static_cast<const T*>(a.gate)[row * a.ldg]) : 1.0f;
+  };
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t r = (int64_t)blockIdx.x * ROWS + grp;
+  int half = 0;
+  Row cur, next;
+  if (HELD) load(cur, r);
+  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.M; base += step, r += step) {
+    if (HELD) load(next, r + step);
+    else load(cur, r);
+    const bool live = r < a.M;
+    const float rs = cur.rs, rp = cur.rp;
+    // one chunk's values: d = dout, dn, xh, yh, w = wq, e = wp and the gate along the row
+    struct Part {
+      float d[8], dn[8], xh[8], yh[8], w[8], e[8], g[8];
+    };
+    auto chunk = [&](int j, Part& p) {
+      cur.d[j].widen(p.d);
+      cur.dn[j].widen(p.dn);
+      cur.o[j].widen(p.xh);
+      cur.y[j].widen(p.yh);
+      if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.w[i] = wq[j][i], p.e[i] = wp[j][i];
+      } else {
+        load_weights<8, T>(a.wq, a.wide, map.col[j], 1.0f, p.w);
+        gated(map.col[j], p.e);
+      }
+      if constexpr (FULL) cur.g[j].widen(p.g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p.xh[i] *= rp;
+        p.yh[i] *= rs;
+        if constexpr (!FULL) p.g[i] = 1.0f;
+      }
+    };
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      Part p;
+      chunk(j, p);
+      float h[8], ye[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[i] = p.dn[i] * p.w[i];
+        ye[i] = p.yh[i] * (p.e[i] * p.g[i]);
+        sq[j][i] = __builtin_fmaf(p.dn[i], p.xh[i], sq[j][i]);
+      }
+      drop(h, map.skip[j]);
+      drop(ye, map.skip[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s0 = __builtin_fmaf(h[i], p.xh[i], s0);
+        s1 = __builtin_fmaf(__builtin_fmaf(rp, h[i], p.d[i]), ye[i], s1);
+        s2 = __builtin_fmaf(p.xh[i], ye[i], s2);
+      }
+    }
+    constexpr int L = G < 64 ? G : 64;
+    s0 = lanes_sum<L>(s0);
+    s1 = lanes_sum<L>(s1);
+    s2 = lanes_sum<L>(s2);
+    if constexpr (G > 64) {
+      if ((threadIdx.x & 63) == 0) {
+        red[half][0][threadIdx.x >> 6] = s0;
+        red[half][1][threadIdx.x >> 6] = s1;
+        red[half][2][threadIdx.x >> 6] = s2;
+      }
+      __syncthreads();
+      s0 = s1 = s2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < G / 64; ++i) {
+        s0 += red[half][0][wave0 + i];
+        s1 += red[half][1][wave0 + i];
+        s2 += red[half][2][wave0 + i];
+      }
+      half ^= 1;
+    }
+    const float c = s0 * inv_n, total = __builtin_fmaf(-rp * c, s2, s1);
+    const float t = a.post ? total * inv_n : 0.0f;
+    const float k = rs * a.scale * cur.gr;
+#pragma unroll
+    for (int j = 0; j < EC; ++j) {
+      Part p;
+      chunk(j, p);
+      float D[8], f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        D[i] = __builtin_fmaf(rp, p.dn[i] * p.w[i] - p.xh[i] * c, p.d[i]);
+        sp[j][i] = __builtin_fmaf(D[i] * (p.g[i] * cur.gr), p.yh[i], sp[j][i]);
+        f[i] = k * (D[i] * (p.e[i] * p.g[i]) - p.yh[i] * t);
+      }
+      if (!live || !map.has(j)) continue;
+      if (a.dy)
+        store_chunk(static_cast<T*>(a.dy) + r * a.lddy + map.col[j], f, map.skip[j], false);
+      if (a.dresidual)
+        store_chunk(static_cast<R*>(a.dresidual) + r * a.lddr + map.col[j], D, map.skip[j],
+                    a.in_place);
+      if constexpr (FULL) {
+        if (a.dgate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = a.scale * D[i] * (p.yh[i] * p.e[i]);
+          store_chunk(static_cast<T*>(a.dgate) + r * a.lddg + map.col[j], f, map.skip[j], false);
+        }
+      }
+    }
+    if (a.kind == kGateRow && a.dgate && live && lane == 0)
+      static_cast<T*>(a.dgate)[r * a.lddg] = from_f32<T>(a.scale * total);
+    if (HELD) cur = next;
+  }
+  if (part == nullptr) return;
+  // the row groups' sums, group by group; each thread of the first group ends with its columns'
+  if constexpr (ROWS > 1) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < EC; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sums[(j * 8 + i) * NT + threadIdx.x] = which ? sp[j][i] : sq[j][i];
+      __syncthreads();
+      // G * EC * 8 column sums over NT threads
+      constexpr int COLS = G * EC * 8, Q = (COLS + NT - 1) / NT;
+      float total[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int e = q * NT + threadIdx.x;
+        total[q] = 0.0f;
+        if (COLS % NT == 0 || e < COLS) {
+          for (int g = 0; g < ROWS; ++g) total[q] += sums[(e / G) * NT + g * G + e % G];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int e = q * NT + threadIdx.x;
+        if (COLS % NT == 0 || e < COLS) sums[e] = total[q];
+      }
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int j = 0; j < EC; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) (which ? sp : sq)[j][i] = sums[(j * 8 + i) * G + lane];
+      }
+    }
+    if (grp != 0) return;
+  }
+  float* pq = part + (int64_t)blockIdx.x * 2 * Np;
+#pragma unroll
+  for (int j = 0; j < EC; ++j) {
+    if (map.skip[j] == 0) {   // a whole chunk: columns 8 n, 16-byte aligned
+      f32x4* q4 = reinterpret_cast<f32x4*>(pq + map.col[j]);
+      f32x4* p4 = reinterpret_cast<f32x4*>(pq + Np + map.col[j]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q4[i] = f32x4{sq[j][4 * i], sq[j][4 * i + 1], sq[j][4 * i + 2], sq[j][4 * i + 3]};
+        p4[i] = f32x4{sp[j][4 * i], sp[j][4 * i + 1], sp[j][4 * i + 2], sp[j][4 * i + 3]};
+      }
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < map.skip[j]) continue;
+      pq[map.col[j] + i] = sq[j][i];
+      pq[Np + map.col[j] + i] = sp[j][i];
+    }
+  }
+}
+
 // Sums the partial rows (16 groups of 4 columns to a workgroup, 16 threads a group) and forms the
 // weights' gradients: dwq = S0, dwp = scale gate S1, dgate = scale wp S1 (a gate of the columns).
 template <typename T>
@@ -305,12 +679,31 @@ __global__ __launch_bounds__(256) void rnorm_finalize_kernel(ResidualNormArgs a,
 
 template <typename T, typename R>
 static hipError_t rnorm_fwd_t(const ResidualNormArgs& a, hipStream_t stream) {
+#define SWG_FWD(G, EC)                                                                         \
+  do {                                                                                         \
+    const dim3 grid(norm_fwd_grid(a.M, G > 256 ? 1 : 256 / G, G > 256 ? G : 256));             \
+    const dim3 block(G > 256 ? G : 256);                                                       \
+    if (a.kind == kGateFull)                                                                   \
+      SWG_TRY(SWG_LAUNCH((rnorm_fwd_kernel<T, R, true, G, EC>), grid, block, 0, stream, a));   \
+    else                                                                                       \
+      SWG_TRY(SWG_LAUNCH((rnorm_fwd_kernel<T, R, false, G, EC>), grid, block, 0, stream, a));  \
+  } while (0)
   if (a.N < 8)
     SWG_TRY(SWG_LAUNCH((rnorm_fwd_any_kernel<T, R, 64>), dim3(row_grid(a.M)), dim3(64), 0, stream,
                        a));
-  else
+  else if (a.N > 16384)
     SWG_TRY(SWG_LAUNCH((rnorm_fwd_any_kernel<T, R, 512>), dim3(row_grid(a.M)), dim3(512), 0,
                        stream, a));
+  else if (a.N <= 64) SWG_FWD(8, 1);
+  else if (a.N <= 128) SWG_FWD(16, 1);
+  else if (a.N <= 256) SWG_FWD(32, 1);
+  else if (a.N <= 512) SWG_FWD(64, 1);
+  else if (a.N <= 1024) SWG_FWD(64, 2);
+  else if (a.N <= 2048) SWG_FWD(256, 1);
+  else if (a.N <= 4096) SWG_FWD(256, 2);
+  else if (a.N <= 8192) SWG_FWD(512, 2);
+  else SWG_FWD(1024, 2);
+#undef SWG_FWD
   return hipSuccess;
 }
 
@@ -320,7 +713,7 @@ static hipError_t rnorm_bwd_t(const ResidualNormArgs& a, const ResidualNormPlan&
   const bool cols = a.dwp || a.dwq || (a.dgate && a.kind == kGateChannel);
   float* stat = ws;
   float* part = ws + p.stat_floats;
-  if (a.M > 0) {
+  if (a.M > 0 && p.group == 0) {
     const bool narrow = a.N < 8;
     if (narrow)
       SWG_TRY(SWG_LAUNCH((rnorm_stat_any_kernel<T, R, 64>), dim3(row_grid(a.M)), dim3(64), 0,
@@ -340,6 +733,31 @@ static hipError_t rnorm_bwd_t(const ResidualNormArgs& a, const ResidualNormPlan&
         SWG_TRY(SWG_LAUNCH((rnorm_apply_any_kernel<T, R, 512>), dim3(row_grid(a.M)), dim3(512), 0,
                            stream, a, stat));
     }
+  } else if (a.M > 0) {
+    float* sums = cols ? part : nullptr;
+#define SWG_BWD(G, EC)                                                                        \
+  case G * 16 + EC: {                                                                         \
+    const dim3 grid((unsigned)p.parts), block(G > 512 ? 1024 : 512);                          \
+    if (a.kind == kGateFull)                                                                  \
+      SWG_TRY(SWG_LAUNCH((rnorm_bwd_kernel<T, R, true, G, EC>), grid, block, 0, stream, a,    \
+                         sums, p.np));                                                        \
+    else                                                                                      \
+      SWG_TRY(SWG_LAUNCH((rnorm_bwd_kernel<T, R, false, G, EC>), grid, block, 0, stream, a,   \
+                         sums, p.np));                                                        \
+    break;                                                                                    \
+  }
+    switch (p.group * 16 + p.chunks) {
+      SWG_BWD(8, 1)
+      SWG_BWD(16, 1)
+      SWG_BWD(32, 1)
+      SWG_BWD(64, 1)
+      SWG_BWD(128, 1)
+      SWG_BWD(128, 2)
+      SWG_BWD(256, 2)
+      SWG_BWD(512, 2)
+      SWG_BWD(1024, 2)
+    }
+#undef SWG_BWD
   }
   if (!cols) return hipSuccess;
   // M = 0: no partial rows, the empty sums
