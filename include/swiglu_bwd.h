@@ -1,7 +1,7 @@
 /*
  * swiglu_bwd.h — C ABI of the MI355X (gfx950) SwiGLU backward and Swish-gradient library, with
- * the operators around the gate: layer norm, residual norm, token log probabilities,
- * distillation.
+ * the operators around the gate: layer norm, residual norm, linear layer, token log
+ * probabilities, distillation.
  *
  * Sources (web pages; cited by title and section):
  *   [SwiGLU page]  "PyPTO-Gym 实战: Fused SwiGLU 反向传播算子 (Ascend NPU 三 Kernel 融合实现)",
@@ -243,9 +243,9 @@ swg_status swish_grad_strided(const void* grad, const void* x, void* grad_x, int
                               swg_dtype dtype, const float* beta, void* stream);
 
 /*
- * Operators around the gate: the layer norm in front of it, the residual norm between blocks and,
- * at the vocabulary end, token log probabilities and distillation from a teacher's top logits.
- * They share these rules:
+ * Operators around the gate: the layer norm in front of it, the linear layer behind it, the
+ * residual norm between blocks and, at the vocabulary end, token log probabilities and
+ * distillation from a teacher's top logits.  They share these rules:
  *   - Matrices are rows of contiguous elements a row stride (ld*, in elements, at least the
  *     row length when there is more than one row) apart, so a slice of a wider buffer is
  *     taken as it is; every other buffer is contiguous.  Pointers need the alignment of
@@ -344,6 +344,56 @@ swg_status residual_norm_bwd(const void* dout, int64_t lddo, const void* dnorm, 
                              swg_dtype rdtype, swg_dtype wdtype, void* workspace,
                              size_t workspace_bytes, void* stream);
 size_t residual_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
+
+/*
+ * Linear layer with its epilogue, over the rows of x [M, K]:
+ *   z = x W + bias,  y = act(z) + residual
+ * W: [K, N] with row stride ldw, or, with w_nk != 0, its transpose [N, K] with row stride ldw.
+ * bias [N], residual [M, N] and z [M, N] may be NULL; z is what linear_bwd takes for an
+ * activation.  Every tensor is of dtype.  act:
+ *   SWG_ACT_NONE       z
+ *   SWG_ACT_RELU       max(z, 0)
+ *   SWG_ACT_SWISH      z sigma(beta z)
+ *   SWG_ACT_GELU       z Phi(z), Phi the normal distribution function
+ *   SWG_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ * beta is finite and used by SWG_ACT_SWISH only.  Bias, activation and residual are applied to the
+ * fp32 sums.  y may be exactly the residual (same pointer and stride).  K and N below 2^22
+ * (SWG_ERR_UNSUPPORTED).  K = 0: z = bias (the empty sums).
+ * workspace: linear_fwd_workspace_size bytes, 16-byte aligned; rows16 says whether every row of x
+ * and of W as stored starts at a multiple of 16 bytes (rows16 = 0 covers both).
+ */
+typedef enum {
+  SWG_ACT_NONE = 0,
+  SWG_ACT_RELU = 1,
+  SWG_ACT_SWISH = 2,
+  SWG_ACT_GELU = 3,
+  SWG_ACT_GELU_TANH = 4
+} swg_act;
+swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int w_nk,
+                      const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                      void* z, int64_t ldz, int64_t M, int64_t K, int64_t N, swg_act act,
+                      float beta, swg_dtype dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+size_t linear_fwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_dtype dtype,
+                                 int rows16);
+
+/*
+ * Its gradients:
+ *   dz = dy act'(z)  (rounded to dtype: the operand of the two products; relu's slope at 0 is 0)
+ *   dx = dz W^T,  dw = x^T dz,  db = sum_m dz  (of the fp32 values of dz)
+ * dx [M, K], dw (stored as W is, row stride lddw) and db [N] may be NULL (not wanted); z is needed
+ * for an activation, x for dw and W for dx.  The gradient of the residual is dy.  accumulate = 0:
+ * dw and db are overwritten; otherwise the sums are added to their contents before the one
+ * rounding.  dx is overwritten.  M = 0: the empty sums; N = 0: dx = 0.
+ * workspace: linear_bwd_workspace_size bytes, 16-byte aligned; rows16 as above, of x, W, dy.
+ */
+swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                      int64_t ldw, int w_nk, const void* z, int64_t ldz, void* dx, int64_t lddx,
+                      void* dw, int64_t lddw, void* db, int accumulate, int64_t M, int64_t K,
+                      int64_t N, swg_act act, float beta, swg_dtype dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_act act,
+                                 swg_dtype dtype, int rows16);
 
 /*
  * Log probabilities over rows of logits z [R, V] (dtype, row stride ld) at a temperature

@@ -31,11 +31,14 @@ Readings taken where the pages are garbled or silent:
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 __all__ = ["sigmoid", "silu", "silu_grad", "swish_grad_ref", "b_ref", "w_ref",
            "x_ref", "swiglu_forward_ref", "swiglu_bwd_ref", "layer_norm_ref",
-           "layer_norm_bwd_ref", "residual_norm_ref", "residual_norm_bwd_ref", "log_softmax_ref", "entropy_ref", "top_ref",
+           "layer_norm_bwd_ref", "residual_norm_ref", "residual_norm_bwd_ref", "activation_ref",
+           "activation_slope_ref", "linear_ref", "linear_bwd_ref", "log_softmax_ref", "entropy_ref", "top_ref",
            "token_logprobs_bwd_ref", "teacher_ref", "distill_ref", "distill_bwd_ref"]
 
 
@@ -220,6 +223,64 @@ def residual_norm_bwd_ref(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, r
         v = _times(du, w_post)
         dy = _f64(rstd_post)[:, None] * (v - yh * (v * yh).mean(1, keepdims=True))
     return dy, D, dw_post, dw_pre, dgate
+
+
+def _tanh_gelu(z):
+    a = math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)
+    return np.tanh(a), math.sqrt(2.0 / math.pi) * (1.0 + 3.0 * 0.044715 * z * z)
+
+
+_erfc = np.frompyfunc(math.erfc, 1, 1)
+
+
+def _phi(z):
+    """Distribution function of the normal distribution."""
+    return 0.5 * _erfc(-z * math.sqrt(0.5)).astype(np.float64)
+
+
+def activation_ref(act, z, beta=1.0):
+    z = _f64(z)
+    if act == "relu":
+        return np.where(z < 0, 0.0, z)
+    if act == "swish":
+        return z * sigmoid(beta * z)
+    if act == "gelu":
+        return z * _phi(z)
+    if act == "gelu_tanh":
+        return 0.5 * z * (1.0 + _tanh_gelu(z)[0])
+    return z
+
+
+def activation_slope_ref(act, z, beta=1.0):
+    z = _f64(z)
+    if act == "relu":
+        return np.where(z > 0, 1.0, 0.0)
+    if act == "swish":
+        s = sigmoid(beta * z)
+        return s * (1.0 + beta * z * (1.0 - s))
+    if act == "gelu":
+        return _phi(z) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    if act == "gelu_tanh":
+        t, da = _tanh_gelu(z)
+        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * da
+    return np.ones_like(z)
+
+
+def linear_ref(x, w, bias=None, residual=None, act="none", beta=1.0):
+    """z = x w + bias, y = act(z) + residual; returns (y, z)."""
+    z = _f64(x) @ _f64(w)
+    if bias is not None:
+        z = z + _f64(bias)
+    y = activation_ref(act, z, beta)
+    return (y if residual is None else y + _f64(residual)), z
+
+
+def linear_bwd_ref(dy, x, w, z=None, act="none", beta=1.0):
+    """Gradients (dx, dw, db, dz) of linear_ref."""
+    dz = _f64(dy)
+    if act != "none":
+        dz = dz * activation_slope_ref(act, z, beta)
+    return dz @ _f64(w).T, _f64(x).T @ dz, dz.sum(0), dz
 
 
 def log_softmax_ref(z, t):

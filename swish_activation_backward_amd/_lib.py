@@ -25,7 +25,8 @@ __all__ = ["SwgError", "load_library", "library_path", "swish_grad", "swish_grad
            "token_logprobs", "token_logprobs_bwd", "token_logprobs_workspace_size", "distill_fwd",
            "distill_bwd", "distill_fwd_bwd", "distill_workspace_size", "MAX_TOP", "MAX_TEACHER",
            "ResidualNorm", "residual_norm_fwd", "residual_norm_bwd",
-           "residual_norm_bwd_workspace_size"]
+           "residual_norm_bwd_workspace_size", "linear_fwd", "linear_bwd",
+           "linear_fwd_workspace_size", "linear_bwd_workspace_size", "ACTIVATION"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libswiglu_bwd.so"
@@ -33,6 +34,8 @@ _LIB_NAME = "libswiglu_bwd.so"
 DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 STATUS = {0: "SWG_OK", 1: "SWG_ERR_NULLPTR", 2: "SWG_ERR_INVALID", 3: "SWG_ERR_UNSUPPORTED",
           4: "SWG_ERR_WORKSPACE", 5: "SWG_ERR_HIP"}
+
+ACTIVATION = {"none": 0, "relu": 1, "swish": 2, "gelu": 3, "gelu_tanh": 4}
 
 _lock = threading.Lock()
 _lib = None
@@ -111,6 +114,16 @@ def load_library():
         lib.residual_norm_bwd.restype = i32
         lib.residual_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
         lib.residual_norm_bwd_workspace_size.restype = sz
+        lib.linear_fwd.argtypes = [vp, i64, vp, i64, i32, vp, vp, i64, vp, i64, vp, i64, i64, i64,
+                                   i64, i32, f32, i32, vp, sz, vp]
+        lib.linear_fwd.restype = i32
+        lib.linear_fwd_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+        lib.linear_fwd_workspace_size.restype = sz
+        lib.linear_bwd.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp,
+                                   i32, i64, i64, i64, i32, f32, i32, vp, sz, vp]
+        lib.linear_bwd.restype = i32
+        lib.linear_bwd_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i32]
+        lib.linear_bwd_workspace_size.restype = sz
         lib.token_logprobs.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, f32, i64,
                                        i32, vp, sz, vp]
         lib.token_logprobs.restype = i32
@@ -765,6 +778,128 @@ def residual_norm_bwd(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, rstd_
           scale, _addr(rstd_post), _addr(rstd_pre), _addr(dy), lddy, _addr(dresidual), lds[2],
           _addr(dw_post), _addr(dw_pre), _addr(dgate), lddg, int(accumulate), M, N, code,
           DTYPE_CODE[rdt], DTYPE_CODE[wdt], _addr(ws), _size(ws))
+
+
+def _act(act):
+    if act not in ACTIVATION:
+        raise ValueError(f"act {act!r}, expected one of {sorted(ACTIVATION)}")
+    return ACTIVATION[act]
+
+
+def _weight(name, t, dtype, shape, device, nk=None):
+    """Checks a weight [K, N] and returns whether it is stored as its transpose [N, K], and the
+    stored rows' stride; ``nk`` says which it has to be."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
+            and t.device == device):
+        _same_kind(name, t, dtype, shape, device)
+    K, N = shape
+    s0, s1 = t.stride()
+    if nk is not True and (N <= 1 or s1 == 1) and (K <= 1 or s0 >= N):
+        return False, max(s0, N)
+    if nk is not False and (K <= 1 or s0 == 1) and (N <= 1 or s1 >= K):
+        return True, max(s1, K)
+    raise ValueError(f"{name}: strides {t.stride()} (rows or columns must be contiguous and may "
+                     f"not overlap{'' if nk is None else ', as those of w'})")
+
+
+def _rows16(t, ld):
+    """Whether every row starts at a multiple of 16 bytes."""
+    return (t.data_ptr() | ld * t.element_size()) % 16 == 0
+
+
+def linear_fwd_workspace_size(M: int, K: int, N: int, dtype, w_nk=False, rows16=False) -> int:
+    return int(load_library().linear_fwd_workspace_size(M, K, N, int(w_nk), DTYPE_CODE[dtype],
+                                                        int(rows16)))
+
+
+def linear_fwd(x, w, bias=None, residual=None, act="none", beta=1.0, y=None, z=None,
+               workspace=None, stream=None):
+    """y = act(z) + residual, z = x w + bias, for x [M, K] and w [K, N] (row-major, or the
+    transpose of a row-major [N, K]).  ``act``: "none", "relu", "swish" (z sigma(beta z)), "gelu"
+    or "gelu_tanh".  ``y`` may be ``residual`` and is allocated if not given; ``z`` is written
+    where it is given (``linear_bwd`` takes it).  Returns y."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return linear_fwd(x, w, bias, residual, act, beta, y, z, workspace)
+    lib = load_library()
+    shape = _matrix("x", x)
+    M, K = shape
+    N = _matrix("w", w)[1]
+    dt, dev = x.dtype, x.device
+    code = _dtype_code(x)
+    ldx = _rows("x", x, dt, shape, dev)
+    nk, ldw = _weight("w", w, dt, (K, N), dev)
+    if bias is not None:
+        _packed("bias", bias, dt, (N,), dev)
+    ldr = N if residual is None else _rows("residual", residual, dt, (M, N), dev)
+    ldz = N if z is None else _rows("z", z, dt, (M, N), dev)
+    kind = _act(act)
+    _gpu(dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=dt, device=dev)
+    ldy = _rows("y", y, dt, (M, N), dev)
+    rows16 = _rows16(x, ldx) and _rows16(w, ldw)
+    ws = _workspace(_workspace_bytes("linear_fwd_workspace_size", M, K, N, nk, code, rows16),
+                    workspace, dev, None)
+    _call("linear_fwd", lib.linear_fwd, dev, x.data_ptr(), ldx, w.data_ptr(), ldw, nk, _addr(bias),
+          _addr(residual), ldr, y.data_ptr(), ldy, _addr(z), ldz, M, K, N, kind, beta, code,
+          _addr(ws), _size(ws))
+    return y
+
+
+def linear_bwd_workspace_size(M: int, K: int, N: int, dtype, act="none", w_nk=False,
+                              rows16=False) -> int:
+    return int(load_library().linear_bwd_workspace_size(M, K, N, int(w_nk), _act(act),
+                                                        DTYPE_CODE[dtype], int(rows16)))
+
+
+def linear_bwd(dy, x, w, z, dx, dw, db=None, act="none", beta=1.0, accumulate=False,
+               workspace=None, stream=None):
+    """Gradients of ``linear_fwd``: writes dx [M, K], dw [K, N] (stored as w is) and db [N], each
+    may be None; with ``accumulate`` dw and db are added to (+=).  ``z`` is needed for an
+    activation, ``x`` for dw and ``w`` for dx (None otherwise)."""
+    if stream is not None:
+        with _on_stream(stream, dy):
+            return linear_bwd(dy, x, w, z, dx, dw, db, act, beta, accumulate, workspace)
+    lib = load_library()
+    shape = _matrix("dy", dy)
+    M, N = shape
+    dt, dev = dy.dtype, dy.device
+    code = _dtype_code(dy)
+    kind = _act(act)
+    lddy = _rows("dy", dy, dt, shape, dev)
+    rows16 = _rows16(dy, lddy)
+    K = next((_matrix(n, t)[i] for n, t, i in (("x", x, 1), ("w", w, 0), ("dx", dx, 1),
+                                               ("dw", dw, 0)) if t is not None), 0)
+    ldx = lddx = K
+    nk, ldw, lddw, ldz = None, max(K, N), max(K, N), N
+    if x is not None:
+        ldx = _rows("x", x, dt, (M, K), dev)
+        rows16 = rows16 and _rows16(x, ldx)
+    if w is not None:
+        nk, ldw = _weight("w", w, dt, (K, N), dev)
+        rows16 = rows16 and _rows16(w, ldw)
+    if dw is not None:
+        if x is None:
+            raise ValueError("dw needs x")
+        nk, lddw = _weight("dw", dw, dt, (K, N), dev, nk)
+    if dx is not None:
+        if w is None:
+            raise ValueError("dx needs w")
+        lddx = _rows("dx", dx, dt, (M, K), dev)
+    if db is not None:
+        _packed("db", db, dt, (N,), dev)
+    if z is not None:
+        ldz = _rows("z", z, dt, shape, dev)
+    elif kind:
+        raise ValueError(f"act {act!r} needs z")
+    _gpu(dev)
+    nk = bool(nk)
+    ws = _workspace(_workspace_bytes("linear_bwd_workspace_size", M, K, N, nk, kind, code, rows16),
+                    workspace, dev, None)
+    _call("linear_bwd", lib.linear_bwd, dev, dy.data_ptr(), lddy, _addr(x), ldx, _addr(w), ldw, nk,
+          _addr(z), ldz, _addr(dx), lddx, _addr(dw), lddw, _addr(db), int(accumulate), M, K, N, kind,
+          beta, code, _addr(ws), _size(ws))
 
 
 class TokenLogprobs(NamedTuple):

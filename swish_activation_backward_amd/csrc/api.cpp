@@ -813,6 +813,148 @@ swg_status residual_norm_bwd(const void* dout, int64_t lddo, const void* dnorm, 
                                              as_stream(stream)));
 }
 
+// ------------------------------------------------------------------- linear layer
+namespace {
+
+// Types, sizes, activation and the stride of a weight [K, N] (nk: stored as [N, K]).
+swg_status linear_checks(int dtype, int act, float beta, int64_t M, int64_t K, int64_t N) {
+  if (!dtype_ok(dtype) || act < SWG_ACT_NONE || act > SWG_ACT_GELU_TANH || !is_finite(beta) ||
+      !row_dims_ok(M, K) || !row_dims_ok(M, N))
+    return SWG_ERR_INVALID;
+  return K < kMaxGemmDim && N < kMaxGemmDim ? SWG_OK : SWG_ERR_UNSUPPORTED;
+}
+bool weight_stride_ok(int64_t K, int64_t N, int64_t ldw, int nk) {
+  return nk ? stride_ok(N, K, ldw) : stride_ok(K, N, ldw);
+}
+Span weight_span(const void* w, int64_t K, int64_t N, int64_t ldw, int nk, int64_t es) {
+  return {w, w ? (nk ? rows_bytes(N, K, ldw, es) : rows_bytes(K, N, ldw, es)) : 0};
+}
+
+}  // namespace
+
+size_t linear_fwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_dtype dtype,
+                                 int rows16) {
+  return 0;
+}
+
+swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int w_nk,
+                      const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                      void* z, int64_t ldz, int64_t M, int64_t K, int64_t N, swg_act act,
+                      float beta, swg_dtype dtype, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  TimedCall timed_;
+  swg_status st = linear_checks(dtype, act, beta, M, K, N);
+  if (st != SWG_OK) return st;
+  if (!stride_ok(M, K, ldx) || !weight_stride_ok(K, N, ldw, w_nk) || !stride_ok(M, N, ldy) ||
+      (residual && !stride_ok(M, N, ldr)) || (z && !stride_ok(M, N, ldz)))
+    return SWG_ERR_INVALID;
+  if (M == 0 || N == 0) return SWG_OK;
+  if (!y || (K > 0 && (!x || !w))) return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype);
+  for (const void* p : {x, w, bias, residual, (const void*)y, (const void*)z})
+    if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
+  const size_t need = linear_fwd_workspace_size(M, K, N, w_nk, dtype, 0);
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  // y may be exactly the residual
+  const bool in_place = y == residual && (ldy == ldr || M == 1);
+  const Span outs[] = {{y, rows_bytes(M, N, ldy, es)}, {z, z ? rows_bytes(M, N, ldz, es) : 0},
+                       {workspace, (int64_t)need}};
+  const Span ins[] = {{x, rows_bytes(M, K, ldx, es)}, weight_span(w, K, N, ldw, w_nk, es),
+                      {bias, N * es}, {in_place ? nullptr : residual,
+                                       residual ? rows_bytes(M, N, ldr, es) : 0}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  Product p{};
+  p.a = {x, ldx, true};
+  p.b = {w, ldw, w_nk != 0};
+  p.P = M; p.Q = N; p.R = K;
+  p.bias = bias; p.residual = residual; p.ldr = ldr; p.out = y; p.ldo = ldy; p.z = z; p.ldz = ldz;
+  p.act = act; p.beta = beta;
+  return hip_status(launch_product(dtype, p, as_stream(stream)));
+}
+
+size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_act act,
+                                 swg_dtype dtype, int rows16) {
+  if (linear_checks(dtype, act, 1.0f, M, K, N) != SWG_OK || M == 0 || N == 0) return 0;
+  return plan_linear_bwd(M, N, act, dtype).ws_bytes;
+}
+
+swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                      int64_t ldw, int w_nk, const void* z, int64_t ldz, void* dx, int64_t lddx,
+                      void* dw, int64_t lddw, void* db, int accumulate, int64_t M, int64_t K,
+                      int64_t N, swg_act act, float beta, swg_dtype dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  TimedCall timed_;
+  swg_status st = linear_checks(dtype, act, beta, M, K, N);
+  if (st != SWG_OK) return st;
+  if (act == SWG_ACT_NONE) z = nullptr;
+  if (!stride_ok(M, N, lddy) || (dw && !stride_ok(M, K, ldx)) ||
+      (dx && !weight_stride_ok(K, N, ldw, w_nk)) || (z && !stride_ok(M, N, ldz)) ||
+      (dx && !stride_ok(M, K, lddx)) || (dw && !weight_stride_ok(K, N, lddw, w_nk)))
+    return SWG_ERR_INVALID;
+  // outputs without elements are not wanted
+  if (M == 0 || K == 0) dx = nullptr;
+  if (K == 0 || N == 0) dw = nullptr;
+  if (N == 0) db = nullptr;
+  if ((M == 0 && accumulate) || (!dx && !dw && !db)) return SWG_OK;
+  if (M > 0 && N > 0 && (!dy || (act != SWG_ACT_NONE && !z) || (dw && !x) || (dx && !w)))
+    return SWG_ERR_NULLPTR;
+  const int64_t es = elem_size(dtype);
+  for (const void* p : {dy, x, w, z, (const void*)dx, (const void*)dw, (const void*)db})
+    if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
+  const LinearBwdPlan plan = plan_linear_bwd(M, N, act, dtype);
+  const size_t need = M > 0 && N > 0 ? plan.ws_bytes : 0;
+  st = workspace_check(workspace, workspace_bytes, need);
+  if (st != SWG_OK) return st;
+  const Span outs[] = {{dx, dx ? rows_bytes(M, K, lddx, es) : 0},
+                       weight_span(dw, K, N, lddw, w_nk, es), {db, N * es},
+                       {workspace, (int64_t)need}};
+  const Span ins[] = {{dy, rows_bytes(M, N, lddy, es)}, {x, dw ? rows_bytes(M, K, ldx, es) : 0},
+                      dx ? weight_span(w, K, N, ldw, w_nk, es) : Span{nullptr, 0},
+                      {z, z ? rows_bytes(M, N, ldz, es) : 0}};
+  if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
+  char* ws = static_cast<char*>(workspace);
+  const hipStream_t hs = as_stream(stream);
+  Operand dz = {dy, lddy, true};
+  if (act != SWG_ACT_NONE || db) {
+    ActBwdArgs a{};
+    a.dy = dy; a.lddy = lddy; a.z = z; a.ldz = ldz; a.db = db; a.M = M; a.N = N; a.act = act;
+    a.beta = beta; a.accumulate = accumulate != 0;
+    if (act != SWG_ACT_NONE && (dx || dw)) {
+      a.dz = ws;
+      a.lddz = plan.lddz;
+      dz = {ws, plan.lddz, true};
+    }
+    const hipError_t e = launch_act_bwd(
+        dtype, a, plan.act, reinterpret_cast<float*>(ws ? ws + plan.part_at : nullptr), hs);
+    if (e != hipSuccess) return hip_status(e);
+  }
+  if (dx) {
+    Product p{};
+    p.a = dz;
+    p.b = {w, ldw, w_nk == 0};
+    p.P = M; p.Q = K; p.R = N;
+    p.out = dx; p.ldo = lddx;
+    const hipError_t e = launch_product(dtype, p, hs);
+    if (e != hipSuccess) return hip_status(e);
+  }
+  if (dw) {
+    Product p{};
+    dz.deep = false;
+    p.a = {x, ldx, false};
+    p.b = dz;
+    p.P = K; p.Q = N; p.R = M;
+    if (w_nk) {
+      p.b = p.a;
+      p.a = dz;
+      p.P = N; p.Q = K;
+    }
+    p.out = dw; p.ldo = lddw; p.accumulate = accumulate != 0;
+    return hip_status(launch_product(dtype, p, hs));
+  }
+  return SWG_OK;
+}
+
 size_t token_logprobs_workspace_size(int64_t R, int64_t V, int64_t top, swg_dtype dtype) {
   if (!dtype_ok(dtype) || !row_dims_ok(R, V) || R == 0 || V == 0 || top < 0 || top > V ||
       top > SWG_MAX_TOP)

@@ -161,6 +161,48 @@ hipError_t launch_residual_norm_fwd(int dtype, int rdtype, const ResidualNormArg
 hipError_t launch_residual_norm_bwd(int dtype, int rdtype, const ResidualNormArgs& a,
                                     const ResidualNormPlan& p, float* ws, hipStream_t stream);
 
+// Linear layer.  One of its products: out[p, q] = sum over r < R of A(p, r) B(q, r), with the
+// epilogue v = sum + bias[q], z = v, out = act(v) + residual (or added to out).  Pointers that a
+// call does not use are null.
+enum ActKind { kActNone = 0, kActRelu = 1, kActSwish = 2, kActGelu = 3, kActGeluTanh = 4 };
+struct Operand {
+  const void* p;
+  int64_t ld;
+  bool deep;                // the contraction index is the contiguous one
+};
+struct Product {
+  Operand a, b;
+  int64_t P, Q, R;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+  void* out;
+  int64_t ldo;
+  void* z;
+  int64_t ldz;
+  int act;                  // ActKind
+  float beta;
+  bool accumulate;
+};
+hipError_t launch_product(int dtype, const Product& a, hipStream_t stream);
+
+// dz = dy act'(z) (dz null: not wanted) and db (null: not wanted)
+struct ActBwdArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* z;
+  int64_t ldz;
+  void* dz;
+  int64_t lddz;
+  void* db;
+  int64_t M, N;
+  int act;
+  float beta;
+  bool accumulate;
+};
+hipError_t launch_act_bwd(int dtype, const ActBwdArgs& a, const ActBwdPlan& p, float* part,
+                          hipStream_t stream);
+
 // Rows of logits [R, V] (row stride ld) with what the forward and backward of the token log
 // probabilities and of the distillation loss read and write; pointers that a call does not
 // use are null.

@@ -359,6 +359,37 @@ inline ResidualNormPlan plan_residual_norm_bwd(int64_t M, int64_t N) {
   return p;
 }
 
+// The linear layer's dz and db: `parts` blocks of `rows` rows, one fp32 partial row of np each.
+struct ActBwdPlan {
+  int64_t rows, parts, np;
+};
+
+inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
+  ActBwdPlan p{};
+  p.np = ceil_div(N, 4) * 4;
+  p.rows = M > 256 * 16 ? ceil_div(M, 256) : 16;
+  p.parts = ceil_div(M, p.rows);
+  return p;
+}
+
+// Workspace of the linear layer's backward pass, from its start: dz (where there is an activation;
+// rows of a multiple of 8 elements), then the partial rows of db.
+struct LinearBwdPlan {
+  ActBwdPlan act;
+  int64_t lddz;
+  size_t part_at;
+  size_t ws_bytes;
+};
+
+inline LinearBwdPlan plan_linear_bwd(int64_t M, int64_t N, int act, int dtype) {
+  LinearBwdPlan p{};
+  p.act = plan_act_bwd(M, N);
+  p.lddz = ceil_div(N, 8) * 8;
+  p.part_at = act != 0 ? (size_t)(ceil_div(M * p.lddz * elem_size(dtype), 16) * 16) : 0;
+  p.ws_bytes = p.part_at + (size_t)(p.act.parts * p.act.np) * sizeof(float);
+  return p;
+}
+
 // Operators on logits [R, V]: a workgroup of `threads` reads a row, or one of `split` segments
 // of `seg` chunks (8 elements) where the rows alone do not fill the GPU.  Segments are whole
 // passes of 256 threads (64 bytes each); a split row leaves the segments' sums (12 bytes each)
