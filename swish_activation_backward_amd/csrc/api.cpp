@@ -826,6 +826,23 @@ swg_status linear_checks(int dtype, int act, float beta, int64_t M, int64_t K, i
 bool weight_stride_ok(int64_t K, int64_t N, int64_t ldw, int nk) {
   return nk ? stride_ok(N, K, ldw) : stride_ok(K, N, ldw);
 }
+// Rows of 16-byte multiples from a 16-byte boundary on, whose tile windows have 32-bit offsets.
+bool rows16_ok(const void* p, int64_t ld, int64_t es) {
+  return aligned(p, 16) && ld * es % 16 == 0 && ld < kMaxGemmDim;
+}
+// Rows of x and W that are no multiple of 8 long end inside a 16-byte vector.  dz as the call
+// itself lays it out is never loose; dy in its place may be.
+ProductPlan plan_linear_fwd(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool x, bool w) {
+  return plan_product(M, N, K, dtype, x || K % 8 != 0, true, w || (nk ? K : N) % 8 != 0, nk);
+}
+ProductPlan plan_linear_dx(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool dz, bool w) {
+  return plan_product(M, K, N, dtype, dz, true, w || (nk ? K : N) % 8 != 0, !nk);
+}
+ProductPlan plan_linear_dw(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool x, bool dz) {
+  x = x || K % 8 != 0;
+  return nk ? plan_product(N, K, M, dtype, dz, false, x, false)
+            : plan_product(K, N, M, dtype, x, false, dz, false);
+}
 Span weight_span(const void* w, int64_t K, int64_t N, int64_t ldw, int nk, int64_t es) {
   return {w, w ? (nk ? rows_bytes(N, K, ldw, es) : rows_bytes(K, N, ldw, es)) : 0};
 }
@@ -834,7 +851,8 @@ Span weight_span(const void* w, int64_t K, int64_t N, int64_t ldw, int nk, int64
 
 size_t linear_fwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_dtype dtype,
                                  int rows16) {
-  return 0;
+  if (linear_checks(dtype, SWG_ACT_NONE, 1.0f, M, K, N) != SWG_OK || M == 0 || N == 0) return 0;
+  return plan_linear_fwd(M, K, N, w_nk != 0, dtype, !rows16, !rows16).ws_bytes;
 }
 
 swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int w_nk,
@@ -853,7 +871,11 @@ swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, in
   const int64_t es = elem_size(dtype);
   for (const void* p : {x, w, bias, residual, (const void*)y, (const void*)z})
     if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
-  const size_t need = linear_fwd_workspace_size(M, K, N, w_nk, dtype, 0);
+  if (rows_bytes(M, K, ldx, es) < 0 || weight_span(w, K, N, ldw, w_nk, es).bytes < 0)
+    return SWG_ERR_INVALID;
+  const ProductPlan plan = plan_linear_fwd(M, K, N, w_nk != 0, dtype, !rows16_ok(x, ldx, es),
+                                           !rows16_ok(w, ldw, es));
+  const size_t need = plan.ws_bytes;
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   // y may be exactly the residual
@@ -870,13 +892,20 @@ swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, in
   p.P = M; p.Q = N; p.R = K;
   p.bias = bias; p.residual = residual; p.ldr = ldr; p.out = y; p.ldo = ldy; p.z = z; p.ldz = ldz;
   p.act = act; p.beta = beta;
-  return hip_status(launch_product(dtype, p, as_stream(stream)));
+  return hip_status(launch_product(dtype, p, plan, workspace, gemm_grid_cap(), as_stream(stream)));
 }
 
 size_t linear_bwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_act act,
                                  swg_dtype dtype, int rows16) {
   if (linear_checks(dtype, act, 1.0f, M, K, N) != SWG_OK || M == 0 || N == 0) return 0;
-  return plan_linear_bwd(M, N, act, dtype).ws_bytes;
+  size_t product = 0;
+  if (K > 0) {
+    const bool dz = act == SWG_ACT_NONE && (!rows16 || N % 8 != 0);
+    const size_t dx = plan_linear_dx(M, K, N, w_nk != 0, dtype, dz, !rows16).ws_bytes;
+    const size_t dw = plan_linear_dw(M, K, N, w_nk != 0, dtype, !rows16, dz).ws_bytes;
+    product = dx > dw ? dx : dw;
+  }
+  return plan_linear_bwd(M, N, act, dtype).product_at + product;
 }
 
 swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
@@ -897,13 +926,27 @@ swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   if (K == 0 || N == 0) dw = nullptr;
   if (N == 0) db = nullptr;
   if ((M == 0 && accumulate) || (!dx && !dw && !db)) return SWG_OK;
-  if (M > 0 && N > 0 && (!dy || (act != SWG_ACT_NONE && !z) || (dw && !x) || (dx && !w)))
+  const bool sums = M > 0 && N > 0;
+  if (sums && (!dy || (act != SWG_ACT_NONE && !z) || (dw && !x) || (dx && !w)))
     return SWG_ERR_NULLPTR;
   const int64_t es = elem_size(dtype);
   for (const void* p : {dy, x, w, z, (const void*)dx, (const void*)dw, (const void*)db})
     if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
+  if (rows_bytes(M, N, lddy, es) < 0 || (dw && rows_bytes(M, K, ldx, es) < 0) ||
+      (dx && weight_span(w, K, N, ldw, w_nk, es).bytes < 0))
+    return SWG_ERR_INVALID;
+  // what the call takes of the workspace
+  const bool nk = w_nk != 0;
   const LinearBwdPlan plan = plan_linear_bwd(M, N, act, dtype);
-  const size_t need = M > 0 && N > 0 ? plan.ws_bytes : 0;
+  const bool own_dz = act != SWG_ACT_NONE && (dx || dw);
+  const bool loose_dz = !own_dz && (!rows16_ok(dy, lddy, es) || N % 8 != 0);
+  ProductPlan plan_dx{}, plan_dw{};
+  if (dx) plan_dx = plan_linear_dx(M, K, N, nk, dtype, loose_dz, !rows16_ok(w, ldw, es));
+  if (dw) plan_dw = plan_linear_dw(M, K, N, nk, dtype, !rows16_ok(x, ldx, es), loose_dz);
+  size_t need = 0;
+  if (sums)
+    need = plan.product_at + (plan_dx.ws_bytes > plan_dw.ws_bytes ? plan_dx.ws_bytes
+                                                                  : plan_dw.ws_bytes);
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   const Span outs[] = {{dx, dx ? rows_bytes(M, K, lddx, es) : 0},
@@ -914,28 +957,29 @@ swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
                       {z, z ? rows_bytes(M, N, ldz, es) : 0}};
   if (!outputs_disjoint(outs, ins)) return SWG_ERR_INVALID;
   char* ws = static_cast<char*>(workspace);
+  char* ws_product = sums ? ws + plan.product_at : nullptr;
   const hipStream_t hs = as_stream(stream);
   Operand dz = {dy, lddy, true};
-  if (act != SWG_ACT_NONE || db) {
+  if (own_dz || db) {
     ActBwdArgs a{};
     a.dy = dy; a.lddy = lddy; a.z = z; a.ldz = ldz; a.db = db; a.M = M; a.N = N; a.act = act;
     a.beta = beta; a.accumulate = accumulate != 0;
-    if (act != SWG_ACT_NONE && (dx || dw)) {
+    if (own_dz) {
       a.dz = ws;
       a.lddz = plan.lddz;
       dz = {ws, plan.lddz, true};
     }
-    const hipError_t e = launch_act_bwd(
-        dtype, a, plan.act, reinterpret_cast<float*>(ws ? ws + plan.part_at : nullptr), hs);
+    float* part = sums ? reinterpret_cast<float*>(ws + plan.part_at) : nullptr;
+    const hipError_t e = launch_act_bwd(dtype, a, plan.act, part, hs);
     if (e != hipSuccess) return hip_status(e);
   }
   if (dx) {
     Product p{};
     p.a = dz;
-    p.b = {w, ldw, w_nk == 0};
+    p.b = {w, ldw, !nk};
     p.P = M; p.Q = K; p.R = N;
     p.out = dx; p.ldo = lddx;
-    const hipError_t e = launch_product(dtype, p, hs);
+    const hipError_t e = launch_product(dtype, p, plan_dx, ws_product, gemm_grid_cap(), hs);
     if (e != hipSuccess) return hip_status(e);
   }
   if (dw) {
@@ -944,13 +988,13 @@ swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
     p.a = {x, ldx, false};
     p.b = dz;
     p.P = K; p.Q = N; p.R = M;
-    if (w_nk) {
+    if (nk) {
       p.b = p.a;
       p.a = dz;
       p.P = N; p.Q = K;
     }
     p.out = dw; p.ldo = lddw; p.accumulate = accumulate != 0;
-    return hip_status(launch_product(dtype, p, hs));
+    return hip_status(launch_product(dtype, p, plan_dw, ws_product, gemm_grid_cap(), hs));
   }
   return SWG_OK;
 }

@@ -184,7 +184,10 @@ struct Product {
   float beta;
   bool accumulate;
 };
-hipError_t launch_product(int dtype, const Product& a, hipStream_t stream);
+hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
+                          hipStream_t stream);
+hipError_t launch_product16(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
+                            hipStream_t stream);
 
 // dz = dy act'(z) (dz null: not wanted) and db (null: not wanted)
 struct ActBwdArgs {

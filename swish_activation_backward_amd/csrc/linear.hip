@@ -3,9 +3,7 @@
 //
 // All three products are C[p, q] = sum_r A(p, r) B(q, r); an operand lies with its contraction
 // index contiguous (A[p ld + r]) or its rows (A[r ld + p]).
-#include "activation.hpp"
-#include "launch.hpp"
-#include "rows.hpp"
+#include "product.hpp"
 
 namespace swg {
 
@@ -17,17 +15,6 @@ namespace swg {
   } while (0)
 
 // ------------------------------------------------------------------ products
-// One element of the output from the fp32 sum.
-template <typename T>
-__device__ inline void finish(const Product& a, int64_t p, int64_t q, float v) {
-  if (a.bias) v += to_f32(static_cast<const T*>(a.bias)[q]);
-  if (a.z) static_cast<T*>(a.z)[p * a.ldz + q] = from_f32<T>(v);
-  v = activate(a.act, a.beta, v);
-  if (a.residual) v += to_f32(static_cast<const T*>(a.residual)[p * a.ldr + q]);
-  T* out = static_cast<T*>(a.out) + p * a.ldo + q;
-  *out = from_f32<T>(a.accumulate ? to_f32(*out) + v : v);
-}
-
 template <typename T>
 __global__ __launch_bounds__(256) void product_kernel(Product a, int64_t nq) {
   __shared__ float la[16][65], lb[16][65];
@@ -59,7 +46,7 @@ __global__ __launch_bounds__(256) void product_kernel(Product a, int64_t nq) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t p = p0 + tp + 16 * i, q = q0 + tq + 16 * j;
-      if (p < a.P && q < a.Q) finish<T>(a, p, q, acc[i][j]);
+      if (p < a.P && q < a.Q) finish<1, T>(a, p, q, &acc[i][j]);
     }
 }
 
@@ -69,9 +56,9 @@ template <typename T> static hipError_t product_t(const Product& a, hipStream_t 
   return hipSuccess;
 }
 
-hipError_t launch_product(int dtype, const Product& a, hipStream_t stream) {
-  if (dtype == 0) return product_t<bf16>(a, stream);
-  if (dtype == 1) return product_t<fp16>(a, stream);
+hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
+                          hipStream_t stream) {
+  if (dtype != 2) return launch_product16(dtype, a, p, ws, cus, stream);
   return product_t<float>(a, stream);
 }
 
@@ -110,8 +97,12 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const T* dy, int64_t lddy,
   };
   if (N - c >= 8) {
     columns(c, std::integral_constant<int, 8>());
-  } else {
-    for (int64_t col = c; col < N; ++col) columns(col, std::integral_constant<int, 1>());
+    return;
+  }
+  for (int64_t col = c; col < N; ++col) columns(col, std::integral_constant<int, 1>());
+  if (dz) {   // the rest of dz's rows takes part in dx's sums
+    for (int64_t r = r0; r < r1; ++r)
+      for (int64_t col = N; col < lddz; ++col) dz[r * lddz + col] = from_f32<T>(0.0f);
   }
 }
 

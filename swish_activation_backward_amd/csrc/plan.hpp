@@ -372,13 +372,94 @@ inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
   return p;
 }
 
+// One product of the linear layer: output [P, Q], contraction R.  16-bit tensors: tiles of edge
+// 64 f, the contraction cut into `splits` ranges of `len` whose fp32 sums [P, ldp] are joined in
+// order; operands that do not lie in rows of 16-byte multiples are laid out again (pack_a, pack_b)
+// in the workspace before.
+//
+// The tile and the split are those of the smallest estimate: rounds of items over the CUs, times an
+// item's stages (32 deep) and what it spends before and after them, plus the partial sums' trip
+// through memory and the launch that joins them.
+struct ProductPlan {
+  int f;
+  int64_t np, nq;
+  int64_t splits, len, ldp;
+  bool pack_a, pack_b;
+  size_t pack_a_at, pack_b_at, part_at;
+  size_t ws_bytes;
+};
+
+constexpr int64_t kProductStageNs[2] = {850, 400};    // one 32-deep stage, f = 4 / f = 2
+constexpr int64_t kProductItemNs[2] = {6000, 3000};   // first loads and epilogue
+constexpr int64_t kJoinNs = 3000;
+
+inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, int f, int64_t splits) {
+  const int64_t tiles = ceil_div(P, tile_edge(f)) * ceil_div(Q, tile_edge(f));
+  const int64_t len = ceil_div(R, splits);
+  const int64_t slots = f == 4 ? kGemmSlots : 2 * kGemmSlots;
+  int64_t stage = stage_ns(kProductStageNs, f);
+  if (f == 2 && tiles * splits > kGemmSlots) stage = stage * 3 / 2;   // two share a CU
+  const int64_t item = 4 * ceil_div(len, 4 * kTileR) * stage + stage_ns(kProductItemNs, f);
+  int64_t t = ceil_div(tiles * splits, slots) * item;
+  if (splits > 1) t += kJoinNs + splits * P * Q * 8 / kStreamBytesPerNs;
+  return t;
+}
+
+inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool pack_a,
+                                bool a_deep, bool pack_b, bool b_deep) {
+  ProductPlan p{};
+  p.f = 4;
+  p.splits = 1;
+  if (dtype != 2) {
+    int64_t best = -1;
+    for (int f = 4; f >= 2; f -= 2) {
+      const int64_t tiles = ceil_div(P, tile_edge(f)) * ceil_div(Q, tile_edge(f));
+      int64_t most = ceil_div(2 * kGemmSlots, tiles < 1 ? 1 : tiles);
+      if (most > R / 256) most = R / 256;
+      for (int64_t s = 1; s == 1 || s <= most; ++s) {
+        const int64_t t = product_ns(P, Q, R, f, s);
+        if (best < 0 || t < best) {
+          best = t;
+          p.f = f;
+          p.splits = s;
+        }
+      }
+    }
+  }
+  p.len = ceil_div(ceil_div(R, p.splits), 4 * kTileR) * 4 * kTileR;
+  p.splits = R > 0 ? ceil_div(R, p.len) : 1;
+  if (p.len < 1) p.len = 1;
+  p.np = ceil_div(P, tile_edge(p.f));
+  p.nq = ceil_div(Q, tile_edge(p.f));
+  p.ldp = ceil_div(Q, 8) * 8;
+  auto packed = [](int64_t rows, int64_t deep_len, bool deep) {
+    const int64_t n = deep ? rows : deep_len, c = deep ? deep_len : rows;
+    return (size_t)(n * (ceil_div(c, 8) * 8)) * 2;
+  };
+  if (dtype != 2 && R > 0 && pack_a) {
+    p.pack_a = true;
+    p.ws_bytes += packed(P, R, a_deep);
+  }
+  if (dtype != 2 && R > 0 && pack_b) {
+    p.pack_b = true;
+    p.pack_b_at = p.ws_bytes;
+    p.ws_bytes += packed(Q, R, b_deep);
+  }
+  if (p.splits > 1) {
+    p.part_at = p.ws_bytes;
+    p.ws_bytes += (size_t)(p.splits * P * p.ldp) * sizeof(float);
+  }
+  return p;
+}
+
 // Workspace of the linear layer's backward pass, from its start: dz (where there is an activation;
-// rows of a multiple of 8 elements), then the partial rows of db.
+// rows of a multiple of 8 elements), the partial rows of db, then what the products take one after
+// the other.
 struct LinearBwdPlan {
   ActBwdPlan act;
   int64_t lddz;
   size_t part_at;
-  size_t ws_bytes;
+  size_t product_at;
 };
 
 inline LinearBwdPlan plan_linear_bwd(int64_t M, int64_t N, int act, int dtype) {
@@ -386,7 +467,7 @@ inline LinearBwdPlan plan_linear_bwd(int64_t M, int64_t N, int act, int dtype) {
   p.act = plan_act_bwd(M, N);
   p.lddz = ceil_div(N, 8) * 8;
   p.part_at = act != 0 ? (size_t)(ceil_div(M * p.lddz * elem_size(dtype), 16) * 16) : 0;
-  p.ws_bytes = p.part_at + (size_t)(p.act.parts * p.act.np) * sizeof(float);
+  p.product_at = p.part_at + (size_t)(p.act.parts * p.act.np) * sizeof(float);
   return p;
 }
 

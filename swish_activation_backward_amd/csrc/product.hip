@@ -1,0 +1,494 @@
+// The linear layer's products for 16-bit tensors on the matrix cores:
+//   C[p, q] = sum over r of A(p, r) B(q, r)
+// An operand lies "deep" (its contraction index contiguous) or "flat" (its rows contiguous):
+//   y = x W:      x deep, W flat (deep where W is stored as its transpose)
+//   dx = dz W^T:  dz deep, W deep (flat)
+//   dW = x^T dz:  both flat
+//
+// A workgroup of four waves (2 x 2) owns a P x P tile of C, P = 64 F: F = 4, each wave 128 x 128
+// outputs = 4 x 4 MFMA tiles of 32 x 32 in 256 accumulators, or F = 2, each wave 64 x 64.  The
+// contraction advances in stages of 32 through a ring of four LDS slots that loads fill straight
+// from memory; a stage is multiplied from registers while the next one's fragments are read from
+// LDS and the stage after the next three is fetched.  A deep operand's stage is [P rows][32], read
+// 16 bytes a lane; a flat one's [32][P], read with the transposing LDS read.  Workgroups are
+// persistent and the ring streams across their tiles.
+//
+// A tile's sums pass through LDS (a part of its own, wave by wave) on their way out, so that the
+// epilogue reads and writes rows of 16 bytes a lane and its code exists once: a wave's 256
+// accumulators have fixed registers, and bias, activation and residual spelled out for each would
+// not fit the instruction cache.
+//
+// Operands have rows of 16-byte multiples at 16-byte boundaries (others are laid out again first);
+// what lies past their edges is fetched at offsets beyond the buffer window and arrives as zeros.
+#include <utility>
+
+#include "mma.hpp"
+#include "product.hpp"
+
+namespace swg {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kDepth = 32;
+
+template <int F> struct Shape {
+  static constexpr int P = 64 * F;                 // tile edge
+  static constexpr int WR = 32 * F;                // rows and columns of a wave
+  static constexpr int SIDE = P * kDepth;          // elements of one operand's stage
+  static constexpr int SLOT = 2 * SIDE;
+  static constexpr int LOADS = 2 * F;              // 1 KiB loads of a wave a stage
+  static constexpr int OUTW = F == 4 ? 64 : 32;    // columns of the epilogue's 32-row blocks
+  static constexpr int OUT = 32 * OUTW;            // floats of a wave's part of the epilogue
+  static constexpr int WAVES = F == 4 ? 1 : 2;     // waves a SIMD (workgroups a CU)
+};
+
+// What a lane needs of one operand: its loads' offsets into a stage's window and the column (along
+// the contiguous index) that each fetches, and its fragments' place in a slot.
+template <bool DEEP, int F> struct Side;
+
+template <int F> struct Side<true, F> {
+  uint32_t voff[F];
+  int col;
+  int at[2];
+  __device__ inline Side(int wave, int part, int lane, int64_t ld) {
+    const int sw = (lane >> 4) & 3;   // xsw of the rows below: multiples of 16 do not change it
+    col = ((lane & 3) ^ sw) * 8;
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const int row = 16 * F * wave + 16 * i + (lane >> 2);
+      voff[i] = (uint32_t)row * (uint32_t)(ld * 2) + (uint32_t)col * 2u;
+    }
+    const int r = part * Shape<F>::WR + (lane & 31);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+      at[kk] = r * kDepth + (((2 * kk + (lane >> 5)) ^ xsw(r)) << 3);
+  }
+  template <typename T, int KK, int I>
+  __device__ inline typename Mfma<T>::frag read(const uint16_t* slot) const {
+    return *reinterpret_cast<const typename Mfma<T>::frag*>(slot + at[KK] + I * 32 * kDepth);
+  }
+  __device__ inline int column(int) const { return col; }
+};
+
+template <int F> struct Side<false, F> {
+  static constexpr int P = Shape<F>::P;
+  uint32_t voff[F];
+  int col[2];
+  int at[F];
+  __device__ inline Side(int wave, int part, int lane, int64_t ld) {
+    constexpr int RPL = 1024 / (2 * P), LPR = 64 / RPL;   // rows a load, lanes a row
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+      const int row = 8 * wave + RPL * i + lane / LPR;
+      const int c = ((lane % LPR) ^ wsw(row)) * 8;        // of two values: row % 4 repeats
+      col[i & 1] = c;
+      voff[i] = (uint32_t)row * (uint32_t)(ld * 2) + (uint32_t)c * 2u;
+    }
+    w_lane_offsets<F, P>(lane, part * (Shape<F>::WR / 8), at);
+  }
+  template <typename T, int KK, int I>
+  __device__ inline typename Mfma<T>::frag read(const uint16_t* slot) const {
+    return tr_frag<T, P>(slot + 16 * KK * P + at[I]);
+  }
+  __device__ inline int column(int i) const { return col[i & 1]; }
+};
+
+// One operand's part of a stage: window, scalar offset and the columns left in it.
+struct Fetch {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t soff;
+  int left;
+};
+
+// Rows row0 .. row0 + P of an operand of `rows`, contraction k .. k + 32 up to `end`.
+template <bool DEEP, int P, typename T>
+__device__ inline Fetch fetch(const T* base, int64_t ld, int row0, int64_t rows, int k, int end) {
+  Fetch f;
+  int64_t first, n;
+  if (DEEP) {
+    first = row0;
+    n = rows - row0 < P ? rows - row0 : P;
+    f.soff = (uint32_t)k * 2u;
+    f.left = end - k;
+  } else {
+    first = k;
+    n = end - k < kDepth ? end - k : kDepth;
+    f.soff = (uint32_t)row0 * 2u;
+    f.left = (int)(rows - row0);
+  }
+  if (n <= 0) first = 0;
+  f.r = make_rsrc(uniform_ptr(base + first * ld),
+                  __builtin_amdgcn_readfirstlane(clamp_bytes(n, ld * 2)));
+  f.soff = __builtin_amdgcn_readfirstlane(f.soff);
+  return f;
+}
+
+struct Stage {
+  Fetch a, b;
+  const uint16_t* dst;   // the wave's part of the slot
+};
+
+// A piece of work: a tile and a range of the contraction.
+struct Item {
+  int split, p0, q0, begin, end, stages;
+};
+
+struct Grid {            // tiles, group of tile rows, ranges of `len`, items
+  int np, nq, group;
+  int64_t tiles, len, items;
+};
+
+// Tiles run down `group` tile rows before they move on a column, so that those that run at once on
+// an XCD (consecutive ones) share rows and columns alike.
+template <int P> __device__ inline Item item(const Grid& g, int64_t L, bool live, int64_t R) {
+  Item t;
+  const int64_t l = live ? L : 0;
+  t.split = (int)(l / g.tiles);
+  const int tile = (int)(l % g.tiles);
+  const int band = tile / (g.group * g.nq), in = tile % (g.group * g.nq);
+  const int rows = g.np - band * g.group < g.group ? g.np - band * g.group : g.group;
+  t.p0 = (band * g.group + in % rows) * P;
+  t.q0 = (in / rows) * P;
+  const int64_t b = t.split * g.len, e = b + g.len < R ? b + g.len : R;
+  t.begin = (int)b;
+  t.end = live ? (int)e : (int)b;      // nothing to fetch past the last item
+  t.stages = (int)((e - b + 4 * kDepth - 1) / (4 * kDepth)) * 4;
+  if (t.stages < 4) t.stages = 4;      // one round of the ring
+  t.p0 = __builtin_amdgcn_readfirstlane(t.p0);
+  t.q0 = __builtin_amdgcn_readfirstlane(t.q0);
+  t.begin = __builtin_amdgcn_readfirstlane(t.begin);
+  t.end = __builtin_amdgcn_readfirstlane(t.end);
+  t.stages = __builtin_amdgcn_readfirstlane(t.stages);
+  return t;
+}
+
+template <typename T, int F> struct Frags {
+  typename Mfma<T>::frag a[2][F], b[2][F];
+};
+
+// Load E (0 .. 2F - 1) of a stage: the first F of A, the others of B.
+template <bool AD, bool BD, int F, int E>
+__device__ inline void load(const Stage& s, const Side<AD, F>& a, const Side<BD, F>& b) {
+  constexpr int i = E % F;
+  // a wave's loads of an operand fill consecutive KiB of the slot
+  if constexpr (E < F) {
+    const uint32_t v = a.column(i) < s.a.left ? a.voff[i] : kOOB;
+    dma16s<i * 1024>(s.a.r, v, s.a.soff, s.dst);
+  } else {
+    const uint32_t v = b.column(i) < s.b.left ? b.voff[i] : kOOB;
+    dma16s<Shape<F>::SIDE * 2 + i * 1024>(s.b.r, v, s.b.soff, s.dst);
+  }
+}
+
+template <bool AD, bool BD, int F, int... E>
+__device__ inline void load_all(std::integer_sequence<int, E...>, const Stage& s,
+                                const Side<AD, F>& a, const Side<BD, F>& b) {
+  (load<AD, BD, F, E>(s, a, b), ...);
+}
+
+// Fragment G (0 .. 4F - 1) of a slot: contraction half G / 2F, then A's blocks, then B's.
+template <typename T, bool AD, bool BD, int F, int G>
+__device__ inline void read_one(const uint16_t* slot, const Side<AD, F>& a, const Side<BD, F>& b,
+                                Frags<T, F>& f) {
+  constexpr int kk = G / (2 * F), i = G % (2 * F);
+  if constexpr (i < F) f.a[kk][i] = a.template read<T, kk, i>(slot);
+  else f.b[kk][i - F] = b.template read<T, kk, i - F>(slot + Shape<F>::SIDE);
+}
+
+template <typename T, bool AD, bool BD, int F, int... G>
+__device__ inline void read_all(std::integer_sequence<int, G...>, const uint16_t* slot,
+                                const Side<AD, F>& a, const Side<BD, F>& b, Frags<T, F>& f) {
+  (read_one<T, AD, BD, F, G>(slot, a, b, f), ...);
+}
+
+// Group G (0 .. 4F - 1) of a step: F / 2 MFMAs of the stage in f, a fragment of the next stage and,
+// in odd groups, a load, kept in this order by the scheduling fence.
+template <typename T, bool AD, bool BD, int F, bool NEXT, int G>
+__device__ inline void group(f32x16 (&acc)[F][F], const Frags<T, F>& f, Frags<T, F>& fn,
+                             const uint16_t* next, const Stage& s, const Side<AD, F>& a,
+                             const Side<BD, F>& b) {
+#pragma unroll
+  for (int e = 0; e < F / 2; ++e) {
+    const int q = G * (F / 2) + e, kk = q / (F * F), i = (q / F) % F, j = q % F;
+    acc[i][j] = Mfma<T>::mma(f.a[kk][i], f.b[kk][j], acc[i][j]);
+  }
+  if constexpr (NEXT) read_one<T, AD, BD, F, G>(next, a, b, fn);
+  if constexpr ((G & 1) != 0) load<AD, BD, F, (G >> 1)>(s, a, b);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <typename T, bool AD, bool BD, int F, bool NEXT, int... G>
+__device__ inline void groups(std::integer_sequence<int, G...>, f32x16 (&acc)[F][F],
+                              const Frags<T, F>& f, Frags<T, F>& fn, const uint16_t* next,
+                              const Stage& s, const Side<AD, F>& a, const Side<BD, F>& b) {
+  (group<T, AD, BD, F, NEXT, G>(acc, f, fn, next, s, a, b), ...);
+}
+
+// ---- epilogue
+// Float (row, column) of a block in the wave's part of LDS.  Rows 4 apart, which the two halves of
+// a wave write at once, use different banks.
+template <int W> __device__ inline int out_at(int row, int col) {
+  return (row * W + col) ^ (((row >> 2) & 1) << 5);
+}
+
+// 32 x 32 sums of one MFMA tile into columns c0 .. of the block
+template <int W>
+__device__ inline void put_tile(const f32x16& v, float* out, int lane, int c0) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    out[out_at<W>(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), c0 + (lane & 31))] = v[r];
+}
+
+// Block B: MFMA tiles (B / 2, 2 (B % 2)) and the one to its right (F = 4), tile (B / 2, B % 2) (F = 2)
+template <int F, int B>
+__device__ inline void put_block(const f32x16 (&acc)[F][F], float* out, int lane) {
+  constexpr int W = Shape<F>::OUTW;
+  if constexpr (F == 4) {
+    put_tile<W>(acc[B / 2][2 * (B % 2)], out, lane, 0);
+    put_tile<W>(acc[B / 2][2 * (B % 2) + 1], out, lane, 32);
+  } else {
+    put_tile<W>(acc[B / 2][B % 2], out, lane, 0);
+  }
+}
+
+template <typename T, int F>
+__device__ inline void epilogue(const f32x16 (&acc)[F][F], const Product& g, float* part,
+                                int64_t ldp, float* out, int lane, int64_t p0, int64_t q0) {
+  constexpr int W = Shape<F>::OUTW, LANES = W / 8, ROWS = 64 / LANES;
+  asm volatile("" : "+v"(lane));   // keeps what follows from lane out of the main loop's registers
+#pragma unroll 1
+  for (int blk = 0; blk < 2 * F; ++blk) {
+    switch (blk) {
+      case 0: put_block<F, 0>(acc, out, lane); break;
+      case 1: put_block<F, 1>(acc, out, lane); break;
+      case 2: put_block<F, 2>(acc, out, lane); break;
+      case 3: put_block<F, 3>(acc, out, lane); break;
+      case 4: if constexpr (F == 4) put_block<F, 4>(acc, out, lane); break;
+      case 5: if constexpr (F == 4) put_block<F, 5>(acc, out, lane); break;
+      case 6: if constexpr (F == 4) put_block<F, 6>(acc, out, lane); break;
+      default: if constexpr (F == 4) put_block<F, 7>(acc, out, lane); break;
+    }
+    const int64_t pb = p0 + 32 * (blk / 2), q = q0 + W * (blk % 2) + 8 * (lane % LANES);
+#pragma unroll 1
+    for (int row = lane / LANES; row < 32; row += ROWS) {
+      float v[8];
+      const float* src = out + out_at<W>(row, 8 * (lane % LANES));
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+      const int64_t p = pb + row;
+      if (p >= g.P || q >= g.Q) continue;
+      if (part) {
+        f32x4* dst = reinterpret_cast<f32x4*>(part + p * ldp + q);
+        dst[0] = lo;
+        dst[1] = hi;
+      } else {
+        finish_chunk<T>(g, p, q, v);
+      }
+    }
+  }
+}
+
+template <typename T, bool AD, bool BD, int F>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<F>::WAVES, Shape<F>::WAVES)))
+void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
+  constexpr int P = Shape<F>::P, SLOT = Shape<F>::SLOT, LOADS = Shape<F>::LOADS;
+  __shared__ __attribute__((aligned(1024))) uint16_t ring[4 * SLOT];
+  __shared__ __attribute__((aligned(16))) float outs[4 * Shape<F>::OUT];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave / 2, wq = wave % 2;
+  const Side<AD, F> sa(wave, wp, lane, g.a.ld);
+  const Side<BD, F> sb(wave, wq, lane, g.b.ld);
+  const T* pa = static_cast<const T*>(g.a.p);
+  const T* pb = static_cast<const T*>(g.b.p);
+  const int64_t G = gridDim.x, first = xcd_remap(blockIdx.x, G);
+  const int64_t mine = grid.items > first ? (grid.items - first + G - 1) / G : 0;
+  auto stage = [&](const Item& t, int st, int slot) {
+    int k = t.begin + st * kDepth;
+    asm volatile("" : "+s"(k));   // formed here: hoisted they would stay live, and spill
+    Stage s;
+    s.a = fetch<AD, P>(pa, g.a.ld, t.p0, g.P, k, t.end);
+    s.b = fetch<BD, P>(pb, g.b.ld, t.q0, g.Q, k, t.end);
+    s.dst = ring + slot * SLOT + wave * F * 512;
+    return s;
+  };
+  // One step u: the fragments of the stage in slot u are in registers and the next three stages in
+  // flight.  Once this wave's loads of the next stage have landed and its LDS reads are done, the
+  // barrier says so of every wave: slot u may be filled again and slot u + 1 read.  Every step
+  // issues the same number of loads, so that "landed" is "at most two stages outstanding".
+#define SWG_STEP(t, st, u, NEXT)                                                            \
+  do {                                                                                      \
+    __builtin_amdgcn_s_waitcnt(vmcnt_le(2 * LOADS));                                        \
+    __builtin_amdgcn_s_waitcnt(kLgkmcnt0);                                                  \
+    SWG_COMPILER_FENCE();                                                                   \
+    __builtin_amdgcn_s_barrier();                                                           \
+    SWG_COMPILER_FENCE();                                                                   \
+    const Stage s_ = stage((t), (st), (u));                                                 \
+    groups<T, AD, BD, F, (NEXT)>(std::make_integer_sequence<int, 4 * F>{}, acc,             \
+                                 frags[(u) & 1], frags[((u) + 1) & 1],                      \
+                                 ring + (((u) + 1) & 3) * SLOT, s_, sa, sb);                \
+  } while (0)
+
+  f32x16 acc[F][F];
+  Frags<T, F> frags[2];
+  Item cur = item<P>(grid, first, mine > 0, g.R);
+  constexpr std::make_integer_sequence<int, LOADS> kLoads{};
+  load_all<AD, BD, F>(kLoads, stage(cur, 0, 0), sa, sb);
+  load_all<AD, BD, F>(kLoads, stage(cur, 1, 1), sa, sb);
+  load_all<AD, BD, F>(kLoads, stage(cur, 2, 2), sa, sb);
+  load_all<AD, BD, F>(kLoads, stage(cur, 3, 3), sa, sb);
+  __builtin_amdgcn_s_waitcnt(vmcnt_le(3 * LOADS));
+  SWG_COMPILER_FENCE();
+  __builtin_amdgcn_s_barrier();
+  SWG_COMPILER_FENCE();
+  for (int64_t j = 0; j < mine; ++j) {
+    const Item nxt = item<P>(grid, first + (j + 1) * G, j + 1 < mine, g.R);
+#pragma unroll
+    for (int a = 0; a < F; ++a)
+#pragma unroll
+      for (int b = 0; b < F; ++b) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+        asm volatile("" : "+a"(acc[a][b]));   // in AGPRs from here on: no copies at the loop
+      }
+    read_all<T, AD, BD, F>(std::make_integer_sequence<int, 4 * F>{}, ring, sa, sb, frags[0]);
+    for (int t = 4; t < cur.stages; t += 4) {
+      SWG_STEP(cur, t, 0, true);
+      SWG_STEP(cur, t + 1, 1, true);
+      SWG_STEP(cur, t + 2, 2, true);
+      SWG_STEP(cur, t + 3, 3, true);
+    }
+    SWG_STEP(nxt, 0, 0, true);
+    SWG_STEP(nxt, 1, 1, true);
+    SWG_STEP(nxt, 2, 2, true);
+    SWG_STEP(nxt, 3, 3, false);   // the next item's first stage is read after the epilogue
+    float* to = part ? part + (int64_t)cur.split * g.P * ldp : nullptr;
+    epilogue<T, F>(acc, g, to, ldp, outs + wave * Shape<F>::OUT, lane,
+                   (int64_t)cur.p0 + wp * Shape<F>::WR, (int64_t)cur.q0 + wq * Shape<F>::WR);
+    cur = nxt;
+  }
+#undef SWG_STEP
+  __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
+}
+
+// out from the `splits` partial sums, in order; a thread takes 8 columns of a row.
+template <typename T>
+__global__ __launch_bounds__(256) void product_join_kernel(Product g, const float* part,
+                                                           int64_t splits, int64_t ldp,
+                                                           int64_t chunks) {
+  const int64_t total = g.P * chunks, plane = g.P * ldp;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
+       e += (int64_t)gridDim.x * 256) {
+    const int64_t p = e / chunks, q = (e % chunks) * 8;
+    const float* src = part + p * ldp + q;
+    f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
+    for (int64_t s = 1; s < splits; ++s) {
+      lo += *reinterpret_cast<const f32x4*>(src + s * plane);
+      hi += *reinterpret_cast<const f32x4*>(src + s * plane + 4);
+    }
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+    finish_chunk<T>(g, p, q, v);
+  }
+}
+
+// rows [n][cols] again with rows of ld elements, zeros past their end; a thread takes 8 columns
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* src, int64_t lds, T* dst, int64_t ldd,
+                                                   int64_t n, int64_t cols) {
+  const int64_t chunks = ldd / 8, total = n * chunks;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
+       e += (int64_t)gridDim.x * 256) {
+    const int64_t r = e / chunks, c = (e % chunks) * 8;
+    Chunk<T> v;
+    if (c + 8 <= cols) {
+      v.load(src + r * lds + c);
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? to_f32(src[r * lds + c + i]) : 0.0f;
+      v.narrow(f);
+    }
+    *reinterpret_cast<u32x4*>(dst + r * ldd + c) = v.v[0];
+  }
+}
+
+unsigned stream_grid(int64_t items) {
+  const int64_t n = ceil_div(items, 256);
+  return (unsigned)(n < kMaxStreamBlocks ? n : kMaxStreamBlocks);
+}
+
+template <typename T, bool AD, bool BD, int F>
+hipError_t tiles(const Product& g, const Grid& grid, float* part, int64_t ldp, int cus,
+                 hipStream_t stream) {
+  const int64_t slots = (int64_t)cus * Shape<F>::WAVES;
+  const int64_t n = grid.items < slots ? grid.items : slots;
+  SWG_LAUNCH((product16_kernel<T, AD, BD, F>), dim3((unsigned)n), dim3(kThreads), 0, stream, g,
+             grid, part, ldp);
+  return hipGetLastError();
+}
+
+template <typename T, int F>
+hipError_t layouts(const Product& g, const Grid& grid, float* part, int64_t ldp, int cus,
+                   hipStream_t stream) {
+  if (g.a.deep && !g.b.deep) return tiles<T, true, false, F>(g, grid, part, ldp, cus, stream);
+  if (g.a.deep) return tiles<T, true, true, F>(g, grid, part, ldp, cus, stream);
+  return tiles<T, false, false, F>(g, grid, part, ldp, cus, stream);
+}
+
+// An operand again in the workspace with rows of 16-byte multiples
+template <typename T>
+hipError_t pack(Operand& o, int64_t rows, int64_t R, void* to, hipStream_t stream) {
+  const int64_t n = o.deep ? rows : R, cols = o.deep ? R : rows, ld = ceil_div(cols, 8) * 8;
+  SWG_LAUNCH((pack_kernel<T>), dim3(stream_grid(n * (ld / 8))), dim3(256), 0, stream,
+             static_cast<const T*>(o.p), o.ld, static_cast<T*>(to), ld, n, cols);
+  o.p = to;
+  o.ld = ld;
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t product16_t(Product g, const ProductPlan& p, void* ws, int cus, hipStream_t stream) {
+  char* w = static_cast<char*>(ws);
+  if (g.R == 0) {   // nothing is fetched
+    g.a.p = g.b.p = nullptr;
+    g.a.ld = g.b.ld = 8;
+  }
+  if (p.pack_a) {
+    const hipError_t e = pack<T>(g.a, g.P, g.R, w + p.pack_a_at, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (p.pack_b) {
+    const hipError_t e = pack<T>(g.b, g.Q, g.R, w + p.pack_b_at, stream);
+    if (e != hipSuccess) return e;
+  }
+  Grid grid;
+  grid.np = (int)p.np;
+  grid.nq = (int)p.nq;
+  grid.group = 4;
+  grid.tiles = p.np * p.nq;
+  grid.len = p.len;
+  grid.items = grid.tiles * p.splits;
+  float* part = p.splits > 1 ? reinterpret_cast<float*>(w + p.part_at) : nullptr;
+  hipError_t e = p.f == 4 ? layouts<T, 4>(g, grid, part, p.ldp, cus, stream)
+                          : layouts<T, 2>(g, grid, part, p.ldp, cus, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t chunks = ceil_div(g.Q, 8);
+  SWG_LAUNCH((product_join_kernel<T>), dim3(stream_grid(g.P * chunks)), dim3(256), 0, stream, g,
+             part, p.splits, p.ldp, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_product16(int dtype, const Product& g, const ProductPlan& p, void* ws, int cus,
+                            hipStream_t stream) {
+  return dtype == 0 ? product16_t<bf16>(g, p, ws, cus, stream)
+                    : product16_t<fp16>(g, p, ws, cus, stream);
+}
+
+}  // namespace swg
