@@ -833,15 +833,16 @@ bool rows16_ok(const void* p, int64_t ld, int64_t es) {
 // Rows of x and W that are no multiple of 8 long end inside a 16-byte vector.  dz as the call
 // itself lays it out is never loose; dy in its place may be.
 ProductPlan plan_linear_fwd(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool x, bool w) {
-  return plan_product(M, N, K, dtype, x || K % 8 != 0, true, w || (nk ? K : N) % 8 != 0, nk);
+  return plan_product(M, N, K, dtype, x || K % 8 != 0, true, w || (nk ? K : N) % 8 != 0, nk,
+                      g_tile_f);
 }
 ProductPlan plan_linear_dx(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool dz, bool w) {
-  return plan_product(M, K, N, dtype, dz, true, w || (nk ? K : N) % 8 != 0, !nk);
+  return plan_product(M, K, N, dtype, dz, true, w || (nk ? K : N) % 8 != 0, !nk, g_tile_f);
 }
 ProductPlan plan_linear_dw(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool x, bool dz) {
   x = x || K % 8 != 0;
-  return nk ? plan_product(N, K, M, dtype, dz, false, x, false)
-            : plan_product(K, N, M, dtype, x, false, dz, false);
+  return nk ? plan_product(N, K, M, dtype, dz, false, x, false, g_tile_f)
+            : plan_product(K, N, M, dtype, x, false, dz, false, g_tile_f);
 }
 Span weight_span(const void* w, int64_t K, int64_t N, int64_t ldw, int nk, int64_t es) {
   return {w, w ? (nk ? rows_bytes(N, K, ldw, es) : rows_bytes(K, N, ldw, es)) : 0};

@@ -64,69 +64,119 @@ hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, voi
 
 // ------------------------------------------------------------------ dz and db
 // dz = dy act'(z) rounded to T, the operand of both products; db sums its fp32 values: one partial
-// row per block of rows, then those in order.  A thread takes 8 columns, or the up to 7 at the end.
+// row per block of rows, then those in order.  A workgroup takes 512 columns, 8 a thread (or the up
+// to 7 at the end), 4 rows at once, and a thread has the loads of 4 of its rows in flight.
+constexpr int kActTx = 64, kActTy = 4, kActFlight = 4;
+
 template <typename T>
-__global__ __launch_bounds__(256) void act_bwd_kernel(const T* dy, int64_t lddy, const T* z,
-                                                      int64_t ldz, T* dz, int64_t lddz, float* part,
-                                                      int64_t Np, int64_t M, int64_t N,
-                                                      int64_t rows, int act, float beta) {
-  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (c >= N) return;
-  const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = r0 + rows < M ? r0 + rows : M;
-  auto columns = [&](int64_t col, auto size) {
-    constexpr int n = decltype(size)::value;
-    float s[n];
+__global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, float* part, int64_t Np,
+                                                      int64_t rows) {
+  __shared__ float red[kActTy][kActTx][8];
+  const int tx = threadIdx.x % kActTx, ty = threadIdx.x / kActTx;
+  const int64_t c = ((int64_t)blockIdx.x * kActTx + tx) * 8;
+  const int64_t r0 = (int64_t)blockIdx.y * rows, r1 = r0 + rows < a.M ? r0 + rows : a.M;
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* z = static_cast<const T*>(a.z);
+  T* dz = static_cast<T*>(a.dz);
+  float s[8];
 #pragma unroll
-    for (int i = 0; i < n; ++i) s[i] = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-      float d[n], f[n];
-      load_part<n>(dy + r * lddy + col, d);
-      if (act != kActNone) {
-        load_part<n>(z + r * ldz + col, f);
+  for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+  if (c + 8 <= a.N) {
+    for (int64_t r = r0 + ty; r < r1; r += kActTy * kActFlight) {
+      Chunk<T> d[kActFlight], f[kActFlight];
 #pragma unroll
-        for (int i = 0; i < n; ++i) d[i] *= activation_slope(act, beta, f[i]);
+      for (int k = 0; k < kActFlight; ++k) {
+        const int64_t row = r + k * kActTy;
+        d[k].zero();
+        f[k].zero();
+        if (row < r1) {
+          d[k].load_stream(dy + row * a.lddy + c);
+          if (a.act != kActNone) f[k].load_stream(z + row * a.ldz + c);
+        }
       }
-      if (dz) store_part<n>(dz + r * lddz + col, d);
 #pragma unroll
-      for (int i = 0; i < n; ++i) s[i] += d[i];
-    }
-    if (part) {
+      for (int k = 0; k < kActFlight; ++k) {
+        const int64_t row = r + k * kActTy;
+        float g[8], v[8];
+        d[k].widen(g);
+        if (a.act != kActNone) {
+          f[k].widen(v);
 #pragma unroll
-      for (int i = 0; i < n; ++i) part[blockIdx.y * Np + col + i] = s[i];
+          for (int i = 0; i < 8; ++i) g[i] *= activation_slope(a.act, a.beta, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += g[i];
+        if (dz && row < r1) {
+          Chunk<T> o;
+          o.narrow(g);
+          o.store_stream(dz + row * a.lddz + c);
+        }
+      }
     }
-  };
-  if (N - c >= 8) {
-    columns(c, std::integral_constant<int, 8>());
-    return;
+  } else if (c < a.N) {
+    const int n = (int)(a.N - c);
+    for (int64_t r = r0 + ty; r < r1; r += kActTy) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float g = 0.0f;
+        if (i < n) {
+          g = to_f32(dy[r * a.lddy + c + i]);
+          if (a.act != kActNone) g *= activation_slope(a.act, a.beta, to_f32(z[r * a.ldz + c + i]));
+        }
+        s[i] += g;
+        // 0 past the row's end, which takes part in dx's sums
+        if (dz && c + i < a.lddz) dz[r * a.lddz + c + i] = from_f32<T>(g);
+      }
+    }
   }
-  for (int64_t col = c; col < N; ++col) columns(col, std::integral_constant<int, 1>());
-  if (dz) {   // the rest of dz's rows takes part in dx's sums
-    for (int64_t r = r0; r < r1; ++r)
-      for (int64_t col = N; col < lddz; ++col) dz[r * lddz + col] = from_f32<T>(0.0f);
+  if (part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[ty][tx][i] = s[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < kActTx * 8; e += 256) {
+    const int64_t col = (int64_t)blockIdx.x * kActTx * 8 + e;
+    if (col >= a.N) break;
+    const float* p = &red[0][0][0] + e;
+    part[blockIdx.y * Np + col] = (p[0] + p[kActTx * 8]) + (p[2 * kActTx * 8] + p[3 * kActTx * 8]);
   }
 }
 
+// Sums the partial rows: 4 groups of 4 columns to a workgroup, 64 threads a group.
 template <typename T>
 __global__ __launch_bounds__(256) void bias_finalize_kernel(const float* part, int64_t nparts,
                                                             T* db, int64_t N, int64_t Np,
                                                             bool accumulate) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
-  float s = 0.0f;
-  for (int64_t p = 0; p < nparts; ++p) s += part[p * Np + c];
-  db[c] = from_f32<T>(accumulate ? to_f32(db[c]) + s : s);
+  constexpr int Q = 4, P = 256 / Q;
+  __shared__ f32x4 red[P][Q];
+  const int q = threadIdx.x % Q, lane = threadIdx.x / Q;
+  const int64_t c = ((int64_t)blockIdx.x * Q + q) * 4;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < Np) {
+#pragma unroll 4
+    for (int64_t p = lane; p < nparts; p += P)
+      s += *reinterpret_cast<const f32x4*>(part + p * Np + c);
+  }
+  red[lane][q] = s;
+  __syncthreads();
+  for (int n = P / 2; n > 0; n >>= 1) {
+    if (lane < n) red[lane][q] += red[lane + n][q];
+    __syncthreads();
+  }
+  const int64_t col = (int64_t)blockIdx.x * 4 * Q + threadIdx.x;
+  if (threadIdx.x >= 4 * Q || col >= N) return;
+  const float v = red[0][threadIdx.x >> 2][threadIdx.x & 3];
+  db[col] = from_f32<T>(accumulate ? to_f32(db[col]) + v : v);
 }
 
 template <typename T>
 static hipError_t act_bwd_t(const ActBwdArgs& a, const ActBwdPlan& p, float* part,
                             hipStream_t stream) {
   if (a.M > 0)
-    SWG_TRY(SWG_LAUNCH((act_bwd_kernel<T>), dim3((unsigned)ceil_div(a.N, 2048), (unsigned)p.parts),
-                       dim3(256), 0, stream, static_cast<const T*>(a.dy), a.lddy,
-                       static_cast<const T*>(a.z), a.ldz, static_cast<T*>(a.dz), a.lddz,
-                       a.db ? part : nullptr, p.np, a.M, a.N, p.rows, a.act, a.beta));
+    SWG_TRY(SWG_LAUNCH((act_bwd_kernel<T>),
+                       dim3((unsigned)ceil_div(a.N, 8 * kActTx), (unsigned)p.parts), dim3(256), 0,
+                       stream, a, a.db ? part : nullptr, p.np, p.rows));
   if (!a.db) return hipSuccess;
-  SWG_TRY(SWG_LAUNCH((bias_finalize_kernel<T>), dim3((unsigned)ceil_div(a.N, 256)), dim3(256), 0,
+  SWG_TRY(SWG_LAUNCH((bias_finalize_kernel<T>), dim3((unsigned)ceil_div(a.N, 16)), dim3(256), 0,
                      stream, part, a.M > 0 ? p.parts : 0, static_cast<T*>(a.db), a.N, p.np,
                      a.accumulate));
   return hipSuccess;

@@ -367,7 +367,10 @@ struct ActBwdPlan {
 inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
   ActBwdPlan p{};
   p.np = ceil_div(N, 4) * 4;
-  p.rows = M > 256 * 16 ? ceil_div(M, 256) : 16;
+  // about 2048 workgroups of 512 columns, 16 rows at least
+  int64_t blocks = ceil_div(2048, ceil_div(N < 1 ? 1 : N, 512));
+  if (blocks > 512) blocks = 512;
+  p.rows = M > blocks * 16 ? ceil_div(M, blocks) : 16;
   p.parts = ceil_div(M, p.rows);
   return p;
 }
@@ -379,7 +382,7 @@ inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
 //
 // The tile and the split are those of the smallest estimate: rounds of items over the CUs, times an
 // item's stages (32 deep) and what it spends before and after them, plus the partial sums' trip
-// through memory and the launch that joins them.
+// through memory and the launch that joins them.  force_f: 4 or 2 overrides the tile.
 struct ProductPlan {
   int f;
   int64_t np, nq;
@@ -406,13 +409,14 @@ inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, int f, int64_t splits
 }
 
 inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool pack_a,
-                                bool a_deep, bool pack_b, bool b_deep) {
+                                bool a_deep, bool pack_b, bool b_deep, int force_f) {
   ProductPlan p{};
   p.f = 4;
   p.splits = 1;
   if (dtype != 2) {
     int64_t best = -1;
     for (int f = 4; f >= 2; f -= 2) {
+      if (force_f != 0 && f != force_f) continue;
       const int64_t tiles = ceil_div(P, tile_edge(f)) * ceil_div(Q, tile_edge(f));
       int64_t most = ceil_div(2 * kGemmSlots, tiles < 1 ? 1 : tiles);
       if (most > R / 256) most = R / 256;

@@ -252,11 +252,34 @@ __device__ inline void put_block(const f32x16 (&acc)[F][F], float* out, int lane
   }
 }
 
+// The wave's sums at (p0, q0) on their way out, a block of 32 rows after the other.  What the
+// epilogue reads for a block (the residual, or the old contents) is loaded a block ahead.
 template <typename T, int F>
 __device__ inline void epilogue(const f32x16 (&acc)[F][F], const Product& g, float* part,
                                 int64_t ldp, float* out, int lane, int64_t p0, int64_t q0) {
-  constexpr int W = Shape<F>::OUTW, LANES = W / 8, ROWS = 64 / LANES;
+  constexpr int W = Shape<F>::OUTW, LANES = W / 8, ROWS = 64 / LANES, PASSES = 32 / ROWS;
   asm volatile("" : "+v"(lane));   // keeps what follows from lane out of the main loop's registers
+  const int row = lane / LANES, col = 8 * (lane % LANES);
+  const int64_t q = q0 + col;
+  const T* more = part ? nullptr
+                       : static_cast<const T*>(g.accumulate ? g.out : g.residual);
+  const int64_t ldm = g.accumulate ? g.ldo : g.ldr;
+  Chunk<T> next[PASSES], bias[2];
+  auto load = [&](int blk) {
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const int64_t p = p0 + 32 * (blk / 2) + row + ROWS * k, c = q + W * (blk % 2);
+      next[k].zero();
+      if (more && p < g.P && c + 8 <= g.Q) next[k].load_stream(more + p * ldm + c);
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    bias[h].zero();
+    if (g.bias && !part && q + W * h + 8 <= g.Q)
+      bias[h].load(static_cast<const T*>(g.bias) + q + W * h);
+  }
+  load(0);
 #pragma unroll 1
   for (int blk = 0; blk < 2 * F; ++blk) {
     switch (blk) {
@@ -269,24 +292,46 @@ __device__ inline void epilogue(const f32x16 (&acc)[F][F], const Product& g, flo
       case 6: if constexpr (F == 4) put_block<F, 6>(acc, out, lane); break;
       default: if constexpr (F == 4) put_block<F, 7>(acc, out, lane); break;
     }
-    const int64_t pb = p0 + 32 * (blk / 2), q = q0 + W * (blk % 2) + 8 * (lane % LANES);
-#pragma unroll 1
-    for (int row = lane / LANES; row < 32; row += ROWS) {
-      float v[8];
-      const float* src = out + out_at<W>(row, 8 * (lane % LANES));
+    Chunk<T> now[PASSES];
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) now[k] = next[k];
+    if (blk + 1 < 2 * F) load(blk + 1);
+    const Chunk<T> b = blk % 2 ? bias[1] : bias[0];
+    const int64_t c = q + W * (blk % 2);
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const int64_t p = p0 + 32 * (blk / 2) + row + ROWS * k;
+      const float* src = out + out_at<W>(row + ROWS * k, col);
       const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
       const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-      const int64_t p = pb + row;
-      if (p >= g.P || q >= g.Q) continue;
+      if (p >= g.P || c >= g.Q) continue;
       if (part) {
-        f32x4* dst = reinterpret_cast<f32x4*>(part + p * ldp + q);
+        f32x4* dst = reinterpret_cast<f32x4*>(part + p * ldp + c);
         dst[0] = lo;
         dst[1] = hi;
-      } else {
-        finish_chunk<T>(g, p, q, v);
+        continue;
       }
+      float v[8], f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+      if (c + 8 > g.Q) {
+        finish_chunk<T>(g, p, c, v);
+        continue;
+      }
+      b.widen(f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += f[i];
+      Chunk<T> o;
+      if (g.z) {
+        o.narrow(v);
+        o.store_stream(static_cast<T*>(g.z) + p * g.ldz + c);
+      }
+      if (g.act != kActNone) activate8(g.act, g.beta, v);
+      now[k].widen(f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += f[i];
+      o.narrow(v);
+      o.store_stream(static_cast<T*>(g.out) + p * g.ldo + c);
     }
   }
 }
