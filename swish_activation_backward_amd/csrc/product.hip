@@ -94,39 +94,60 @@ template <int F> struct Side<false, F> {
   __device__ inline int column(int i) const { return col[i & 1]; }
 };
 
-// One operand's part of a stage: window, scalar offset and the columns left in it.
-struct Fetch {
-  __amdgpu_buffer_rsrc_t r;
-  uint32_t soff;
-  int left;
+// Where an operand's next stage is fetched from: a window of rows (deep) or of contraction indices
+// (flat), a scalar offset into it and how far it reaches beyond that.  A stage's fetch only steps
+// it on: anything longer would hold up the matrix cores behind the barrier.
+template <bool DEEP, int P> struct Cursor {
+  uint64_t base;
+  uint32_t bytes, soff, step;   // step: bytes of 32 contraction indices (flat)
+  int left;                     // deep: contraction indices; flat: rows from the tile's first on
+  int end;                      // flat: contraction indices
+
+  template <typename T>
+  __device__ inline void start(const T* p, int64_t ld, int row0, int64_t rows, int k, int last) {
+    const int n = (int)(rows - row0 < P ? rows - row0 : P);
+    const uint32_t row = (uint32_t)ld * 2u;
+    int64_t at;
+    if constexpr (DEEP) {
+      at = (int64_t)row0 * ld;
+      bytes = n > 0 ? (uint32_t)n * row : 0u;
+      soff = (uint32_t)k * 2u;
+      left = last - k;
+    } else {
+      at = (int64_t)k * ld;
+      soff = (uint32_t)row0 * 2u;
+      left = (int)(rows - row0);
+      end = last - k;
+      step = row * kDepth;
+      bytes = flat_bytes(row);
+    }
+    base = (uint64_t)(uintptr_t)uniform_ptr(p + at);
+    bytes = __builtin_amdgcn_readfirstlane(bytes);
+    soff = __builtin_amdgcn_readfirstlane(soff);
+  }
+  __device__ inline uint32_t flat_bytes(uint32_t row) const {
+    const int n = end < kDepth ? end : kDepth;
+    return n > 0 ? (uint32_t)n * row : 0u;
+  }
+  __device__ inline void advance() {
+    if constexpr (DEEP) {
+      soff += kDepth * 2;
+      left -= kDepth;
+    } else {
+      // past the end the window is empty and its base no longer matters
+      base += step;
+      end -= kDepth;
+      bytes = flat_bytes(step / kDepth);
+    }
+  }
+  __device__ inline __amdgpu_buffer_rsrc_t window() const {
+    return make_rsrc((const void*)(uintptr_t)base, bytes);
+  }
 };
 
-// Rows row0 .. row0 + P of an operand of `rows`, contraction k .. k + 32 up to `end`.
-template <bool DEEP, int P, typename T>
-__device__ inline Fetch fetch(const T* base, int64_t ld, int row0, int64_t rows, int k, int end) {
-  Fetch f;
-  int64_t first, n;
-  if (DEEP) {
-    first = row0;
-    n = rows - row0 < P ? rows - row0 : P;
-    f.soff = (uint32_t)k * 2u;
-    f.left = end - k;
-  } else {
-    first = k;
-    n = end - k < kDepth ? end - k : kDepth;
-    f.soff = (uint32_t)row0 * 2u;
-    f.left = (int)(rows - row0);
-  }
-  if (n <= 0) first = 0;
-  f.r = make_rsrc(uniform_ptr(base + first * ld),
-                  __builtin_amdgcn_readfirstlane(clamp_bytes(n, ld * 2)));
-  f.soff = __builtin_amdgcn_readfirstlane(f.soff);
-  return f;
-}
-
-struct Stage {
-  Fetch a, b;
-  const uint16_t* dst;   // the wave's part of the slot
+template <bool AD, bool BD, int P> struct Source {
+  Cursor<AD, P> a;
+  Cursor<BD, P> b;
 };
 
 // A piece of work: a tile and a range of the contraction.
@@ -135,31 +156,29 @@ struct Item {
 };
 
 struct Grid {            // tiles, group of tile rows, ranges of `len`, items
-  int np, nq, group;
-  int64_t tiles, len, items;
+  uint32_t np, nq, group, tiles, items;
+  int64_t len;
 };
 
 // Tiles run down `group` tile rows before they move on a column, so that those that run at once on
 // an XCD (consecutive ones) share rows and columns alike.
-template <int P> __device__ inline Item item(const Grid& g, int64_t L, bool live, int64_t R) {
+template <int P> __device__ inline Item item(const Grid& g, uint32_t L, bool live, int64_t R) {
   Item t;
-  const int64_t l = live ? L : 0;
-  t.split = (int)(l / g.tiles);
-  const int tile = (int)(l % g.tiles);
-  const int band = tile / (g.group * g.nq), in = tile % (g.group * g.nq);
-  const int rows = g.np - band * g.group < g.group ? g.np - band * g.group : g.group;
-  t.p0 = (band * g.group + in % rows) * P;
-  t.q0 = (in / rows) * P;
-  const int64_t b = t.split * g.len, e = b + g.len < R ? b + g.len : R;
-  t.begin = (int)b;
-  t.end = live ? (int)e : (int)b;      // nothing to fetch past the last item
-  t.stages = (int)((e - b + 4 * kDepth - 1) / (4 * kDepth)) * 4;
-  if (t.stages < 4) t.stages = 4;      // one round of the ring
-  t.p0 = __builtin_amdgcn_readfirstlane(t.p0);
-  t.q0 = __builtin_amdgcn_readfirstlane(t.q0);
-  t.begin = __builtin_amdgcn_readfirstlane(t.begin);
-  t.end = __builtin_amdgcn_readfirstlane(t.end);
-  t.stages = __builtin_amdgcn_readfirstlane(t.stages);
+  const uint32_t l = live ? L : 0;
+  const uint32_t split = l / g.tiles, tile = l % g.tiles;
+  const uint32_t full = g.group * g.nq, band = tile / full, in = tile % full;
+  const uint32_t first = band * g.group;
+  const uint32_t rows = g.np - first < g.group ? g.np - first : g.group;
+  const int64_t b = split * g.len, e = b + g.len < R ? b + g.len : R;
+  t.split = __builtin_amdgcn_readfirstlane((int)split);
+  t.p0 = __builtin_amdgcn_readfirstlane((int)(first + in % rows) * P);
+  t.q0 = __builtin_amdgcn_readfirstlane((int)(in / rows) * P);
+  t.begin = __builtin_amdgcn_readfirstlane((int)b);
+  // nothing to fetch past the last item
+  t.end = __builtin_amdgcn_readfirstlane(live ? (int)e : (int)b);
+  int n = (int)((e - b + 4 * kDepth - 1) / (4 * kDepth)) * 4;
+  if (n < 4) n = 4;                    // one round of the ring
+  t.stages = __builtin_amdgcn_readfirstlane(n);
   return t;
 }
 
@@ -167,24 +186,28 @@ template <typename T, int F> struct Frags {
   typename Mfma<T>::frag a[2][F], b[2][F];
 };
 
-// Load E (0 .. 2F - 1) of a stage: the first F of A, the others of B.
+// Load E (0 .. 2F - 1) of a stage to the wave's part of a slot: the first F of A, the others of B.
 template <bool AD, bool BD, int F, int E>
-__device__ inline void load(const Stage& s, const Side<AD, F>& a, const Side<BD, F>& b) {
+__device__ inline void load(const Source<AD, BD, Shape<F>::P>& s, const uint16_t* dst,
+                            const Side<AD, F>& a, const Side<BD, F>& b) {
   constexpr int i = E % F;
   // a wave's loads of an operand fill consecutive KiB of the slot
   if constexpr (E < F) {
     const uint32_t v = a.column(i) < s.a.left ? a.voff[i] : kOOB;
-    dma16s<i * 1024>(s.a.r, v, s.a.soff, s.dst);
+    dma16s<i * 1024>(s.a.window(), v, s.a.soff, dst);
   } else {
     const uint32_t v = b.column(i) < s.b.left ? b.voff[i] : kOOB;
-    dma16s<Shape<F>::SIDE * 2 + i * 1024>(s.b.r, v, s.b.soff, s.dst);
+    dma16s<Shape<F>::SIDE * 2 + i * 1024>(s.b.window(), v, s.b.soff, dst);
   }
 }
 
 template <bool AD, bool BD, int F, int... E>
-__device__ inline void load_all(std::integer_sequence<int, E...>, const Stage& s,
+__device__ inline void load_all(std::integer_sequence<int, E...>,
+                                Source<AD, BD, Shape<F>::P>& s, const uint16_t* dst,
                                 const Side<AD, F>& a, const Side<BD, F>& b) {
-  (load<AD, BD, F, E>(s, a, b), ...);
+  (load<AD, BD, F, E>(s, dst, a, b), ...);
+  s.a.advance();
+  s.b.advance();
 }
 
 // Fragment G (0 .. 4F - 1) of a slot: contraction half G / 2F, then A's blocks, then B's.
@@ -203,26 +226,30 @@ __device__ inline void read_all(std::integer_sequence<int, G...>, const uint16_t
 }
 
 // Group G (0 .. 4F - 1) of a step: F / 2 MFMAs of the stage in f, a fragment of the next stage and,
-// in odd groups, a load, kept in this order by the scheduling fence.
+// in odd groups, a load, kept in this order by the scheduling fence.  An operand's cursor steps on
+// behind its last load.
 template <typename T, bool AD, bool BD, int F, bool NEXT, int G>
 __device__ inline void group(f32x16 (&acc)[F][F], const Frags<T, F>& f, Frags<T, F>& fn,
-                             const uint16_t* next, const Stage& s, const Side<AD, F>& a,
-                             const Side<BD, F>& b) {
+                             const uint16_t* next, Source<AD, BD, Shape<F>::P>& s,
+                             const uint16_t* dst, const Side<AD, F>& a, const Side<BD, F>& b) {
 #pragma unroll
   for (int e = 0; e < F / 2; ++e) {
     const int q = G * (F / 2) + e, kk = q / (F * F), i = (q / F) % F, j = q % F;
     acc[i][j] = Mfma<T>::mma(f.a[kk][i], f.b[kk][j], acc[i][j]);
   }
   if constexpr (NEXT) read_one<T, AD, BD, F, G>(next, a, b, fn);
-  if constexpr ((G & 1) != 0) load<AD, BD, F, (G >> 1)>(s, a, b);
+  if constexpr ((G & 1) != 0) load<AD, BD, F, (G >> 1)>(s, dst, a, b);
+  if constexpr (G == 2 * F - 1) s.a.advance();
+  if constexpr (G == 4 * F - 1) s.b.advance();
   __builtin_amdgcn_sched_barrier(0);
 }
 
 template <typename T, bool AD, bool BD, int F, bool NEXT, int... G>
 __device__ inline void groups(std::integer_sequence<int, G...>, f32x16 (&acc)[F][F],
                               const Frags<T, F>& f, Frags<T, F>& fn, const uint16_t* next,
-                              const Stage& s, const Side<AD, F>& a, const Side<BD, F>& b) {
-  (group<T, AD, BD, F, NEXT, G>(acc, f, fn, next, s, a, b), ...);
+                              Source<AD, BD, Shape<F>::P>& s, const uint16_t* dst,
+                              const Side<AD, F>& a, const Side<BD, F>& b) {
+  (group<T, AD, BD, F, NEXT, G>(acc, f, fn, next, s, dst, a, b), ...);
 }
 
 // ---- epilogue
@@ -349,48 +376,45 @@ void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
   const Side<BD, F> sb(wave, wq, lane, g.b.ld);
   const T* pa = static_cast<const T*>(g.a.p);
   const T* pb = static_cast<const T*>(g.b.p);
-  const int64_t G = gridDim.x, first = xcd_remap(blockIdx.x, G);
-  const int64_t mine = grid.items > first ? (grid.items - first + G - 1) / G : 0;
-  auto stage = [&](const Item& t, int st, int slot) {
-    int k = t.begin + st * kDepth;
-    asm volatile("" : "+s"(k));   // formed here: hoisted they would stay live, and spill
-    Stage s;
-    s.a = fetch<AD, P>(pa, g.a.ld, t.p0, g.P, k, t.end);
-    s.b = fetch<BD, P>(pb, g.b.ld, t.q0, g.Q, k, t.end);
-    s.dst = ring + slot * SLOT + wave * F * 512;
-    return s;
+  const uint32_t G = gridDim.x, first = (uint32_t)xcd_remap(blockIdx.x, G);
+  const uint32_t mine = grid.items > first ? (grid.items - first + G - 1) / G : 0;
+  uint16_t* const dst = ring + wave * F * 512;   // the wave's part of slot 0
+  Source<AD, BD, P> src;                         // of the stages being fetched
+  auto start = [&](const Item& t) {
+    src.a.start(pa, g.a.ld, t.p0, g.P, t.begin, t.end);
+    src.b.start(pb, g.b.ld, t.q0, g.Q, t.begin, t.end);
   };
   // One step u: the fragments of the stage in slot u are in registers and the next three stages in
   // flight.  Once this wave's loads of the next stage have landed and its LDS reads are done, the
   // barrier says so of every wave: slot u may be filled again and slot u + 1 read.  Every step
   // issues the same number of loads, so that "landed" is "at most two stages outstanding".
-#define SWG_STEP(t, st, u, NEXT)                                                            \
+#define SWG_STEP(u, NEXT)                                                                   \
   do {                                                                                      \
     __builtin_amdgcn_s_waitcnt(vmcnt_le(2 * LOADS));                                        \
     __builtin_amdgcn_s_waitcnt(kLgkmcnt0);                                                  \
     SWG_COMPILER_FENCE();                                                                   \
     __builtin_amdgcn_s_barrier();                                                           \
     SWG_COMPILER_FENCE();                                                                   \
-    const Stage s_ = stage((t), (st), (u));                                                 \
     groups<T, AD, BD, F, (NEXT)>(std::make_integer_sequence<int, 4 * F>{}, acc,             \
                                  frags[(u) & 1], frags[((u) + 1) & 1],                      \
-                                 ring + (((u) + 1) & 3) * SLOT, s_, sa, sb);                \
+                                 ring + (((u) + 1) & 3) * SLOT, src, dst + (u) * SLOT, sa,  \
+                                 sb);                                                       \
   } while (0)
 
   f32x16 acc[F][F];
   Frags<T, F> frags[2];
   Item cur = item<P>(grid, first, mine > 0, g.R);
+  start(cur);
   constexpr std::make_integer_sequence<int, LOADS> kLoads{};
-  load_all<AD, BD, F>(kLoads, stage(cur, 0, 0), sa, sb);
-  load_all<AD, BD, F>(kLoads, stage(cur, 1, 1), sa, sb);
-  load_all<AD, BD, F>(kLoads, stage(cur, 2, 2), sa, sb);
-  load_all<AD, BD, F>(kLoads, stage(cur, 3, 3), sa, sb);
+  load_all<AD, BD, F>(kLoads, src, dst, sa, sb);
+  load_all<AD, BD, F>(kLoads, src, dst + SLOT, sa, sb);
+  load_all<AD, BD, F>(kLoads, src, dst + 2 * SLOT, sa, sb);
+  load_all<AD, BD, F>(kLoads, src, dst + 3 * SLOT, sa, sb);
   __builtin_amdgcn_s_waitcnt(vmcnt_le(3 * LOADS));
   SWG_COMPILER_FENCE();
   __builtin_amdgcn_s_barrier();
   SWG_COMPILER_FENCE();
-  for (int64_t j = 0; j < mine; ++j) {
-    const Item nxt = item<P>(grid, first + (j + 1) * G, j + 1 < mine, g.R);
+  for (uint32_t j = 0; j < mine; ++j) {
 #pragma unroll
     for (int a = 0; a < F; ++a)
 #pragma unroll
@@ -401,15 +425,17 @@ void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
       }
     read_all<T, AD, BD, F>(std::make_integer_sequence<int, 4 * F>{}, ring, sa, sb, frags[0]);
     for (int t = 4; t < cur.stages; t += 4) {
-      SWG_STEP(cur, t, 0, true);
-      SWG_STEP(cur, t + 1, 1, true);
-      SWG_STEP(cur, t + 2, 2, true);
-      SWG_STEP(cur, t + 3, 3, true);
+      SWG_STEP(0, true);
+      SWG_STEP(1, true);
+      SWG_STEP(2, true);
+      SWG_STEP(3, true);
     }
-    SWG_STEP(nxt, 0, 0, true);
-    SWG_STEP(nxt, 1, 1, true);
-    SWG_STEP(nxt, 2, 2, true);
-    SWG_STEP(nxt, 3, 3, false);   // the next item's first stage is read after the epilogue
+    const Item nxt = item<P>(grid, first + (j + 1) * G, j + 1 < mine, g.R);
+    start(nxt);
+    SWG_STEP(0, true);
+    SWG_STEP(1, true);
+    SWG_STEP(2, true);
+    SWG_STEP(3, false);   // the next item's first stage is read after the epilogue
     float* to = part ? part + (int64_t)cur.split * g.P * ldp : nullptr;
     epilogue<T, F>(acc, g, to, ldp, outs + wave * Shape<F>::OUT, lane,
                    (int64_t)cur.p0 + wp * Shape<F>::WR, (int64_t)cur.q0 + wq * Shape<F>::WR);
@@ -512,12 +538,12 @@ hipError_t product16_t(Product g, const ProductPlan& p, void* ws, int cus, hipSt
     if (e != hipSuccess) return e;
   }
   Grid grid;
-  grid.np = (int)p.np;
-  grid.nq = (int)p.nq;
+  grid.np = (uint32_t)p.np;
+  grid.nq = (uint32_t)p.nq;
   grid.group = 4;
-  grid.tiles = p.np * p.nq;
+  grid.tiles = (uint32_t)(p.np * p.nq);
+  grid.items = (uint32_t)(p.np * p.nq * p.splits);
   grid.len = p.len;
-  grid.items = grid.tiles * p.splits;
   float* part = p.splits > 1 ? reinterpret_cast<float*>(w + p.part_at) : nullptr;
   hipError_t e = p.f == 4 ? layouts<T, 4>(g, grid, part, p.ldp, cus, stream)
                           : layouts<T, 2>(g, grid, part, p.ldp, cus, stream);
