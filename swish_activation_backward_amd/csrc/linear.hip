@@ -14,52 +14,10 @@ namespace swg {
     if (e_ != hipSuccess) return e_;           \
   } while (0)
 
-// ------------------------------------------------------------------ products
-template <typename T>
-__global__ __launch_bounds__(256) void product_kernel(Product a, int64_t nq) {
-  __shared__ float la[16][65], lb[16][65];
-  const int64_t p0 = (int64_t)(blockIdx.x / nq) * 64, q0 = (int64_t)(blockIdx.x % nq) * 64;
-  const int tp = threadIdx.x / 16, tq = threadIdx.x % 16;
-  float acc[4][4] = {};
-  auto at = [](const Operand& o, int64_t row, int64_t r) {
-    return to_f32(static_cast<const T*>(o.p)[o.deep ? row * o.ld + r : r * o.ld + row]);
-  };
-  for (int64_t r0 = 0; r0 < a.R; r0 += 16) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < 16 * 64; e += 256) {
-      const int ra = a.a.deep ? e % 16 : e / 64, pa = a.a.deep ? e / 16 : e % 64;
-      const int rb = a.b.deep ? e % 16 : e / 64, qb = a.b.deep ? e / 16 : e % 64;
-      la[ra][pa] = r0 + ra < a.R && p0 + pa < a.P ? at(a.a, p0 + pa, r0 + ra) : 0.0f;
-      lb[rb][qb] = r0 + rb < a.R && q0 + qb < a.Q ? at(a.b, q0 + qb, r0 + rb) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_fmaf(la[r][tp + 16 * i], lb[r][tq + 16 * j], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t p = p0 + tp + 16 * i, q = q0 + tq + 16 * j;
-      if (p < a.P && q < a.Q) finish<1, T>(a, p, q, &acc[i][j]);
-    }
-}
-
-template <typename T> static hipError_t product_t(const Product& a, hipStream_t stream) {
-  const int64_t nq = ceil_div(a.Q, 64), tiles = ceil_div(a.P, 64) * nq;
-  SWG_TRY(SWG_LAUNCH((product_kernel<T>), dim3((unsigned)tiles), dim3(256), 0, stream, a, nq));
-  return hipSuccess;
-}
-
 hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
                           hipStream_t stream) {
   if (dtype != 2) return launch_product16(dtype, a, p, ws, cus, stream);
-  return product_t<float>(a, stream);
+  return launch_product32(a, p, ws, stream);
 }
 
 // ------------------------------------------------------------------ dz and db

@@ -375,14 +375,14 @@ inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
   return p;
 }
 
-// One product of the linear layer: output [P, Q], contraction R.  16-bit tensors: tiles of edge
-// 64 f, the contraction cut into `splits` ranges of `len` whose fp32 sums [P, ldp] are joined in
-// order; operands that do not lie in rows of 16-byte multiples are laid out again (pack_a, pack_b)
-// in the workspace before.
+// One product of the linear layer: output [P, Q], contraction R, in tiles of edge 64 f (f = 4 or 2
+// for 16-bit tensors, 2 or 1 for fp32), the contraction cut into `splits` ranges of `len` whose fp32
+// sums [P, ldp] are joined in order.  16-bit operands that do not lie in rows of 16-byte multiples
+// are laid out again (pack_a, pack_b) in the workspace before.
 //
 // The tile and the split are those of the smallest estimate: rounds of items over the CUs, times an
 // item's stages (32 deep) and what it spends before and after them, plus the partial sums' trip
-// through memory and the launch that joins them.  force_f: 4 or 2 overrides the tile.
+// through memory and the launch that joins them.  force_f: 4 or 2 overrides the tile (16-bit).
 struct ProductPlan {
   int f;
   int64_t np, nq;
@@ -392,18 +392,22 @@ struct ProductPlan {
   size_t ws_bytes;
 };
 
-constexpr int64_t kProductStageNs[2] = {850, 400};    // one 32-deep stage, f = 4 / f = 2
-constexpr int64_t kProductItemNs[2] = {6000, 3000};   // first loads and epilogue
+// Time of a stage and of an item's ends, in ns, by f, and the items that share a CU.
+struct ProductCost {
+  int f;
+  int64_t stage, item, share;
+};
+constexpr ProductCost kProduct16[2] = {{4, 800, 12000, 1}, {2, 290, 3000, 2}};
+constexpr ProductCost kProduct32[2] = {{2, 1900, 4000, 1}, {1, 600, 2000, 1}};
 constexpr int64_t kJoinNs = 3000;
 
-inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, int f, int64_t splits) {
-  const int64_t tiles = ceil_div(P, tile_edge(f)) * ceil_div(Q, tile_edge(f));
-  const int64_t len = ceil_div(R, splits);
-  const int64_t slots = f == 4 ? kGemmSlots : 2 * kGemmSlots;
-  int64_t stage = stage_ns(kProductStageNs, f);
-  if (f == 2 && tiles * splits > kGemmSlots) stage = stage * 3 / 2;   // two share a CU
-  const int64_t item = 4 * ceil_div(len, 4 * kTileR) * stage + stage_ns(kProductItemNs, f);
-  int64_t t = ceil_div(tiles * splits, slots) * item;
+inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, const ProductCost& c, int64_t splits) {
+  const int64_t items = ceil_div(P, tile_edge(c.f)) * ceil_div(Q, tile_edge(c.f)) * splits;
+  const int64_t share = items > kGemmSlots ? c.share : 1;
+  const int64_t stages = ceil_div(ceil_div(R, splits), 4 * kTileR) * 4;
+  // items that share a CU take turns; one alone waits for its loads
+  const int64_t stage = c.share > share ? c.stage * 5 / 4 : c.stage;
+  int64_t t = ceil_div(items, kGemmSlots * share) * (stages * stage * share + c.item);
   if (splits > 1) t += kJoinNs + splits * P * Q * 8 / kStreamBytesPerNs;
   return t;
 }
@@ -411,22 +415,19 @@ inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, int f, int64_t splits
 inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool pack_a,
                                 bool a_deep, bool pack_b, bool b_deep, int force_f) {
   ProductPlan p{};
-  p.f = 4;
   p.splits = 1;
-  if (dtype != 2) {
-    int64_t best = -1;
-    for (int f = 4; f >= 2; f -= 2) {
-      if (force_f != 0 && f != force_f) continue;
-      const int64_t tiles = ceil_div(P, tile_edge(f)) * ceil_div(Q, tile_edge(f));
-      int64_t most = ceil_div(2 * kGemmSlots, tiles < 1 ? 1 : tiles);
-      if (most > R / 256) most = R / 256;
-      for (int64_t s = 1; s == 1 || s <= most; ++s) {
-        const int64_t t = product_ns(P, Q, R, f, s);
-        if (best < 0 || t < best) {
-          best = t;
-          p.f = f;
-          p.splits = s;
-        }
+  int64_t best = -1;
+  for (const ProductCost& c : dtype == 2 ? kProduct32 : kProduct16) {
+    if (dtype != 2 && force_f != 0 && c.f != force_f) continue;
+    const int64_t tiles = ceil_div(P, tile_edge(c.f)) * ceil_div(Q, tile_edge(c.f));
+    int64_t most = ceil_div(2 * kGemmSlots, tiles < 1 ? 1 : tiles);
+    if (most > R / 256) most = R / 256;
+    for (int64_t s = 1; s == 1 || s <= most; ++s) {
+      const int64_t t = product_ns(P, Q, R, c, s);
+      if (best < 0 || t < best) {
+        best = t;
+        p.f = c.f;
+        p.splits = s;
       }
     }
   }

@@ -30,7 +30,6 @@ namespace swg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDepth = 32;
 
 template <int F> struct Shape {
   static constexpr int P = 64 * F;                 // tile edge
@@ -150,38 +149,6 @@ template <bool AD, bool BD, int P> struct Source {
   Cursor<BD, P> b;
 };
 
-// A piece of work: a tile and a range of the contraction.
-struct Item {
-  int split, p0, q0, begin, end, stages;
-};
-
-struct Grid {            // tiles, group of tile rows, ranges of `len`, items
-  uint32_t np, nq, group, tiles, items;
-  int64_t len;
-};
-
-// Tiles run down `group` tile rows before they move on a column, so that those that run at once on
-// an XCD (consecutive ones) share rows and columns alike.
-template <int P> __device__ inline Item item(const Grid& g, uint32_t L, bool live, int64_t R) {
-  Item t;
-  const uint32_t l = live ? L : 0;
-  const uint32_t split = l / g.tiles, tile = l % g.tiles;
-  const uint32_t full = g.group * g.nq, band = tile / full, in = tile % full;
-  const uint32_t first = band * g.group;
-  const uint32_t rows = g.np - first < g.group ? g.np - first : g.group;
-  const int64_t b = split * g.len, e = b + g.len < R ? b + g.len : R;
-  t.split = __builtin_amdgcn_readfirstlane((int)split);
-  t.p0 = __builtin_amdgcn_readfirstlane((int)(first + in % rows) * P);
-  t.q0 = __builtin_amdgcn_readfirstlane((int)(in / rows) * P);
-  t.begin = __builtin_amdgcn_readfirstlane((int)b);
-  // nothing to fetch past the last item
-  t.end = __builtin_amdgcn_readfirstlane(live ? (int)e : (int)b);
-  int n = (int)((e - b + 4 * kDepth - 1) / (4 * kDepth)) * 4;
-  if (n < 4) n = 4;                    // one round of the ring
-  t.stages = __builtin_amdgcn_readfirstlane(n);
-  return t;
-}
-
 template <typename T, int F> struct Frags {
   typename Mfma<T>::frag a[2][F], b[2][F];
 };
@@ -253,20 +220,6 @@ __device__ inline void groups(std::integer_sequence<int, G...>, f32x16 (&acc)[F]
 }
 
 // ---- epilogue
-// Float (row, column) of a block in the wave's part of LDS.  Rows 4 apart, which the two halves of
-// a wave write at once, use different banks.
-template <int W> __device__ inline int out_at(int row, int col) {
-  return (row * W + col) ^ (((row >> 2) & 1) << 5);
-}
-
-// 32 x 32 sums of one MFMA tile into columns c0 .. of the block
-template <int W>
-__device__ inline void put_tile(const f32x16& v, float* out, int lane, int c0) {
-#pragma unroll
-  for (int r = 0; r < 16; ++r)
-    out[out_at<W>(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), c0 + (lane & 31))] = v[r];
-}
-
 // Block B: MFMA tiles (B / 2, 2 (B % 2)) and the one to its right (F = 4), tile (B / 2, B % 2) (F = 2)
 template <int F, int B>
 __device__ inline void put_block(const f32x16 (&acc)[F][F], float* out, int lane) {
@@ -365,7 +318,7 @@ __device__ inline void epilogue(const f32x16 (&acc)[F][F], const Product& g, flo
 
 template <typename T, bool AD, bool BD, int F>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<F>::WAVES, Shape<F>::WAVES)))
-void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
+void product16_kernel(Product g, ProductGrid grid, float* part, int64_t ldp) {
   constexpr int P = Shape<F>::P, SLOT = Shape<F>::SLOT, LOADS = Shape<F>::LOADS;
   __shared__ __attribute__((aligned(1024))) uint16_t ring[4 * SLOT];
   __shared__ __attribute__((aligned(16))) float outs[4 * Shape<F>::OUT];
@@ -380,7 +333,7 @@ void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
   const uint32_t mine = grid.items > first ? (grid.items - first + G - 1) / G : 0;
   uint16_t* const dst = ring + wave * F * 512;   // the wave's part of slot 0
   Source<AD, BD, P> src;                         // of the stages being fetched
-  auto start = [&](const Item& t) {
+  auto start = [&](const ProductItem& t) {
     src.a.start(pa, g.a.ld, t.p0, g.P, t.begin, t.end);
     src.b.start(pb, g.b.ld, t.q0, g.Q, t.begin, t.end);
   };
@@ -403,7 +356,7 @@ void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
 
   f32x16 acc[F][F];
   Frags<T, F> frags[2];
-  Item cur = item<P>(grid, first, mine > 0, g.R);
+  ProductItem cur = product_item<P, 4 * kDepth>(grid, first, mine > 0, g.R);
   start(cur);
   constexpr std::make_integer_sequence<int, LOADS> kLoads{};
   load_all<AD, BD, F>(kLoads, src, dst, sa, sb);
@@ -430,7 +383,7 @@ void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
       SWG_STEP(2, true);
       SWG_STEP(3, true);
     }
-    const Item nxt = item<P>(grid, first + (j + 1) * G, j + 1 < mine, g.R);
+    const ProductItem nxt = product_item<P, 4 * kDepth>(grid, first + (j + 1) * G, j + 1 < mine, g.R);
     start(nxt);
     SWG_STEP(0, true);
     SWG_STEP(1, true);
@@ -443,28 +396,6 @@ void product16_kernel(Product g, Grid grid, float* part, int64_t ldp) {
   }
 #undef SWG_STEP
   __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
-}
-
-// out from the `splits` partial sums, in order; a thread takes 8 columns of a row.
-template <typename T>
-__global__ __launch_bounds__(256) void product_join_kernel(Product g, const float* part,
-                                                           int64_t splits, int64_t ldp,
-                                                           int64_t chunks) {
-  const int64_t total = g.P * chunks, plane = g.P * ldp;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
-       e += (int64_t)gridDim.x * 256) {
-    const int64_t p = e / chunks, q = (e % chunks) * 8;
-    const float* src = part + p * ldp + q;
-    f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
-    for (int64_t s = 1; s < splits; ++s) {
-      lo += *reinterpret_cast<const f32x4*>(src + s * plane);
-      hi += *reinterpret_cast<const f32x4*>(src + s * plane + 4);
-    }
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-    finish_chunk<T>(g, p, q, v);
-  }
 }
 
 // rows [n][cols] again with rows of ld elements, zeros past their end; a thread takes 8 columns
@@ -488,13 +419,8 @@ __global__ __launch_bounds__(256) void pack_kernel(const T* src, int64_t lds, T*
   }
 }
 
-unsigned stream_grid(int64_t items) {
-  const int64_t n = ceil_div(items, 256);
-  return (unsigned)(n < kMaxStreamBlocks ? n : kMaxStreamBlocks);
-}
-
 template <typename T, bool AD, bool BD, int F>
-hipError_t tiles(const Product& g, const Grid& grid, float* part, int64_t ldp, int cus,
+hipError_t tiles(const Product& g, const ProductGrid& grid, float* part, int64_t ldp, int cus,
                  hipStream_t stream) {
   const int64_t slots = (int64_t)cus * Shape<F>::WAVES;
   const int64_t n = grid.items < slots ? grid.items : slots;
@@ -504,7 +430,7 @@ hipError_t tiles(const Product& g, const Grid& grid, float* part, int64_t ldp, i
 }
 
 template <typename T, int F>
-hipError_t layouts(const Product& g, const Grid& grid, float* part, int64_t ldp, int cus,
+hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, int64_t ldp, int cus,
                    hipStream_t stream) {
   if (g.a.deep && !g.b.deep) return tiles<T, true, false, F>(g, grid, part, ldp, cus, stream);
   if (g.a.deep) return tiles<T, true, true, F>(g, grid, part, ldp, cus, stream);
@@ -537,21 +463,12 @@ hipError_t product16_t(Product g, const ProductPlan& p, void* ws, int cus, hipSt
     const hipError_t e = pack<T>(g.b, g.Q, g.R, w + p.pack_b_at, stream);
     if (e != hipSuccess) return e;
   }
-  Grid grid;
-  grid.np = (uint32_t)p.np;
-  grid.nq = (uint32_t)p.nq;
-  grid.group = 4;
-  grid.tiles = (uint32_t)(p.np * p.nq);
-  grid.items = (uint32_t)(p.np * p.nq * p.splits);
-  grid.len = p.len;
+  const ProductGrid grid = product_grid(p);
   float* part = p.splits > 1 ? reinterpret_cast<float*>(w + p.part_at) : nullptr;
   hipError_t e = p.f == 4 ? layouts<T, 4>(g, grid, part, p.ldp, cus, stream)
                           : layouts<T, 2>(g, grid, part, p.ldp, cus, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t chunks = ceil_div(g.Q, 8);
-  SWG_LAUNCH((product_join_kernel<T>), dim3(stream_grid(g.P * chunks)), dim3(256), 0, stream, g,
-             part, p.splits, p.ldp, chunks);
-  return hipGetLastError();
+  return product_join<T>(g, p, part, stream);
 }
 
 }  // namespace

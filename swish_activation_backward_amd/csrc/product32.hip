@@ -1,0 +1,185 @@
+// The linear layer's products for fp32 tensors, on the fp32 matrix instructions
+// (v_mfma_f32_32x32x2_f32: a lane supplies row l % 32 and contraction index l / 32):
+//   C[p, q] = sum over r of A(p, r) B(q, r)
+// with operands of any alignment, deep or flat (see product.hip).
+//
+// A workgroup of four waves (2 x 2) owns a tile of edge 64 F, each wave 32 F x 32 F outputs.  A
+// stage of 32 contraction indices is loaded into registers while the one before it is multiplied,
+// and written to the other of two LDS buffers: a deep operand as [row][32], of which a lane reads
+// four consecutive indices at once, a flat one as [32][row].  Lane half h takes index 8 j + 4 h + s
+// in step s of a group j, of both operands alike.
+#include "mma.hpp"
+#include "product.hpp"
+
+namespace swg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// One operand's part of a stage: V 16-byte vectors a thread.
+template <bool DEEP, int F> struct Part {
+  static constexpr int P = 64 * F, V = P * kDepth / 4 / kThreads;
+  static constexpr int PITCH = DEEP ? kDepth + 4 : P + 4;
+  static constexpr int FLOATS = DEEP ? P * PITCH : kDepth * PITCH;
+  f32x4 v[V];
+
+  // row and contraction index of vector h
+  static __device__ inline int row(int h) {
+    return DEEP ? threadIdx.x / 8 + 32 * h : (threadIdx.x % (P / 4)) * 4;
+  }
+  static __device__ inline int deep(int h) {
+    return DEEP ? (threadIdx.x % 8) * 4 : threadIdx.x / (P / 4) + kThreads / (P / 4) * h;
+  }
+
+  // rows row0 .. of `rows`, contraction r0 .. up to `end`; 0 past them
+  __device__ inline void load(const float* src, int64_t ld, int64_t row0, int64_t rows, int64_t r0,
+                              int64_t end) {
+#pragma unroll
+    for (int h = 0; h < V; ++h) {
+      const int64_t p = row0 + row(h), r = r0 + deep(h);
+      const int64_t left = DEEP ? end - r : rows - p;   // along the vector
+      v[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (DEEP ? p >= rows : r >= end) continue;
+      const float* q = src + (DEEP ? p * ld + r : r * ld + p);
+      if (left >= 4) {
+        const u32x4_el4 u = *reinterpret_cast<const u32x4_el4*>(q);
+        v[h] = __builtin_bit_cast(f32x4, u);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e < left) v[h][e] = q[e];
+      }
+    }
+  }
+  __device__ inline void store(float* lds) const {
+#pragma unroll
+    for (int h = 0; h < V; ++h)
+      *reinterpret_cast<f32x4*>(lds + (DEEP ? row(h) * PITCH + deep(h)
+                                            : deep(h) * PITCH + row(h))) = v[h];
+  }
+  // the four steps' values of group j, of the row `at`
+  static __device__ inline f32x4 read(const float* lds, int at, int j, int half) {
+    const int r = 8 * j + 4 * half;
+    if constexpr (DEEP) return *reinterpret_cast<const f32x4*>(lds + at * PITCH + r);
+    f32x4 f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) f[s] = lds[(r + s) * PITCH + at];
+    return f;
+  }
+};
+
+template <bool AD, bool BD, int F>
+__global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductGrid grid,
+                                                             float* part, int64_t ldp) {
+  typedef Part<AD, F> A;
+  typedef Part<BD, F> B;
+  constexpr int P = 64 * F, WR = 32 * F, BUF = A::FLOATS + B::FLOATS;
+  static_assert(BUF >= 2 * 1024, "the way out takes a block of 1024 floats a wave");
+  __shared__ __attribute__((aligned(16))) float lds[2 * BUF];
+  const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wp = wave / 2, wq = wave % 2;
+  const ProductItem t = product_item<P, kDepth>(grid, (uint32_t)xcd_remap(blockIdx.x, gridDim.x),
+                                                true, g.R);
+  const float* pa = static_cast<const float*>(g.a.p);
+  const float* pb = static_cast<const float*>(g.b.p);
+  f32x16 acc[F][F];
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  A a;
+  B b;
+  a.load(pa, g.a.ld, t.p0, g.P, t.begin, t.end);
+  b.load(pb, g.b.ld, t.q0, g.Q, t.begin, t.end);
+  a.store(lds);
+  b.store(lds + A::FLOATS);
+  __syncthreads();
+  for (int st = 0; st < t.stages; ++st) {
+    const float* cur = lds + (st & 1) * BUF;
+    float* other = lds + ((st & 1) ^ 1) * BUF;
+    const bool more = st + 1 < t.stages;
+    if (more) {
+      const int64_t r = t.begin + (int64_t)(st + 1) * kDepth;
+      a.load(pa, g.a.ld, t.p0, g.P, r, t.end);
+      b.load(pb, g.b.ld, t.q0, g.Q, r, t.end);
+    }
+#pragma unroll
+    for (int j = 0; j < kDepth / 8; ++j) {
+      f32x4 fa[F], fb[F];
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        fa[i] = A::read(cur, wp * WR + 32 * i + col, j, half);
+        fb[i] = B::read(cur + A::FLOATS, wq * WR + 32 * i + col, j, half);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int k = 0; k < F; ++k)
+            acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i][s], fb[k][s], acc[i][k], 0, 0, 0);
+    }
+    if (more) {
+      a.store(other);
+      b.store(other + A::FLOATS);
+    }
+    __syncthreads();
+  }
+  // out, 32 x 32 sums of a wave at a time
+  float* out = lds + wave * 1024;
+  if (part) part += (int64_t)t.split * g.P * ldp;
+#pragma unroll
+  for (int i = 0; i < F; ++i)
+#pragma unroll
+    for (int k = 0; k < F; ++k) {
+      put_tile<32>(acc[i][k], out, lane, 0);
+      const int64_t p0 = (int64_t)t.p0 + wp * WR + 32 * i;
+      const int64_t q = (int64_t)t.q0 + wq * WR + 32 * k + 8 * (lane % 4);
+#pragma unroll 1
+      for (int row = lane / 4; row < 32; row += 16) {
+        const float* src = out + out_at<32>(row, 8 * (lane % 4));
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = src[e];
+        const int64_t p = p0 + row;
+        if (p >= g.P || q >= g.Q) continue;
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) part[p * ldp + q + e] = v[e];
+        } else {
+          finish_chunk<float>(g, p, q, v);
+        }
+      }
+    }
+}
+
+template <int F>
+hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, int64_t ldp,
+                   hipStream_t stream) {
+  const dim3 blocks(grid.items), block(kThreads);
+  if (g.a.deep && !g.b.deep)
+    SWG_LAUNCH((product32_kernel<true, false, F>), blocks, block, 0, stream, g, grid, part, ldp);
+  else if (g.a.deep)
+    SWG_LAUNCH((product32_kernel<true, true, F>), blocks, block, 0, stream, g, grid, part, ldp);
+  else
+    SWG_LAUNCH((product32_kernel<false, false, F>), blocks, block, 0, stream, g, grid, part, ldp);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_product32(const Product& g, const ProductPlan& p, void* ws, hipStream_t stream) {
+  const ProductGrid grid = product_grid(p);
+  float* part = nullptr;
+  if (p.splits > 1) part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_at);
+  const hipError_t e = p.f == 2 ? layouts<2>(g, grid, part, p.ldp, stream)
+                                : layouts<1>(g, grid, part, p.ldp, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return product_join<float>(g, p, part, stream);
+}
+
+}  // namespace swg
