@@ -39,7 +39,12 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, float* part,
   float s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-  if (c + 8 <= a.N) {
+  if (c < a.N && a.N >= 8) {
+    // columns that are no multiple of 8 end with a chunk moved back to the row's end: its first
+    // `skip` elements count in the chunk before
+    const int64_t at = c + 8 <= a.N ? c : a.N - 8;
+    const int skip = (int)(c - at);
+    const int64_t pad = skip > 0 && dz ? (a.N + 7) / 8 * 8 : 0;
     for (int64_t r = r0 + ty; r < r1; r += kActTy * kActFlight) {
       Chunk<T> d[kActFlight], f[kActFlight];
 #pragma unroll
@@ -48,8 +53,8 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, float* part,
         d[k].zero();
         f[k].zero();
         if (row < r1) {
-          d[k].load_stream(dy + row * a.lddy + c);
-          if (a.act != kActNone) f[k].load_stream(z + row * a.ldz + c);
+          d[k].load_stream(dy + row * a.lddy + at);
+          if (a.act != kActNone) f[k].load_stream(z + row * a.ldz + at);
         }
       }
 #pragma unroll
@@ -67,23 +72,35 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, float* part,
         if (dz && row < r1) {
           Chunk<T> o;
           o.narrow(g);
-          o.store_stream(dz + row * a.lddz + c);
+          o.store_stream(dz + row * a.lddz + at);
+          // 0 up to a multiple of 8, which takes part in dx's sums
+          for (int64_t e = a.N; e < pad; ++e) dz[row * a.lddz + e] = from_f32<T>(0.0f);
         }
       }
     }
-  } else if (c < a.N) {
-    const int n = (int)(a.N - c);
+    // to the places of columns c ..
+    if (skip > 0) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = s[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[i] = k == i + skip ? v[k] : s[i];
+      }
+    }
+  } else if (c < a.N) {   // fewer than 8 columns
     for (int64_t r = r0 + ty; r < r1; r += kActTy) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float g = 0.0f;
-        if (i < n) {
-          g = to_f32(dy[r * a.lddy + c + i]);
-          if (a.act != kActNone) g *= activation_slope(a.act, a.beta, to_f32(z[r * a.ldz + c + i]));
+        if (i < a.N) {
+          g = to_f32(dy[r * a.lddy + i]);
+          if (a.act != kActNone) g *= activation_slope(a.act, a.beta, to_f32(z[r * a.ldz + i]));
         }
         s[i] += g;
-        // 0 past the row's end, which takes part in dx's sums
-        if (dz && c + i < a.lddz) dz[r * a.lddz + c + i] = from_f32<T>(g);
+        if (dz) dz[r * a.lddz + i] = from_f32<T>(g);
       }
     }
   }

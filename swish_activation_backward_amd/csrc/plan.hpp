@@ -392,22 +392,27 @@ struct ProductPlan {
   size_t ws_bytes;
 };
 
-// Time of a stage and of an item's ends, in ns, by f, and the items that share a CU.
+// Row stride of a 16-bit operand that is laid out again: whole 128-byte lines, so that the 64-byte
+// pieces of its rows that a stage fetches lie in one line each.
+inline int64_t packed_ld(int64_t cols) { return ceil_div(cols, 64) * 64; }
+
+// In ns, by f: a stage's time on a CU that is busy, the least time from one stage of an item to the
+// next (its loads' latency), an item's ends, and the items that can share a CU.
 struct ProductCost {
   int f;
-  int64_t stage, item, share;
+  int64_t busy, least, ends, share;
 };
-constexpr ProductCost kProduct16[2] = {{4, 800, 12000, 1}, {2, 290, 3000, 2}};
-constexpr ProductCost kProduct32[2] = {{2, 1900, 4000, 1}, {1, 600, 2000, 1}};
-constexpr int64_t kJoinNs = 3000;
+constexpr ProductCost kProduct16[2] = {{4, 800, 800, 12000, 1}, {2, 280, 450, 3000, 2}};
+constexpr ProductCost kProduct32[2] = {{2, 1900, 1900, 4000, 2}, {1, 480, 1000, 2000, 4}};
+constexpr int64_t kJoinNs = 5000;
 
 inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, const ProductCost& c, int64_t splits) {
   const int64_t items = ceil_div(P, tile_edge(c.f)) * ceil_div(Q, tile_edge(c.f)) * splits;
-  const int64_t share = items > kGemmSlots ? c.share : 1;
   const int64_t stages = ceil_div(ceil_div(R, splits), 4 * kTileR) * 4;
-  // items that share a CU take turns; one alone waits for its loads
-  const int64_t stage = c.share > share ? c.stage * 5 / 4 : c.stage;
-  int64_t t = ceil_div(items, kGemmSlots * share) * (stages * stage * share + c.item);
+  int64_t share = ceil_div(items, kGemmSlots);
+  if (share > c.share) share = c.share;
+  const int64_t stage = c.busy * share > c.least ? c.busy * share : c.least;
+  int64_t t = ceil_div(items, kGemmSlots * share) * (stages * stage + c.ends);
   if (splits > 1) t += kJoinNs + splits * P * Q * 8 / kStreamBytesPerNs;
   return t;
 }
@@ -420,7 +425,7 @@ inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool
   for (const ProductCost& c : dtype == 2 ? kProduct32 : kProduct16) {
     if (dtype != 2 && force_f != 0 && c.f != force_f) continue;
     const int64_t tiles = ceil_div(P, tile_edge(c.f)) * ceil_div(Q, tile_edge(c.f));
-    int64_t most = ceil_div(2 * kGemmSlots, tiles < 1 ? 1 : tiles);
+    int64_t most = ceil_div(c.share * kGemmSlots, tiles < 1 ? 1 : tiles);
     if (most > R / 256) most = R / 256;
     for (int64_t s = 1; s == 1 || s <= most; ++s) {
       const int64_t t = product_ns(P, Q, R, c, s);
@@ -439,7 +444,7 @@ inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool
   p.ldp = ceil_div(Q, 8) * 8;
   auto packed = [](int64_t rows, int64_t deep_len, bool deep) {
     const int64_t n = deep ? rows : deep_len, c = deep ? deep_len : rows;
-    return (size_t)(n * (ceil_div(c, 8) * 8)) * 2;
+    return (size_t)(n * packed_ld(c)) * 2;
   };
   if (dtype != 2 && R > 0 && pack_a) {
     p.pack_a = true;
@@ -470,7 +475,7 @@ struct LinearBwdPlan {
 inline LinearBwdPlan plan_linear_bwd(int64_t M, int64_t N, int act, int dtype) {
   LinearBwdPlan p{};
   p.act = plan_act_bwd(M, N);
-  p.lddz = ceil_div(N, 8) * 8;
+  p.lddz = packed_ld(N);
   p.part_at = act != 0 ? (size_t)(ceil_div(M * p.lddz * elem_size(dtype), 16) * 16) : 0;
   p.product_at = p.part_at + (size_t)(p.act.parts * p.act.np) * sizeof(float);
   return p;

@@ -20,6 +20,7 @@
 //
 // Operands have rows of 16-byte multiples at 16-byte boundaries (others are laid out again first);
 // what lies past their edges is fetched at offsets beyond the buffer window and arrives as zeros.
+#include <type_traits>
 #include <utility>
 
 #include "mma.hpp"
@@ -30,6 +31,10 @@ namespace swg {
 namespace {
 
 constexpr int kThreads = 256;
+
+// Functions that take the accumulators are inlined before anything else happens to them, and index
+// them by constants.
+#define SWG_INLINE __device__ __attribute__((always_inline)) inline
 
 template <int F> struct Shape {
   static constexpr int P = 64 * F;                 // tile edge
@@ -192,18 +197,32 @@ __device__ inline void read_all(std::integer_sequence<int, G...>, const uint16_t
   (read_one<T, AD, BD, F, G>(slot, a, b, f), ...);
 }
 
+// MFMA Q of a stage: contraction half, row block, column block
+template <typename T, int F, int Q>
+SWG_INLINE void mma(f32x16 (&acc)[F][F], const Frags<T, F>& f) {
+  constexpr int kk = Q / (F * F), i = (Q / F) % F, j = Q % F;
+  acc[i][j] = Mfma<T>::mma(f.a[kk][i], f.b[kk][j], acc[i][j]);
+}
+
+// Clears an accumulator, in AGPRs from there on: no copies at the loop.
+SWG_INLINE void clear_one(f32x16& v) {
+  v = (f32x16)(0.0f);
+  asm volatile("" : "+a"(v));
+}
+template <int F, int... I>
+SWG_INLINE void clear(std::integer_sequence<int, I...>, f32x16 (&acc)[F][F]) {
+  (clear_one(acc[I / F][I % F]), ...);
+}
+
 // Group G (0 .. 4F - 1) of a step: F / 2 MFMAs of the stage in f, a fragment of the next stage and,
 // in odd groups, a load, kept in this order by the scheduling fence.  An operand's cursor steps on
 // behind its last load.
 template <typename T, bool AD, bool BD, int F, bool NEXT, int G>
-__device__ inline void group(f32x16 (&acc)[F][F], const Frags<T, F>& f, Frags<T, F>& fn,
+SWG_INLINE void group(f32x16 (&acc)[F][F], const Frags<T, F>& f, Frags<T, F>& fn,
                              const uint16_t* next, Source<AD, BD, Shape<F>::P>& s,
                              const uint16_t* dst, const Side<AD, F>& a, const Side<BD, F>& b) {
-#pragma unroll
-  for (int e = 0; e < F / 2; ++e) {
-    const int q = G * (F / 2) + e, kk = q / (F * F), i = (q / F) % F, j = q % F;
-    acc[i][j] = Mfma<T>::mma(f.a[kk][i], f.b[kk][j], acc[i][j]);
-  }
+  mma<T, F, G * (F / 2)>(acc, f);
+  if constexpr (F == 4) mma<T, F, G * (F / 2) + 1>(acc, f);
   if constexpr (NEXT) read_one<T, AD, BD, F, G>(next, a, b, fn);
   if constexpr ((G & 1) != 0) load<AD, BD, F, (G >> 1)>(s, dst, a, b);
   if constexpr (G == 2 * F - 1) s.a.advance();
@@ -212,7 +231,7 @@ __device__ inline void group(f32x16 (&acc)[F][F], const Frags<T, F>& f, Frags<T,
 }
 
 template <typename T, bool AD, bool BD, int F, bool NEXT, int... G>
-__device__ inline void groups(std::integer_sequence<int, G...>, f32x16 (&acc)[F][F],
+SWG_INLINE void groups(std::integer_sequence<int, G...>, f32x16 (&acc)[F][F],
                               const Frags<T, F>& f, Frags<T, F>& fn, const uint16_t* next,
                               Source<AD, BD, Shape<F>::P>& s, const uint16_t* dst,
                               const Side<AD, F>& a, const Side<BD, F>& b) {
@@ -221,102 +240,166 @@ __device__ inline void groups(std::integer_sequence<int, G...>, f32x16 (&acc)[F]
 
 // ---- epilogue
 // Block B: MFMA tiles (B / 2, 2 (B % 2)) and the one to its right (F = 4), tile (B / 2, B % 2) (F = 2)
+// The sums pass through an empty assembly of each block's own: the compiler would join the blocks'
+// reads into one of a choice of accumulators, for which they would have to be in memory.
+template <int B> SWG_INLINE f32x16 apart(f32x16 v) {
+  asm volatile("; block %1" : "+a"(v) : "i"(B));
+  return v;
+}
 template <int F, int B>
-__device__ inline void put_block(const f32x16 (&acc)[F][F], float* out, int lane) {
+SWG_INLINE void put_block(const f32x16 (&acc)[F][F], float* out, int lane) {
   constexpr int W = Shape<F>::OUTW;
   if constexpr (F == 4) {
-    put_tile<W>(acc[B / 2][2 * (B % 2)], out, lane, 0);
-    put_tile<W>(acc[B / 2][2 * (B % 2) + 1], out, lane, 32);
+    put_tile<W>(apart<B>(acc[B / 2][2 * (B % 2)]), out, lane, 0);
+    put_tile<W>(apart<B>(acc[B / 2][2 * (B % 2) + 1]), out, lane, 32);
   } else {
-    put_tile<W>(acc[B / 2][B % 2], out, lane, 0);
+    put_tile<W>(apart<B>(acc[B / 2][B % 2]), out, lane, 0);
   }
 }
 
-// The wave's sums at (p0, q0) on their way out, a block of 32 rows after the other.  What the
-// epilogue reads for a block (the residual, or the old contents) is loaded a block ahead.
+template <int F>
+SWG_INLINE void put_any(const f32x16 (&acc)[F][F], float* out, int lane, int blk) {
+  switch (blk) {
+    case 0: put_block<F, 0>(acc, out, lane); break;
+    case 1: put_block<F, 1>(acc, out, lane); break;
+    case 2: put_block<F, 2>(acc, out, lane); break;
+    case 3: put_block<F, 3>(acc, out, lane); break;
+    case 4: if constexpr (F == 4) put_block<F, 4>(acc, out, lane); break;
+    case 5: if constexpr (F == 4) put_block<F, 5>(acc, out, lane); break;
+    case 6: if constexpr (F == 4) put_block<F, 6>(acc, out, lane); break;
+    default: if constexpr (F == 4) put_block<F, 7>(acc, out, lane); break;
+  }
+}
+
+// A wave's rows of a tensor of the epilogue: a window over those that exist, and the lane's place.
+struct Rows {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t at, row;   // bytes
+  __device__ inline Rows(const void* base, int64_t ld, int es, int64_t p0, int64_t q0, int n, int row_,
+                         int col) {
+    row = (uint32_t)(ld * es);
+    r = make_rsrc(uniform_ptr(static_cast<const char*>(base) + (p0 * ld + q0) * es),
+                  base ? __builtin_amdgcn_readfirstlane(clamp_bytes(n, row)) : 0u);
+    at = (uint32_t)row_ * row + (uint32_t)(col * es);
+  }
+  // `down` rows further
+  __device__ inline uint32_t below(int down) const { return at + (uint32_t)down * row; }
+};
+
+// at column bytes `col`, which carries kOOB where the column does not exist
+__device__ inline int column_at(uint32_t v, uint32_t col) {
+  return (int)((v + (col & 0x7fffffffu)) | (col & kOOB));
+}
+
+// The wave's sums at (p0, q0) on their way out, a block of 32 rows after the other, in two forms.
+// Where rows are of 16-byte multiples at 16-byte boundaries they go through buffer windows, which
+// drop what lies past the edges, and what the epilogue reads (the residual, or the old contents) is
+// loaded two blocks ahead.
 template <typename T, int F>
-__device__ inline void epilogue(const f32x16 (&acc)[F][F], const Product& g, float* part,
-                                int64_t ldp, float* out, int lane, int64_t p0, int64_t q0) {
+SWG_INLINE void epilogue_whole(const f32x16 (&acc)[F][F], const Product& g, float* out,
+                                      int lane, int64_t p0, int64_t q0) {
   constexpr int W = Shape<F>::OUTW, LANES = W / 8, ROWS = 64 / LANES, PASSES = 32 / ROWS;
   asm volatile("" : "+v"(lane));   // keeps what follows from lane out of the main loop's registers
   const int row = lane / LANES, col = 8 * (lane % LANES);
-  const int64_t q = q0 + col;
-  const T* more = part ? nullptr
-                       : static_cast<const T*>(g.accumulate ? g.out : g.residual);
-  const int64_t ldm = g.accumulate ? g.ldo : g.ldr;
-  Chunk<T> next[PASSES], bias[2];
-  auto load = [&](int blk) {
+  const int n = g.P - p0 < Shape<F>::WR ? (int)(g.P - p0) : Shape<F>::WR;
+  const float* src = out + out_at<W>(row, col);   // rows ROWS further: ROWS W floats
+  const void* read = g.accumulate ? g.out : g.residual;
+  const Rows more(read, g.accumulate ? g.ldo : g.ldr, 2, p0, q0, n, row, col);
+  const Rows to(g.out, g.ldo, 2, p0, q0, n, row, col), to_z(g.z, g.ldz, 2, p0, q0, n, row, col);
+  u32x4 ahead[2][PASSES], bias[2];
+  uint32_t cols[2];   // byte offsets of the blocks' left and right half, or none
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool has = q0 + W * h + col < g.Q;
+    cols[h] = (uint32_t)(W * h * 2) | (has ? 0u : kOOB);
+    bias[h] = u32x4{0, 0, 0, 0};
+    if (g.bias && has) {
+      Chunk<T> b;
+      b.load(static_cast<const T*>(g.bias) + q0 + W * h + col);
+      bias[h] = b.v[0];
+    }
+  }
+  auto load = [&](int pair, auto S) {
+    constexpr int side = decltype(S)::value;
+    uint32_t at = more.below(32 * pair);
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) {
-      const int64_t p = p0 + 32 * (blk / 2) + row + ROWS * k, c = q + W * (blk % 2);
-      next[k].zero();
-      if (more && p < g.P && c + 8 <= g.Q) next[k].load_stream(more + p * ldm + c);
+      ahead[side][k] =
+          __builtin_amdgcn_raw_buffer_load_b128(more.r, column_at(at, cols[side]), 0, 2);
+      at += ROWS * more.row;
     }
   };
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    bias[h].zero();
-    if (g.bias && !part && q + W * h + 8 <= g.Q)
-      bias[h].load(static_cast<const T*>(g.bias) + q + W * h);
+  for (int k = 0; k < PASSES; ++k) ahead[0][k] = ahead[1][k] = u32x4{0, 0, 0, 0};
+  if (read) {
+    load(0, std::integral_constant<int, 0>());
+    load(0, std::integral_constant<int, 1>());
   }
-  load(0);
-#pragma unroll 1
-  for (int blk = 0; blk < 2 * F; ++blk) {
-    switch (blk) {
-      case 0: put_block<F, 0>(acc, out, lane); break;
-      case 1: put_block<F, 1>(acc, out, lane); break;
-      case 2: put_block<F, 2>(acc, out, lane); break;
-      case 3: put_block<F, 3>(acc, out, lane); break;
-      case 4: if constexpr (F == 4) put_block<F, 4>(acc, out, lane); break;
-      case 5: if constexpr (F == 4) put_block<F, 5>(acc, out, lane); break;
-      case 6: if constexpr (F == 4) put_block<F, 6>(acc, out, lane); break;
-      default: if constexpr (F == 4) put_block<F, 7>(acc, out, lane); break;
-    }
-    Chunk<T> now[PASSES];
-#pragma unroll
-    for (int k = 0; k < PASSES; ++k) now[k] = next[k];
-    if (blk + 1 < 2 * F) load(blk + 1);
-    const Chunk<T> b = blk % 2 ? bias[1] : bias[0];
-    const int64_t c = q + W * (blk % 2);
+  auto finish_block = [&](int pair, auto S) {
+    constexpr int side = decltype(S)::value;
+    uint32_t at = to.below(32 * pair), at_z = to_z.below(32 * pair);
 #pragma unroll
     for (int k = 0; k < PASSES; ++k) {
-      const int64_t p = p0 + 32 * (blk / 2) + row + ROWS * k;
-      const float* src = out + out_at<W>(row + ROWS * k, col);
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
-      if (p >= g.P || c >= g.Q) continue;
-      if (part) {
-        f32x4* dst = reinterpret_cast<f32x4*>(part + p * ldp + c);
-        dst[0] = lo;
-        dst[1] = hi;
-        continue;
-      }
       float v[8], f[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-      if (c + 8 > g.Q) {
-        finish_chunk<T>(g, p, c, v);
-        continue;
-      }
-      b.widen(f);
+      for (int i = 0; i < 8; ++i) v[i] = src[k * ROWS * W + i];
+      Vec16<T>::widen(bias[side], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += f[i];
-      Chunk<T> o;
-      if (g.z) {
-        o.narrow(v);
-        o.store_stream(static_cast<T*>(g.z) + p * g.ldz + c);
-      }
+      if (g.z)
+        __builtin_amdgcn_raw_buffer_store_b128(Vec16<T>::narrow(v), to_z.r,
+                                               column_at(at_z, cols[side]), 0, 2);
       if (g.act != kActNone) activate8(g.act, g.beta, v);
-      now[k].widen(f);
+      Vec16<T>::widen(ahead[side][k], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += f[i];
-      o.narrow(v);
-      o.store_stream(static_cast<T*>(g.out) + p * g.ldo + c);
+      __builtin_amdgcn_raw_buffer_store_b128(Vec16<T>::narrow(v), to.r,
+                                             column_at(at, cols[side]), 0, 2);
+      at += ROWS * to.row;
+      at_z += ROWS * to_z.row;
+    }
+    if (read && pair + 1 < F) load(pair + 1, S);
+  };
+#pragma unroll 1
+  for (int blk = 0; blk < 2 * F; ++blk) {
+    put_any<F>(acc, out, lane, blk);
+    if (blk & 1) finish_block(blk / 2, std::integral_constant<int, 1>());
+    else finish_block(blk / 2, std::integral_constant<int, 0>());
+  }
+}
+
+// The other form: partial sums, or outputs of any alignment.
+template <typename T, int F>
+SWG_INLINE void epilogue_any(const f32x16 (&acc)[F][F], const Product& g, float* part,
+                                    int64_t ldp, float* out, int lane, int64_t p0, int64_t q0) {
+  constexpr int W = Shape<F>::OUTW, LANES = W / 8, ROWS = 64 / LANES;
+  asm volatile("" : "+v"(lane));
+#pragma unroll 1
+  for (int blk = 0; blk < 2 * F; ++blk) {
+    put_any<F>(acc, out, lane, blk);
+    const int64_t pb = p0 + 32 * (blk / 2), q = q0 + W * (blk % 2) + 8 * (lane % LANES);
+#pragma unroll 1
+    for (int row = lane / LANES; row < 32; row += ROWS) {
+      const float* src = out + out_at<W>(row, 8 * (lane % LANES));
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+      const int64_t p = pb + row;
+      if (p >= g.P || q >= g.Q) continue;
+      if (part) {
+        f32x4* dst = reinterpret_cast<f32x4*>(part + p * ldp + q);
+        dst[0] = lo;
+        dst[1] = hi;
+      } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+        finish_chunk<T>(g, p, q, v);
+      }
     }
   }
 }
 
-template <typename T, bool AD, bool BD, int F>
+template <typename T, bool AD, bool BD, int F, bool WHOLE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<F>::WAVES, Shape<F>::WAVES)))
 void product16_kernel(Product g, ProductGrid grid, float* part, int64_t ldp) {
   constexpr int P = Shape<F>::P, SLOT = Shape<F>::SLOT, LOADS = Shape<F>::LOADS;
@@ -368,14 +451,7 @@ void product16_kernel(Product g, ProductGrid grid, float* part, int64_t ldp) {
   __builtin_amdgcn_s_barrier();
   SWG_COMPILER_FENCE();
   for (uint32_t j = 0; j < mine; ++j) {
-#pragma unroll
-    for (int a = 0; a < F; ++a)
-#pragma unroll
-      for (int b = 0; b < F; ++b) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-        asm volatile("" : "+a"(acc[a][b]));   // in AGPRs from here on: no copies at the loop
-      }
+    clear(std::make_integer_sequence<int, F * F>{}, acc);
     read_all<T, AD, BD, F>(std::make_integer_sequence<int, 4 * F>{}, ring, sa, sb, frags[0]);
     for (int t = 4; t < cur.stages; t += 4) {
       SWG_STEP(0, true);
@@ -389,20 +465,26 @@ void product16_kernel(Product g, ProductGrid grid, float* part, int64_t ldp) {
     SWG_STEP(1, true);
     SWG_STEP(2, true);
     SWG_STEP(3, false);   // the next item's first stage is read after the epilogue
-    float* to = part ? part + (int64_t)cur.split * g.P * ldp : nullptr;
-    epilogue<T, F>(acc, g, to, ldp, outs + wave * Shape<F>::OUT, lane,
-                   (int64_t)cur.p0 + wp * Shape<F>::WR, (int64_t)cur.q0 + wq * Shape<F>::WR);
+    const int64_t p0 = (int64_t)cur.p0 + wp * Shape<F>::WR, q0 = (int64_t)cur.q0 + wq * Shape<F>::WR;
+    float* out = outs + wave * Shape<F>::OUT;
+    if constexpr (WHOLE) {
+      epilogue_whole<T, F>(acc, g, out, lane, p0, q0);
+    } else {
+      float* to = part ? part + (int64_t)cur.split * g.P * ldp : nullptr;
+      epilogue_any<T, F>(acc, g, to, ldp, out, lane, p0, q0);
+    }
     cur = nxt;
   }
 #undef SWG_STEP
   __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
 }
 
-// rows [n][cols] again with rows of ld elements, zeros past their end; a thread takes 8 columns
+// rows [n][cols] again with rows of ld elements, zeros up to a multiple of 8; a thread takes 8
+// columns
 template <typename T>
 __global__ __launch_bounds__(256) void pack_kernel(const T* src, int64_t lds, T* dst, int64_t ldd,
                                                    int64_t n, int64_t cols) {
-  const int64_t chunks = ldd / 8, total = n * chunks;
+  const int64_t chunks = (cols + 7) / 8, total = n * chunks;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
        e += (int64_t)gridDim.x * 256) {
     const int64_t r = e / chunks, c = (e % chunks) * 8;
@@ -419,13 +501,26 @@ __global__ __launch_bounds__(256) void pack_kernel(const T* src, int64_t lds, T*
   }
 }
 
+// Whether what the epilogue touches lies in rows of 16-byte multiples with 32-bit window offsets.
+bool rows_whole(const Product& g) {
+  const int64_t most = int64_t(1) << 22;
+  auto ok = [&](const void* p, int64_t ld) {
+    return !p || ((uintptr_t)p % 16 == 0 && ld % 8 == 0 && ld < most);
+  };
+  return g.Q % 8 == 0 && ok(g.out, g.ldo) && ok(g.z, g.ldz) && ok(g.residual, g.ldr);
+}
+
 template <typename T, bool AD, bool BD, int F>
 hipError_t tiles(const Product& g, const ProductGrid& grid, float* part, int64_t ldp, int cus,
                  hipStream_t stream) {
   const int64_t slots = (int64_t)cus * Shape<F>::WAVES;
   const int64_t n = grid.items < slots ? grid.items : slots;
-  SWG_LAUNCH((product16_kernel<T, AD, BD, F>), dim3((unsigned)n), dim3(kThreads), 0, stream, g,
-             grid, part, ldp);
+  if (!part && rows_whole(g))
+    SWG_LAUNCH((product16_kernel<T, AD, BD, F, true>), dim3((unsigned)n), dim3(kThreads), 0, stream,
+               g, grid, part, ldp);
+  else
+    SWG_LAUNCH((product16_kernel<T, AD, BD, F, false>), dim3((unsigned)n), dim3(kThreads), 0,
+               stream, g, grid, part, ldp);
   return hipGetLastError();
 }
 
@@ -440,8 +535,8 @@ hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, int64
 // An operand again in the workspace with rows of 16-byte multiples
 template <typename T>
 hipError_t pack(Operand& o, int64_t rows, int64_t R, void* to, hipStream_t stream) {
-  const int64_t n = o.deep ? rows : R, cols = o.deep ? R : rows, ld = ceil_div(cols, 8) * 8;
-  SWG_LAUNCH((pack_kernel<T>), dim3(stream_grid(n * (ld / 8))), dim3(256), 0, stream,
+  const int64_t n = o.deep ? rows : R, cols = o.deep ? R : rows, ld = packed_ld(cols);
+  SWG_LAUNCH((pack_kernel<T>), dim3(stream_grid(n * ceil_div(cols, 8))), dim3(256), 0, stream,
              static_cast<const T*>(o.p), o.ld, static_cast<T*>(to), ld, n, cols);
   o.p = to;
   o.ld = ld;

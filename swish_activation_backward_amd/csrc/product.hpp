@@ -98,9 +98,10 @@ template <int W> __device__ inline int out_at(int row, int col) {
   return (row * W + col) ^ (((row >> 2) & 1) << 5);
 }
 
-// 32 x 32 sums of one MFMA tile into columns c0 .. of the block
+// 32 x 32 sums of one MFMA tile into columns c0 .. of the block: out_at of their rows and columns,
+// two lane addresses and constants
 template <int W>
-__device__ inline void put_tile(const f32x16& v, float* out, int lane, int c0) {
+__device__ __attribute__((always_inline)) inline void put_tile(const f32x16 v, float* out, int lane, int c0) {
 #pragma unroll
   for (int r = 0; r < 16; ++r)
     out[out_at<W>(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), c0 + (lane & 31))] = v[r];
