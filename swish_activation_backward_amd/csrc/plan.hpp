@@ -376,17 +376,19 @@ inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
 }
 
 // One product of the linear layer: output [P, Q], contraction R, in tiles of edge 64 f (f = 4 or 2
-// for 16-bit tensors, 2 or 1 for fp32), the contraction cut into `splits` ranges of `len` whose fp32
-// sums [P, ldp] are joined in order.  16-bit operands that do not lie in rows of 16-byte multiples
-// are laid out again (pack_a, pack_b) in the workspace before.
+// for 16-bit tensors, 2 or 1 for fp32).  The first `whole` tiles, whole rounds over the CUs, are
+// finished by one workgroup each; the contraction of the others is cut into `splits` ranges of
+// `len`, so that they too fill the CUs, and the ranges' fp32 sums are joined in order.  16-bit
+// operands that do not lie in rows of 16-byte multiples are laid out again (pack_a, pack_b) in the
+// workspace before.
 //
 // The tile and the split are those of the smallest estimate: rounds of items over the CUs, times an
 // item's stages (32 deep) and what it spends before and after them, plus the partial sums' trip
-// through memory and the launch that joins them.  force_f: 4 or 2 overrides the tile (16-bit).
+// through memory and the launches.  force_f: 4 or 2 overrides the tile (16-bit).
 struct ProductPlan {
   int f;
-  int64_t np, nq;
-  int64_t splits, len, ldp;
+  int64_t np, nq, whole;
+  int64_t splits, len;
   bool pack_a, pack_b;
   size_t pack_a_at, pack_b_at, part_at;
   size_t ws_bytes;
@@ -402,46 +404,54 @@ struct ProductCost {
   int f;
   int64_t busy, least, ends, share;
 };
-constexpr ProductCost kProduct16[2] = {{4, 800, 800, 12000, 1}, {2, 280, 450, 3000, 2}};
+constexpr ProductCost kProduct16[2] = {{4, 800, 800, 12000, 1}, {2, 270, 600, 4000, 2}};
 constexpr ProductCost kProduct32[2] = {{2, 1900, 1900, 4000, 2}, {1, 480, 1000, 2000, 4}};
-constexpr int64_t kJoinNs = 5000;
+constexpr int64_t kJoinNs = 6000;     // the join's launch and, of whole rounds before, the split's
 
-inline int64_t product_ns(int64_t P, int64_t Q, int64_t R, const ProductCost& c, int64_t splits) {
-  const int64_t items = ceil_div(P, tile_edge(c.f)) * ceil_div(Q, tile_edge(c.f)) * splits;
-  const int64_t stages = ceil_div(ceil_div(R, splits), 4 * kTileR) * 4;
+// `items` of `len` contraction indices each
+inline int64_t product_items_ns(int64_t items, int64_t len, const ProductCost& c) {
+  if (items <= 0) return 0;
+  const int64_t stages = ceil_div(len, 4 * kTileR) * 4;
   int64_t share = ceil_div(items, kGemmSlots);
   if (share > c.share) share = c.share;
   const int64_t stage = c.busy * share > c.least ? c.busy * share : c.least;
-  int64_t t = ceil_div(items, kGemmSlots * share) * (stages * stage + c.ends);
-  if (splits > 1) t += kJoinNs + splits * P * Q * 8 / kStreamBytesPerNs;
-  return t;
+  return ceil_div(items, kGemmSlots * share) * (stages * stage + c.ends);
 }
 
 inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool pack_a,
                                 bool a_deep, bool pack_b, bool b_deep, int force_f) {
   ProductPlan p{};
-  p.splits = 1;
   int64_t best = -1;
+  auto consider = [&](const ProductCost& c, int64_t whole, int64_t rest, int64_t s) {
+    int64_t t = product_items_ns(whole, R, c) + product_items_ns(rest * s, ceil_div(R, s), c);
+    const int64_t edge = tile_edge(c.f);
+    if (s > 1) t += kJoinNs + s * rest * edge * edge * 8 / kStreamBytesPerNs;
+    if (best >= 0 && t >= best) return;
+    best = t;
+    p.f = c.f;
+    p.whole = s > 1 ? whole : whole + rest;
+    p.splits = s;
+  };
   for (const ProductCost& c : dtype == 2 ? kProduct32 : kProduct16) {
     if (dtype != 2 && force_f != 0 && c.f != force_f) continue;
     const int64_t tiles = ceil_div(P, tile_edge(c.f)) * ceil_div(Q, tile_edge(c.f));
-    int64_t most = ceil_div(c.share * kGemmSlots, tiles < 1 ? 1 : tiles);
-    if (most > R / 256) most = R / 256;
-    for (int64_t s = 1; s == 1 || s <= most; ++s) {
-      const int64_t t = product_ns(P, Q, R, c, s);
-      if (best < 0 || t < best) {
-        best = t;
-        p.f = c.f;
-        p.splits = s;
-      }
+    consider(c, tiles, 0, 1);
+    for (int64_t share = 1; share <= c.share; share *= 2) {
+      const int64_t slots = share * kGemmSlots, whole = tiles / slots * slots, rest = tiles - whole;
+      if (rest == 0) continue;
+      const int64_t most = slots / rest < R / 256 ? slots / rest : R / 256;
+      // 2, 3, 4, 6, 8, 12, ... and the most: this runs in every call
+      for (int64_t s = 2; s < most; s += s & (s - 1) ? s / 3 : s / 2) consider(c, whole, rest, s);
+      if (most > 1) consider(c, whole, rest, most);
     }
   }
   p.len = ceil_div(ceil_div(R, p.splits), 4 * kTileR) * 4 * kTileR;
-  p.splits = R > 0 ? ceil_div(R, p.len) : 1;
+  if (R > 0) p.splits = ceil_div(R, p.len);
   if (p.len < 1) p.len = 1;
   p.np = ceil_div(P, tile_edge(p.f));
   p.nq = ceil_div(Q, tile_edge(p.f));
-  p.ldp = ceil_div(Q, 8) * 8;
+  const int64_t rest = p.np * p.nq - p.whole;
+  if (p.splits == 1) p.whole += rest;
   auto packed = [](int64_t rows, int64_t deep_len, bool deep) {
     const int64_t n = deep ? rows : deep_len, c = deep ? deep_len : rows;
     return (size_t)(n * packed_ld(c)) * 2;
@@ -457,7 +467,7 @@ inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool
   }
   if (p.splits > 1) {
     p.part_at = p.ws_bytes;
-    p.ws_bytes += (size_t)(p.splits * P * p.ldp) * sizeof(float);
+    p.ws_bytes += (size_t)(p.splits * rest * tile_edge(p.f) * tile_edge(p.f)) * sizeof(float);
   }
   return p;
 }

@@ -368,32 +368,31 @@ SWG_INLINE void epilogue_whole(const f32x16 (&acc)[F][F], const Product& g, floa
   }
 }
 
-// The other form: partial sums, or outputs of any alignment.
+// The other form: a tile's partial sums (part: the wave's place in it), or outputs of any alignment.
 template <typename T, int F>
-SWG_INLINE void epilogue_any(const f32x16 (&acc)[F][F], const Product& g, float* part,
-                                    int64_t ldp, float* out, int lane, int64_t p0, int64_t q0) {
+SWG_INLINE void epilogue_any(const f32x16 (&acc)[F][F], const Product& g, float* part, float* out,
+                             int lane, int64_t p0, int64_t q0) {
   constexpr int W = Shape<F>::OUTW, LANES = W / 8, ROWS = 64 / LANES;
   asm volatile("" : "+v"(lane));
 #pragma unroll 1
   for (int blk = 0; blk < 2 * F; ++blk) {
     put_any<F>(acc, out, lane, blk);
-    const int64_t pb = p0 + 32 * (blk / 2), q = q0 + W * (blk % 2) + 8 * (lane % LANES);
+    const int pb = 32 * (blk / 2), q = W * (blk % 2) + 8 * (lane % LANES);
 #pragma unroll 1
     for (int row = lane / LANES; row < 32; row += ROWS) {
       const float* src = out + out_at<W>(row, 8 * (lane % LANES));
       const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
       const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
-      const int64_t p = pb + row;
-      if (p >= g.P || q >= g.Q) continue;
+      if (p0 + pb + row >= g.P || q0 + q >= g.Q) continue;
       if (part) {
-        f32x4* dst = reinterpret_cast<f32x4*>(part + p * ldp + q);
+        f32x4* dst = reinterpret_cast<f32x4*>(part + (pb + row) * Shape<F>::P + q);
         dst[0] = lo;
         dst[1] = hi;
       } else {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-        finish_chunk<T>(g, p, q, v);
+        finish_chunk<T>(g, p0 + pb + row, q0 + q, v);
       }
     }
   }
@@ -401,7 +400,7 @@ SWG_INLINE void epilogue_any(const f32x16 (&acc)[F][F], const Product& g, float*
 
 template <typename T, bool AD, bool BD, int F, bool WHOLE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(Shape<F>::WAVES, Shape<F>::WAVES)))
-void product16_kernel(Product g, ProductGrid grid, float* part, int64_t ldp) {
+void product16_kernel(Product g, ProductGrid grid, float* part) {
   constexpr int P = Shape<F>::P, SLOT = Shape<F>::SLOT, LOADS = Shape<F>::LOADS;
   __shared__ __attribute__((aligned(1024))) uint16_t ring[4 * SLOT];
   __shared__ __attribute__((aligned(16))) float outs[4 * Shape<F>::OUT];
@@ -470,8 +469,11 @@ void product16_kernel(Product g, ProductGrid grid, float* part, int64_t ldp) {
     if constexpr (WHOLE) {
       epilogue_whole<T, F>(acc, g, out, lane, p0, q0);
     } else {
-      float* to = part ? part + (int64_t)cur.split * g.P * ldp : nullptr;
-      epilogue_any<T, F>(acc, g, to, ldp, out, lane, p0, q0);
+      float* to = nullptr;
+      if (part)
+        to = part + ((int64_t)cur.split * grid.tiles + cur.tile) * P * P +
+             wp * Shape<F>::WR * P + wq * Shape<F>::WR;
+      epilogue_any<T, F>(acc, g, to, out, lane, p0, q0);
     }
     cur = nxt;
   }
@@ -511,25 +513,28 @@ bool rows_whole(const Product& g) {
 }
 
 template <typename T, bool AD, bool BD, int F>
-hipError_t tiles(const Product& g, const ProductGrid& grid, float* part, int64_t ldp, int cus,
+hipError_t tiles(const Product& g, const ProductGrid& grid, float* part, int cus,
                  hipStream_t stream) {
   const int64_t slots = (int64_t)cus * Shape<F>::WAVES;
-  const int64_t n = grid.items < slots ? grid.items : slots;
+  const dim3 n((unsigned)(grid.items < slots ? grid.items : slots)), block(kThreads);
   if (!part && rows_whole(g))
-    SWG_LAUNCH((product16_kernel<T, AD, BD, F, true>), dim3((unsigned)n), dim3(kThreads), 0, stream,
-               g, grid, part, ldp);
+    SWG_LAUNCH((product16_kernel<T, AD, BD, F, true>), n, block, 0, stream, g, grid, part);
   else
-    SWG_LAUNCH((product16_kernel<T, AD, BD, F, false>), dim3((unsigned)n), dim3(kThreads), 0,
-               stream, g, grid, part, ldp);
+    SWG_LAUNCH((product16_kernel<T, AD, BD, F, false>), n, block, 0, stream, g, grid, part);
   return hipGetLastError();
 }
 
-template <typename T, int F>
-hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, int64_t ldp, int cus,
-                   hipStream_t stream) {
-  if (g.a.deep && !g.b.deep) return tiles<T, true, false, F>(g, grid, part, ldp, cus, stream);
-  if (g.a.deep) return tiles<T, true, true, F>(g, grid, part, ldp, cus, stream);
-  return tiles<T, false, false, F>(g, grid, part, ldp, cus, stream);
+template <typename T>
+hipError_t layouts(const Product& g, const ProductPlan& p, const ProductGrid& grid, float* part,
+                   int cus, hipStream_t stream) {
+  if (p.f == 4) {
+    if (g.a.deep && !g.b.deep) return tiles<T, true, false, 4>(g, grid, part, cus, stream);
+    if (g.a.deep) return tiles<T, true, true, 4>(g, grid, part, cus, stream);
+    return tiles<T, false, false, 4>(g, grid, part, cus, stream);
+  }
+  if (g.a.deep && !g.b.deep) return tiles<T, true, false, 2>(g, grid, part, cus, stream);
+  if (g.a.deep) return tiles<T, true, true, 2>(g, grid, part, cus, stream);
+  return tiles<T, false, false, 2>(g, grid, part, cus, stream);
 }
 
 // An operand again in the workspace with rows of 16-byte multiples
@@ -558,12 +563,15 @@ hipError_t product16_t(Product g, const ProductPlan& p, void* ws, int cus, hipSt
     const hipError_t e = pack<T>(g.b, g.Q, g.R, w + p.pack_b_at, stream);
     if (e != hipSuccess) return e;
   }
-  const ProductGrid grid = product_grid(p);
-  float* part = p.splits > 1 ? reinterpret_cast<float*>(w + p.part_at) : nullptr;
-  hipError_t e = p.f == 4 ? layouts<T, 4>(g, grid, part, p.ldp, cus, stream)
-                          : layouts<T, 2>(g, grid, part, p.ldp, cus, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
-  return product_join<T>(g, p, part, stream);
+  if (p.whole > 0) {
+    const hipError_t e = layouts<T>(g, p, product_grid(p, true), nullptr, cus, stream);
+    if (e != hipSuccess || p.splits == 1) return e;
+  }
+  const ProductGrid rest = product_grid(p, false);
+  float* part = reinterpret_cast<float*>(w + p.part_at);
+  const hipError_t e = layouts<T>(g, p, rest, part, cus, stream);
+  if (e != hipSuccess) return e;
+  return product_join<T>(g, p, rest, part, stream);
 }
 
 }  // namespace

@@ -46,29 +46,32 @@ __device__ inline void finish_chunk(const Product& a, int64_t p, int64_t q, floa
 // ---- pieces of work
 constexpr int kDepth = 32;   // contraction indices of a stage
 
-// A piece of work: a tile and a range of the contraction.
+// A piece of work: a tile and a range of the contraction; `tile` counts from the launch's first.
 struct ProductItem {
-  int split, p0, q0, begin, end, stages;
+  int split, tile, p0, q0, begin, end, stages;
 };
 
-struct ProductGrid {     // tiles, group of tile rows, ranges of `len`, items
-  uint32_t np, nq, group, tiles, items;
+// Tiles of the output (rows, columns, tile rows of a band), those of a launch (from `first` on,
+// `tiles` of them), and the ranges that the contraction is cut into for them.
+struct ProductGrid {
+  uint32_t np, nq, band, first, tiles, items;
   int64_t len;
 };
 
-// Tiles run down `group` tile rows before they move on a column, so that those that run at once on
+// Tiles run down a band of tile rows before they move on a column, so that those that run at once on
 // an XCD (consecutive ones) share rows and columns alike.
 template <int P, int ROUND>
 __device__ inline ProductItem product_item(const ProductGrid& g, uint32_t L, bool live, int64_t R) {
   ProductItem t;
   const uint32_t l = live ? L : 0;
   const uint32_t split = l / g.tiles, tile = l % g.tiles;
-  const uint32_t full = g.group * g.nq, band = tile / full, in = tile % full;
-  const uint32_t first = band * g.group;
-  const uint32_t rows = g.np - first < g.group ? g.np - first : g.group;
+  const uint32_t full = g.band * g.nq, band = (g.first + tile) / full, in = (g.first + tile) % full;
+  const uint32_t top = band * g.band;
+  const uint32_t rows = g.np - top < g.band ? g.np - top : g.band;
   const int64_t b = split * g.len, e = b + g.len < R ? b + g.len : R;
   t.split = __builtin_amdgcn_readfirstlane((int)split);
-  t.p0 = __builtin_amdgcn_readfirstlane((int)(first + in % rows) * P);
+  t.tile = __builtin_amdgcn_readfirstlane((int)tile);
+  t.p0 = __builtin_amdgcn_readfirstlane((int)(top + in % rows) * P);
   t.q0 = __builtin_amdgcn_readfirstlane((int)(in / rows) * P);
   t.begin = __builtin_amdgcn_readfirstlane((int)b);
   // nothing to fetch past the last item
@@ -80,14 +83,16 @@ __device__ inline ProductItem product_item(const ProductGrid& g, uint32_t L, boo
   return t;
 }
 
-inline ProductGrid product_grid(const ProductPlan& p) {
+// The launch of the whole tiles, and of the others.
+inline ProductGrid product_grid(const ProductPlan& p, bool whole) {
   ProductGrid g;
   g.np = (uint32_t)p.np;
   g.nq = (uint32_t)p.nq;
-  g.group = 4;
-  g.tiles = (uint32_t)(p.np * p.nq);
-  g.items = (uint32_t)(p.np * p.nq * p.splits);
-  g.len = p.len;
+  g.band = 4;
+  g.first = whole ? 0 : (uint32_t)p.whole;
+  g.tiles = (uint32_t)(whole ? p.whole : p.np * p.nq - p.whole);
+  g.items = whole ? g.tiles : g.tiles * (uint32_t)p.splits;
+  g.len = whole ? p.splits * p.len : p.len;
   return g;
 }
 
@@ -108,18 +113,24 @@ __device__ __attribute__((always_inline)) inline void put_tile(const f32x16 v, f
 }
 
 // ---- joining partial sums
-// out from the `splits` partial sums, in order; a thread takes 8 columns of a row.
+// out from the sums [split][tile][P][P] of tiles of edge P, in order; a thread takes 8 columns of a
+// row.
 template <typename T>
-__global__ __launch_bounds__(256) void product_join_kernel(Product g, const float* part,
-                                                           int64_t splits, int64_t ldp,
-                                                           int64_t chunks) {
-  const int64_t total = g.P * chunks, plane = g.P * ldp;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
+__global__ __launch_bounds__(256) void product_join_kernel(Product g, ProductGrid grid, int P,
+                                                           const float* part, int splits) {
+  const int64_t plane = (int64_t)grid.tiles * P * P;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < plane / 8;
        e += (int64_t)gridDim.x * 256) {
-    const int64_t p = e / chunks, q = (e % chunks) * 8;
-    const float* src = part + p * ldp + q;
+    const uint32_t tile = (uint32_t)(e / (P * P / 8)), in = (uint32_t)(e % (P * P / 8));
+    const uint32_t full = grid.band * grid.nq, band = (grid.first + tile) / full;
+    const uint32_t at = (grid.first + tile) % full, top = band * grid.band;
+    const uint32_t rows = grid.np - top < grid.band ? grid.np - top : grid.band;
+    const int64_t p = (int64_t)(top + at % rows) * P + in / (P / 8);
+    const int64_t q = (int64_t)(at / rows) * P + in % (P / 8) * 8;
+    if (p >= g.P || q >= g.Q) continue;
+    const float* src = part + e * 8;
     f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
-    for (int64_t s = 1; s < splits; ++s) {
+    for (int s = 1; s < splits; ++s) {
       lo += *reinterpret_cast<const f32x4*>(src + s * plane);
       hi += *reinterpret_cast<const f32x4*>(src + s * plane + 4);
     }
@@ -136,11 +147,11 @@ inline unsigned stream_grid(int64_t items) {
 }
 
 template <typename T>
-inline hipError_t product_join(const Product& g, const ProductPlan& p, const float* part,
-                               hipStream_t stream) {
-  const int64_t chunks = ceil_div(g.Q, 8);
-  SWG_LAUNCH((product_join_kernel<T>), dim3(stream_grid(g.P * chunks)), dim3(256), 0, stream, g,
-             part, p.splits, p.ldp, chunks);
+inline hipError_t product_join(const Product& g, const ProductPlan& p, const ProductGrid& grid,
+                               const float* part, hipStream_t stream) {
+  const int P = (int)tile_edge(p.f);
+  SWG_LAUNCH((product_join_kernel<T>), dim3(stream_grid((int64_t)grid.tiles * P * P / 8)), dim3(256),
+             0, stream, g, grid, P, part, (int)p.splits);
   return hipGetLastError();
 }
 

@@ -71,7 +71,7 @@ template <bool DEEP, int F> struct Part {
 
 template <bool AD, bool BD, int F>
 __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductGrid grid,
-                                                             float* part, int64_t ldp) {
+                                                             float* part) {
   typedef Part<AD, F> A;
   typedef Part<BD, F> B;
   constexpr int P = 64 * F, WR = 32 * F, BUF = A::FLOATS + B::FLOATS;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
   }
   // out, 32 x 32 sums of a wave at a time
   float* out = lds + wave * 1024;
-  if (part) part += (int64_t)t.split * g.P * ldp;
+  if (part) part += ((int64_t)t.split * grid.tiles + t.tile) * P * P;
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
         if (p >= g.P || q >= g.Q) continue;
         if (part) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) part[p * ldp + q + e] = v[e];
+          for (int e = 0; e < 8; ++e) part[(p - t.p0) * P + (q - t.q0) + e] = v[e];
         } else {
           finish_chunk<float>(g, p, q, v);
         }
@@ -158,28 +158,32 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
 }
 
 template <int F>
-hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, int64_t ldp,
-                   hipStream_t stream) {
+hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, hipStream_t stream) {
   const dim3 blocks(grid.items), block(kThreads);
   if (g.a.deep && !g.b.deep)
-    SWG_LAUNCH((product32_kernel<true, false, F>), blocks, block, 0, stream, g, grid, part, ldp);
+    SWG_LAUNCH((product32_kernel<true, false, F>), blocks, block, 0, stream, g, grid, part);
   else if (g.a.deep)
-    SWG_LAUNCH((product32_kernel<true, true, F>), blocks, block, 0, stream, g, grid, part, ldp);
+    SWG_LAUNCH((product32_kernel<true, true, F>), blocks, block, 0, stream, g, grid, part);
   else
-    SWG_LAUNCH((product32_kernel<false, false, F>), blocks, block, 0, stream, g, grid, part, ldp);
+    SWG_LAUNCH((product32_kernel<false, false, F>), blocks, block, 0, stream, g, grid, part);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_product32(const Product& g, const ProductPlan& p, void* ws, hipStream_t stream) {
-  const ProductGrid grid = product_grid(p);
-  float* part = nullptr;
-  if (p.splits > 1) part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_at);
-  const hipError_t e = p.f == 2 ? layouts<2>(g, grid, part, p.ldp, stream)
-                                : layouts<1>(g, grid, part, p.ldp, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
-  return product_join<float>(g, p, part, stream);
+  auto run = [&](const ProductGrid& grid, float* part) {
+    return p.f == 2 ? layouts<2>(g, grid, part, stream) : layouts<1>(g, grid, part, stream);
+  };
+  if (p.whole > 0) {
+    const hipError_t e = run(product_grid(p, true), nullptr);
+    if (e != hipSuccess || p.splits == 1) return e;
+  }
+  const ProductGrid rest = product_grid(p, false);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_at);
+  const hipError_t e = run(rest, part);
+  if (e != hipSuccess) return e;
+  return product_join<float>(g, p, rest, part, stream);
 }
 
 }  // namespace swg
