@@ -223,7 +223,11 @@ SWG_INLINE void group(f32x16 (&acc)[F][F], const Frags<T, F>& f, Frags<T, F>& fn
                              const uint16_t* dst, const Side<AD, F>& a, const Side<BD, F>& b) {
   mma<T, F, G * (F / 2)>(acc, f);
   if constexpr (F == 4) mma<T, F, G * (F / 2) + 1>(acc, f);
-  if constexpr (NEXT) read_one<T, AD, BD, F, G>(next, a, b, fn);
+  // the reads end a quarter early: a step begins with a wait for the last of them
+  if constexpr (NEXT && G < 3 * F) {
+    read_one<T, AD, BD, F, G * 4 / 3>(next, a, b, fn);
+    if constexpr ((G + 1) * 4 / 3 - G * 4 / 3 == 2) read_one<T, AD, BD, F, G * 4 / 3 + 1>(next, a, b, fn);
+  }
   if constexpr ((G & 1) != 0) load<AD, BD, F, (G >> 1)>(s, dst, a, b);
   if constexpr (G == 2 * F - 1) s.a.advance();
   if constexpr (G == 4 * F - 1) s.b.advance();

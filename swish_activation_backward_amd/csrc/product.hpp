@@ -113,22 +113,23 @@ __device__ __attribute__((always_inline)) inline void put_tile(const f32x16 v, f
 }
 
 // ---- joining partial sums
-// out from the sums [split][tile][P][P] of tiles of edge P, in order; a thread takes 8 columns of a
-// row.
+// out from the sums [split][tile][P][P] of tiles of edge P, in order; a thread takes 8 columns of
+// one of a tile's first `height` rows (fewer than P exist where there is one tile row).
 template <typename T>
-__global__ __launch_bounds__(256) void product_join_kernel(Product g, ProductGrid grid, int P,
-                                                           const float* part, int splits) {
+__global__ __launch_bounds__(256) void product_join_kernel(Product g, ProductGrid grid, uint32_t P,
+                                                           uint32_t height, const float* part,
+                                                           int splits) {
   const int64_t plane = (int64_t)grid.tiles * P * P;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < plane / 8;
-       e += (int64_t)gridDim.x * 256) {
-    const uint32_t tile = (uint32_t)(e / (P * P / 8)), in = (uint32_t)(e % (P * P / 8));
+  const uint32_t each = height * P / 8, total = grid.tiles * each;
+  for (uint32_t e = blockIdx.x * 256 + threadIdx.x; e < total; e += gridDim.x * 256) {
+    const uint32_t tile = e / each, in = e % each;
     const uint32_t full = grid.band * grid.nq, band = (grid.first + tile) / full;
     const uint32_t at = (grid.first + tile) % full, top = band * grid.band;
     const uint32_t rows = grid.np - top < grid.band ? grid.np - top : grid.band;
     const int64_t p = (int64_t)(top + at % rows) * P + in / (P / 8);
     const int64_t q = (int64_t)(at / rows) * P + in % (P / 8) * 8;
     if (p >= g.P || q >= g.Q) continue;
-    const float* src = part + e * 8;
+    const float* src = part + (int64_t)tile * P * P + in * 8;
     f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
     for (int s = 1; s < splits; ++s) {
       lo += *reinterpret_cast<const f32x4*>(src + s * plane);
@@ -149,9 +150,10 @@ inline unsigned stream_grid(int64_t items) {
 template <typename T>
 inline hipError_t product_join(const Product& g, const ProductPlan& p, const ProductGrid& grid,
                                const float* part, hipStream_t stream) {
-  const int P = (int)tile_edge(p.f);
-  SWG_LAUNCH((product_join_kernel<T>), dim3(stream_grid((int64_t)grid.tiles * P * P / 8)), dim3(256),
-             0, stream, g, grid, P, part, (int)p.splits);
+  const uint32_t P = (uint32_t)tile_edge(p.f);
+  const uint32_t height = p.np == 1 ? (uint32_t)g.P : P;
+  SWG_LAUNCH((product_join_kernel<T>), dim3(stream_grid((int64_t)grid.tiles * height * P / 8)),
+             dim3(256), 0, stream, g, grid, P, height, part, (int)p.splits);
   return hipGetLastError();
 }
 

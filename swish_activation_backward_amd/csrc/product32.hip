@@ -4,10 +4,12 @@
 // with operands of any alignment, deep or flat (see product.hip).
 //
 // A workgroup of four waves (2 x 2) owns a tile of edge 64 F, each wave 32 F x 32 F outputs.  A
-// stage of 32 contraction indices is loaded into registers while the one before it is multiplied,
+// stage of 32 contraction indices is loaded into registers while the two before it are multiplied,
 // and written to the other of two LDS buffers: a deep operand as [row][32], of which a lane reads
 // four consecutive indices at once, a flat one as [32][row].  Lane half h takes index 8 j + 4 h + s
 // in step s of a group j, of both operands alike.
+#include <type_traits>
+
 #include "mma.hpp"
 #include "product.hpp"
 
@@ -32,25 +34,44 @@ template <bool DEEP, int F> struct Part {
     return DEEP ? (threadIdx.x % 8) * 4 : threadIdx.x / (P / 4) + kThreads / (P / 4) * h;
   }
 
-  // rows row0 .. of `rows`, contraction r0 .. up to `end`; 0 past them
-  __device__ inline void load(const float* src, int64_t ld, int64_t row0, int64_t rows, int64_t r0,
-                              int64_t end) {
+  // The vectors' places in memory, a stage further with every load.
+  struct Source {
+    const float* q[V];
+    int rows[V];      // of the vector's rows, those that exist (deep: 1 or 0)
+    int64_t step;
+    int left;         // contraction indices
+    __device__ inline Source(const float* src, int64_t ld, int64_t row0, int64_t rows_, int begin,
+                             int end) {
+      left = end - begin;
+      step = DEEP ? kDepth : kDepth * ld;
 #pragma unroll
-    for (int h = 0; h < V; ++h) {
-      const int64_t p = row0 + row(h), r = r0 + deep(h);
-      const int64_t left = DEEP ? end - r : rows - p;   // along the vector
-      v[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (DEEP ? p >= rows : r >= end) continue;
-      const float* q = src + (DEEP ? p * ld + r : r * ld + p);
-      if (left >= 4) {
-        const u32x4_el4 u = *reinterpret_cast<const u32x4_el4*>(q);
-        v[h] = __builtin_bit_cast(f32x4, u);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (e < left) v[h][e] = q[e];
+      for (int h = 0; h < V; ++h) {
+        const int64_t p = row0 + row(h), r = begin + deep(h);
+        const int64_t n = rows_ - p, most = DEEP ? 1 : 4;
+        rows[h] = (int)(n < 0 ? 0 : n < most ? n : most);
+        q[h] = src + (DEEP ? p * ld + r : r * ld + p);
       }
     }
+  };
+
+  // 0 past the rows and the contraction's end, where nothing is read
+  __device__ inline void load(Source& s) {
+#pragma unroll
+    for (int h = 0; h < V; ++h) {
+      const int along = s.left - deep(h);
+      const int n = DEEP ? (s.rows[h] ? along : 0) : (along > 0 ? s.rows[h] : 0);
+      v[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (n >= 4) {
+        const u32x4_el4 u = *reinterpret_cast<const u32x4_el4*>(s.q[h]);
+        v[h] = __builtin_bit_cast(f32x4, u);
+      } else if (n > 0) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e < n) v[h][e] = s.q[h][e];
+      }
+      s.q[h] += s.step;
+    }
+    s.left -= kDepth;
   }
   __device__ inline void store(float* lds) const {
 #pragma unroll
@@ -80,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
   const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wp = wave / 2, wq = wave % 2;
-  const ProductItem t = product_item<P, kDepth>(grid, (uint32_t)xcd_remap(blockIdx.x, gridDim.x),
+  const ProductItem t = product_item<P, 2 * kDepth>(grid, (uint32_t)xcd_remap(blockIdx.x, gridDim.x),
                                                 true, g.R);
   const float* pa = static_cast<const float*>(g.a.p);
   const float* pb = static_cast<const float*>(g.b.p);
@@ -91,22 +112,19 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
     for (int j = 0; j < F; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  A a;
-  B b;
-  a.load(pa, g.a.ld, t.p0, g.P, t.begin, t.end);
-  b.load(pb, g.b.ld, t.q0, g.Q, t.begin, t.end);
-  a.store(lds);
-  b.store(lds + A::FLOATS);
-  __syncthreads();
-  for (int st = 0; st < t.stages; ++st) {
-    const float* cur = lds + (st & 1) * BUF;
-    float* other = lds + ((st & 1) ^ 1) * BUF;
-    const bool more = st + 1 < t.stages;
-    if (more) {
-      const int64_t r = t.begin + (int64_t)(st + 1) * kDepth;
-      a.load(pa, g.a.ld, t.p0, g.P, r, t.end);
-      b.load(pb, g.b.ld, t.q0, g.Q, r, t.end);
-    }
+  // two stages in flight: a set of registers is loaded again as soon as it is written to LDS
+  A a[2];
+  B b[2];
+  typename A::Source sa(pa, g.a.ld, t.p0, g.P, t.begin, t.end);
+  typename B::Source sb(pb, g.b.ld, t.q0, g.Q, t.begin, t.end);
+  auto load = [&](auto Set) {
+    a[decltype(Set)::value].load(sa);
+    b[decltype(Set)::value].load(sb);
+  };
+  auto step = [&](auto Set) {
+    constexpr int set = decltype(Set)::value;   // of the next stage, odd or even
+    const float* cur = lds + (set ^ 1) * BUF;
+    float* other = lds + set * BUF;
 #pragma unroll
     for (int j = 0; j < kDepth / 8; ++j) {
       f32x4 fa[F], fb[F];
@@ -123,11 +141,22 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
           for (int k = 0; k < F; ++k)
             acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i][s], fb[k][s], acc[i][k], 0, 0, 0);
     }
-    if (more) {
-      a.store(other);
-      b.store(other + A::FLOATS);
-    }
+    a[set].store(other);
+    b[set].store(other + A::FLOATS);
+    load(Set);
     __syncthreads();
+  };
+  constexpr std::integral_constant<int, 0> kEven{};
+  constexpr std::integral_constant<int, 1> kOdd{};
+  load(kEven);
+  load(kOdd);
+  a[0].store(lds);
+  b[0].store(lds + A::FLOATS);
+  load(kEven);
+  __syncthreads();
+  for (int st = 0; st < t.stages; st += 2) {   // an even number of stages
+    step(kOdd);
+    step(kEven);
   }
   // out, 32 x 32 sums of a wave at a time
   float* out = lds + wave * 1024;
