@@ -380,7 +380,7 @@ inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
 // finished by one workgroup each; the contraction of the others is cut into `splits` ranges of
 // `len`, so that they too fill the CUs, and the ranges' fp32 sums are joined in order.  16-bit
 // operands that do not lie in rows of 16-byte multiples are laid out again (pack_a, pack_b) in the
-// workspace before.
+// workspace before, and so are fp32 operands with fewer than four elements along their rows.
 //
 // The tile and the split are those of the smallest estimate: rounds of items over the CUs, times an
 // item's stages (32 deep) and what it spends before and after them, plus the partial sums' trip
@@ -394,7 +394,7 @@ struct ProductPlan {
   size_t ws_bytes;
 };
 
-// Row stride of a 16-bit operand that is laid out again: whole 128-byte lines, so that the 64-byte
+// Row stride of an operand that is laid out again: whole 128-byte lines, so that the 64-byte
 // pieces of its rows that a stage fetches lie in one line each.
 inline int64_t packed_ld(int64_t cols) { return ceil_div(cols, 64) * 64; }
 
@@ -405,7 +405,7 @@ struct ProductCost {
   int64_t busy, least, ends, share;
 };
 constexpr ProductCost kProduct16[2] = {{4, 800, 800, 12000, 1}, {2, 270, 600, 4000, 2}};
-constexpr ProductCost kProduct32[2] = {{2, 1900, 1900, 4000, 2}, {1, 480, 1000, 2000, 4}};
+constexpr ProductCost kProduct32[2] = {{2, 1900, 1900, 4000, 2}, {1, 480, 700, 2000, 4}};
 constexpr int64_t kJoinNs = 6000;     // the join's launch and, of whole rounds before, the split's
 
 // `items` of `len` contraction indices each
@@ -452,15 +452,21 @@ inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool
   p.nq = ceil_div(Q, tile_edge(p.f));
   const int64_t rest = p.np * p.nq - p.whole;
   if (p.splits == 1) p.whole += rest;
-  auto packed = [](int64_t rows, int64_t deep_len, bool deep) {
+  // fp32 operands are read four elements at a time, from any address, and need as many
+  if (dtype == 2) {
+    pack_a = (a_deep ? R : P) < 4;
+    pack_b = (b_deep ? R : Q) < 4;
+  }
+  const int64_t es = elem_size(dtype);
+  auto packed = [es](int64_t rows, int64_t deep_len, bool deep) {
     const int64_t n = deep ? rows : deep_len, c = deep ? deep_len : rows;
-    return (size_t)(n * packed_ld(c)) * 2;
+    return (size_t)(n * packed_ld(c) * es);
   };
-  if (dtype != 2 && R > 0 && pack_a) {
+  if (R > 0 && pack_a) {
     p.pack_a = true;
     p.ws_bytes += packed(P, R, a_deep);
   }
-  if (dtype != 2 && R > 0 && pack_b) {
+  if (R > 0 && pack_b) {
     p.pack_b = true;
     p.pack_b_at = p.ws_bytes;
     p.ws_bytes += packed(Q, R, b_deep);

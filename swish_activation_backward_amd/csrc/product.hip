@@ -485,28 +485,6 @@ void product16_kernel(Product g, ProductGrid grid, float* part) {
   __builtin_amdgcn_s_waitcnt(vmcnt_le(0));
 }
 
-// rows [n][cols] again with rows of ld elements, zeros up to a multiple of 8; a thread takes 8
-// columns
-template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(const T* src, int64_t lds, T* dst, int64_t ldd,
-                                                   int64_t n, int64_t cols) {
-  const int64_t chunks = (cols + 7) / 8, total = n * chunks;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
-       e += (int64_t)gridDim.x * 256) {
-    const int64_t r = e / chunks, c = (e % chunks) * 8;
-    Chunk<T> v;
-    if (c + 8 <= cols) {
-      v.load(src + r * lds + c);
-    } else {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? to_f32(src[r * lds + c + i]) : 0.0f;
-      v.narrow(f);
-    }
-    *reinterpret_cast<u32x4*>(dst + r * ldd + c) = v.v[0];
-  }
-}
-
 // Whether what the epilogue touches lies in rows of 16-byte multiples with 32-bit window offsets.
 bool rows_whole(const Product& g) {
   const int64_t most = int64_t(1) << 22;
@@ -541,17 +519,6 @@ hipError_t layouts(const Product& g, const ProductPlan& p, const ProductGrid& gr
   return tiles<T, false, false, 2>(g, grid, part, cus, stream);
 }
 
-// An operand again in the workspace with rows of 16-byte multiples
-template <typename T>
-hipError_t pack(Operand& o, int64_t rows, int64_t R, void* to, hipStream_t stream) {
-  const int64_t n = o.deep ? rows : R, cols = o.deep ? R : rows, ld = packed_ld(cols);
-  SWG_LAUNCH((pack_kernel<T>), dim3(stream_grid(n * ceil_div(cols, 8))), dim3(256), 0, stream,
-             static_cast<const T*>(o.p), o.ld, static_cast<T*>(to), ld, n, cols);
-  o.p = to;
-  o.ld = ld;
-  return hipGetLastError();
-}
-
 template <typename T>
 hipError_t product16_t(Product g, const ProductPlan& p, void* ws, int cus, hipStream_t stream) {
   char* w = static_cast<char*>(ws);
@@ -560,11 +527,11 @@ hipError_t product16_t(Product g, const ProductPlan& p, void* ws, int cus, hipSt
     g.a.ld = g.b.ld = 8;
   }
   if (p.pack_a) {
-    const hipError_t e = pack<T>(g.a, g.P, g.R, w + p.pack_a_at, stream);
+    const hipError_t e = pack_operand<T>(g.a, g.P, g.R, w + p.pack_a_at, stream);
     if (e != hipSuccess) return e;
   }
   if (p.pack_b) {
-    const hipError_t e = pack<T>(g.b, g.Q, g.R, w + p.pack_b_at, stream);
+    const hipError_t e = pack_operand<T>(g.b, g.Q, g.R, w + p.pack_b_at, stream);
     if (e != hipSuccess) return e;
   }
   if (p.whole > 0) {

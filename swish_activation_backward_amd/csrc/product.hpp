@@ -157,4 +157,40 @@ inline hipError_t product_join(const Product& g, const ProductPlan& p, const Pro
   return hipGetLastError();
 }
 
+// ---- operands laid out again
+// rows [n][cols] again with rows of ld elements, zeros up to a multiple of 8; a thread takes 8
+// columns
+template <typename T>
+__global__ __launch_bounds__(256) void pack_kernel(const T* src, int64_t lds, T* dst, int64_t ldd,
+                                                   int64_t n, int64_t cols) {
+  const int64_t chunks = (cols + 7) / 8, total = n * chunks;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total;
+       e += (int64_t)gridDim.x * 256) {
+    const int64_t r = e / chunks, c = (e % chunks) * 8;
+    Chunk<T> v;
+    if (c + 8 <= cols) {
+      v.load(src + r * lds + c);
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? to_f32(src[r * lds + c + i]) : 0.0f;
+      v.narrow(f);
+    }
+#pragma unroll
+    for (int i = 0; i < Chunk<T>::NV; ++i)
+      reinterpret_cast<u32x4*>(dst + r * ldd + c)[i] = v.v[i];
+  }
+}
+
+// An operand again in the workspace with rows of 16-byte multiples
+template <typename T>
+inline hipError_t pack_operand(Operand& o, int64_t rows, int64_t R, void* to, hipStream_t stream) {
+  const int64_t n = o.deep ? rows : R, cols = o.deep ? R : rows, ld = packed_ld(cols);
+  SWG_LAUNCH((pack_kernel<T>), dim3(stream_grid(n * ceil_div(cols, 8))), dim3(256), 0, stream,
+             static_cast<const T*>(o.p), o.ld, static_cast<T*>(to), ld, n, cols);
+  o.p = to;
+  o.ld = ld;
+  return hipGetLastError();
+}
+
 }  // namespace swg

@@ -34,44 +34,72 @@ template <bool DEEP, int F> struct Part {
     return DEEP ? (threadIdx.x % 8) * 4 : threadIdx.x / (P / 4) + kThreads / (P / 4) * h;
   }
 
-  // The vectors' places in memory, a stage further with every load.
+  // The vectors' places in memory, a stage further with every load.  Every load is executed, so that
+  // the compiler can count those in flight: a vector that would end past the row's end (deep) or the
+  // last row (flat) starts as much earlier and is shifted; one past the contraction's end is taken
+  // from the operand's first row and dropped.  Rows that do not exist repeat an existing one: their
+  // outputs are dropped.  Both extents are at least 4.
   struct Source {
+    const float* first;
     const float* q[V];
-    int rows[V];      // of the vector's rows, those that exist (deep: 1 or 0)
     int64_t step;
-    int left;         // contraction indices
-    __device__ inline Source(const float* src, int64_t ld, int64_t row0, int64_t rows_, int begin,
-                             int end) {
-      left = end - begin;
-      step = DEEP ? kDepth : kDepth * ld;
+    int r, end, shift;   // contraction index of the stage, its end, shift of a flat vector
+    __device__ inline Source(const float* src, int64_t ld, int64_t row0, int64_t rows, int begin,
+                             int end_) {
+      first = src;
+      r = begin;
+      end = end_;
+      step = kDepth * ld;
 #pragma unroll
       for (int h = 0; h < V; ++h) {
-        const int64_t p = row0 + row(h), r = begin + deep(h);
-        const int64_t n = rows_ - p, most = DEEP ? 1 : 4;
-        rows[h] = (int)(n < 0 ? 0 : n < most ? n : most);
-        q[h] = src + (DEEP ? p * ld + r : r * ld + p);
+        const int64_t p = row0 + row(h);
+        if constexpr (DEEP) {
+          q[h] = src + (p < rows ? p : rows - 1) * ld;
+        } else {
+          const int64_t at = p + 4 <= rows ? p : rows - 4;
+          shift = (int)(p - at);
+          q[h] = src + (int64_t)(begin + deep(h)) * ld + at;
+        }
       }
     }
   };
 
-  // 0 past the rows and the contraction's end, where nothing is read
   __device__ inline void load(Source& s) {
 #pragma unroll
     for (int h = 0; h < V; ++h) {
-      const int along = s.left - deep(h);
-      const int n = DEEP ? (s.rows[h] ? along : 0) : (along > 0 ? s.rows[h] : 0);
-      v[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (n >= 4) {
-        const u32x4_el4 u = *reinterpret_cast<const u32x4_el4*>(s.q[h]);
-        v[h] = __builtin_bit_cast(f32x4, u);
-      } else if (n > 0) {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (e < n) v[h][e] = s.q[h][e];
+      const float* p = s.q[h];
+      if constexpr (DEEP) {
+        const int c = s.r + deep(h);
+        p += c + 4 <= s.end ? c : s.end - 4;
+      } else {
+        p = s.r + deep(h) < s.end ? p : s.first;
+        s.q[h] += s.step;
       }
-      s.q[h] += s.step;
+      const u32x4_el4 u = *reinterpret_cast<const u32x4_el4*>(p);
+      v[h] = __builtin_bit_cast(f32x4, u);
     }
-    s.left -= kDepth;
+    s.r += kDepth;
+  }
+  // v[n ..], zeros behind
+  static __device__ inline f32x4 shifted(f32x4 v, int n) {
+    if (n & 1) v = f32x4{v[1], v[2], v[3], 0.0f};
+    if (n & 2) v = f32x4{v[2], v[3], 0.0f, 0.0f};
+    if (n & ~3) v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    return v;
+  }
+  // of the stage from contraction index r on: what does not exist becomes 0
+  __device__ inline void trim(const Source& s, int r) {
+    const bool tail = r + kDepth > s.end;
+#pragma unroll
+    for (int h = 0; h < V; ++h) {
+      if constexpr (DEEP) {
+        const int c = r + deep(h);
+        if (tail) v[h] = shifted(v[h], c + 4 <= s.end ? 0 : c + 4 - s.end);
+      } else {
+        if (s.shift) v[h] = shifted(v[h], s.shift);
+        if (tail && r + deep(h) >= s.end) v[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    }
   }
   __device__ inline void store(float* lds) const {
 #pragma unroll
@@ -92,7 +120,7 @@ template <bool DEEP, int F> struct Part {
 
 template <bool AD, bool BD, int F>
 __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductGrid grid,
-                                                             float* part) {
+                                                             float* part, int pad_a, int pad_b) {
   typedef Part<AD, F> A;
   typedef Part<BD, F> B;
   constexpr int P = 64 * F, WR = 32 * F, BUF = A::FLOATS + B::FLOATS;
@@ -115,8 +143,13 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
   // two stages in flight: a set of registers is loaded again as soon as it is written to LDS
   A a[2];
   B b[2];
-  typename A::Source sa(pa, g.a.ld, t.p0, g.P, t.begin, t.end);
-  typename B::Source sb(pb, g.b.ld, t.q0, g.Q, t.begin, t.end);
+  // an operand that was laid out again has zeros up to an extent of pad_a (pad_b)
+  auto extent = [](int64_t n, int pad) { return n < pad ? (int64_t)pad : n; };
+  typename A::Source sa(pa, g.a.ld, t.p0, AD ? g.P : extent(g.P, pad_a), t.begin,
+                        AD ? (int)extent(t.end, pad_a) : t.end);
+  typename B::Source sb(pb, g.b.ld, t.q0, BD ? g.Q : extent(g.Q, pad_b), t.begin,
+                        BD ? (int)extent(t.end, pad_b) : t.end);
+  int r = t.begin;   // of the stage being multiplied
   auto load = [&](auto Set) {
     a[decltype(Set)::value].load(sa);
     b[decltype(Set)::value].load(sb);
@@ -125,22 +158,29 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
     constexpr int set = decltype(Set)::value;   // of the next stage, odd or even
     const float* cur = lds + (set ^ 1) * BUF;
     float* other = lds + set * BUF;
+    // all reads ahead of the products: between them each would be waited for
+    f32x4 fa[kDepth / 8][F], fb[kDepth / 8][F];
 #pragma unroll
-    for (int j = 0; j < kDepth / 8; ++j) {
-      f32x4 fa[F], fb[F];
+    for (int j = 0; j < kDepth / 8; ++j)
 #pragma unroll
       for (int i = 0; i < F; ++i) {
-        fa[i] = A::read(cur, wp * WR + 32 * i + col, j, half);
-        fb[i] = B::read(cur + A::FLOATS, wq * WR + 32 * i + col, j, half);
+        fa[j][i] = A::read(cur, wp * WR + 32 * i + col, j, half);
+        fb[j][i] = B::read(cur + A::FLOATS, wq * WR + 32 * i + col, j, half);
       }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kDepth / 8; ++j)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int i = 0; i < F; ++i)
 #pragma unroll
           for (int k = 0; k < F; ++k)
-            acc[i][k] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i][s], fb[k][s], acc[i][k], 0, 0, 0);
-    }
+            acc[i][k] =
+                __builtin_amdgcn_mfma_f32_32x32x2f32(fa[j][i][s], fb[j][k][s], acc[i][k], 0, 0, 0);
+    r += kDepth;
+    a[set].trim(sa, r);
+    b[set].trim(sb, r);
     a[set].store(other);
     b[set].store(other + A::FLOATS);
     load(Set);
@@ -148,15 +188,19 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
   };
   constexpr std::integral_constant<int, 0> kEven{};
   constexpr std::integral_constant<int, 1> kOdd{};
-  load(kEven);
-  load(kOdd);
-  a[0].store(lds);
-  b[0].store(lds + A::FLOATS);
-  load(kEven);
-  __syncthreads();
-  for (int st = 0; st < t.stages; st += 2) {   // an even number of stages
-    step(kOdd);
-    step(kEven);
+  if (g.R > 0) {
+    load(kEven);
+    load(kOdd);
+    a[0].trim(sa, r);
+    b[0].trim(sb, r);
+    a[0].store(lds);
+    b[0].store(lds + A::FLOATS);
+    load(kEven);
+    __syncthreads();
+    for (int st = 0; st < t.stages; st += 2) {   // an even number of stages
+      step(kOdd);
+      step(kEven);
+    }
   }
   // out, 32 x 32 sums of a wave at a time
   float* out = lds + wave * 1024;
@@ -187,30 +231,38 @@ __global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductG
 }
 
 template <int F>
-hipError_t layouts(const Product& g, const ProductGrid& grid, float* part, hipStream_t stream) {
+hipError_t layouts(const Product& g, const ProductPlan& p, const ProductGrid& grid, float* part,
+                   hipStream_t stream) {
   const dim3 blocks(grid.items), block(kThreads);
+  const int a = p.pack_a ? 8 : 0, b = p.pack_b ? 8 : 0;
   if (g.a.deep && !g.b.deep)
-    SWG_LAUNCH((product32_kernel<true, false, F>), blocks, block, 0, stream, g, grid, part);
+    SWG_LAUNCH((product32_kernel<true, false, F>), blocks, block, 0, stream, g, grid, part, a, b);
   else if (g.a.deep)
-    SWG_LAUNCH((product32_kernel<true, true, F>), blocks, block, 0, stream, g, grid, part);
+    SWG_LAUNCH((product32_kernel<true, true, F>), blocks, block, 0, stream, g, grid, part, a, b);
   else
-    SWG_LAUNCH((product32_kernel<false, false, F>), blocks, block, 0, stream, g, grid, part);
+    SWG_LAUNCH((product32_kernel<false, false, F>), blocks, block, 0, stream, g, grid, part, a, b);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_product32(const Product& g, const ProductPlan& p, void* ws, hipStream_t stream) {
+hipError_t launch_product32(Product g, const ProductPlan& p, void* ws, hipStream_t stream) {
+  char* w = static_cast<char*>(ws);
+  hipError_t e = hipSuccess;
+  if (p.pack_a) e = pack_operand<float>(g.a, g.P, g.R, w + p.pack_a_at, stream);
+  if (e == hipSuccess && p.pack_b) e = pack_operand<float>(g.b, g.Q, g.R, w + p.pack_b_at, stream);
+  if (e != hipSuccess) return e;
   auto run = [&](const ProductGrid& grid, float* part) {
-    return p.f == 2 ? layouts<2>(g, grid, part, stream) : layouts<1>(g, grid, part, stream);
+    return p.f == 2 ? layouts<2>(g, p, grid, part, stream)
+                    : layouts<1>(g, p, grid, part, stream);
   };
   if (p.whole > 0) {
-    const hipError_t e = run(product_grid(p, true), nullptr);
+    e = run(product_grid(p, true), nullptr);
     if (e != hipSuccess || p.splits == 1) return e;
   }
   const ProductGrid rest = product_grid(p, false);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_at);
-  const hipError_t e = run(rest, part);
+  float* part = reinterpret_cast<float*>(w + p.part_at);
+  e = run(rest, part);
   if (e != hipSuccess) return e;
   return product_join<float>(g, p, rest, part, stream);
 }
