@@ -634,7 +634,8 @@ def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace
 
 class ResidualNorm(NamedTuple):
     """What ``residual_norm_fwd`` returns: the new residual stream out [M, N], its norm [M, N] (None
-    where ``pre`` is off) and the fp32 statistics [M] of the norms that are on."""
+    where ``pre`` is off) and, where they were asked for, the fp32 statistics [M] of the norms that
+    are on."""
     out: torch.Tensor
     norm: Optional[torch.Tensor]
     rstd_post: Optional[torch.Tensor]
@@ -644,15 +645,14 @@ class ResidualNorm(NamedTuple):
 _GATE_NONE, _GATE_CHANNEL, _GATE_ROW, _GATE_FULL = range(4)
 
 
-def _gate(name, t, dtype, wdtype, shape, device):
-    """Kind and row stride of a gate: [N] (``wdtype``), [M, 1] or [M, N] (``dtype``)."""
+def _gate(name, t, dtype, shape, device):
+    """Kind and row stride of a gate: [N] (checked as the weights are), [M, 1] or [M, N]."""
     if t is None:
         return _GATE_NONE, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     M, N = shape
     if t.dim() == 1:
-        _packed(name, t, wdtype, (N,), device)
         return _GATE_CHANNEL, N
     if t.shape == shape:
         return _GATE_FULL, _rows(name, t, dtype, shape, device)
@@ -667,8 +667,8 @@ def _vectors(gate):
 
 
 def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0, post=True,
-                      pre=True, out=None, norm=None, rstd_post=None, rstd_pre=None, eps=1e-5,
-                      stream=None):
+                      pre=True, out=None, norm=None, stats=False, rstd_post=None, rstd_pre=None,
+                      eps=1e-5, stream=None):
     """The root mean square norm after a block (``post``), its gate, the residual sum and the norm
     before the next block (``pre``) over the rows of y [M, N]:
 
@@ -676,12 +676,13 @@ def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0
 
     ``residual`` [M, N] (None: 0) and ``out`` have y's dtype or fp32, ``w_post`` and ``w_pre`` [N]
     (None: 1) y's dtype or fp32.  ``gate`` is None, [N] (of the weights' type), or [M, 1] or [M, N]
-    (of y's).  ``out`` may be ``residual``; outputs that are not given are allocated.  Returns
-    ``ResidualNorm``."""
+    (of y's).  ``out`` may be ``residual``; outputs that are not given are allocated.  ``stats``
+    asks for the statistics that ``residual_norm_bwd`` takes (``rstd_post`` and ``rstd_pre`` [M],
+    allocated if not given).  Returns ``ResidualNorm``."""
     if stream is not None:
         with _on_stream(stream, y):
             return residual_norm_fwd(y, residual, w_post, w_pre, gate, scale, post, pre, out, norm,
-                                     rstd_post, rstd_pre, eps)
+                                     stats, rstd_post, rstd_pre, eps)
     lib = load_library()
     shape = _matrix("y", y)
     M, N = shape
@@ -689,7 +690,7 @@ def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0
     code = _dtype_code(y)
     ldy = _rows("y", y, dt, shape, dev)
     wdt = _affine(dt, N, dev, w_post=w_post, w_pre=w_pre, gate=_vectors(gate))
-    kind, ldg = _gate("gate", gate, dt, wdt, shape, dev)
+    kind, ldg = _gate("gate", gate, dt, shape, dev)
     rdt, ldr = dt, N
     if residual is not None:
         if not isinstance(residual, torch.Tensor):
@@ -708,10 +709,10 @@ def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0
         if norm is None:
             norm = torch.empty(shape, dtype=dt, device=dev)
         ldn = _rows("norm", norm, dt, shape, dev)
-        rstd_pre = _out("rstd_pre", rstd_pre, torch.float32, (M,), dev)
     else:
-        norm = rstd_pre = None
-    rstd_post = _out("rstd_post", rstd_post, torch.float32, (M,), dev) if post else None
+        norm = None
+    rstd_pre = _out("rstd_pre", rstd_pre, torch.float32, (M,), dev) if stats and pre else None
+    rstd_post = _out("rstd_post", rstd_post, torch.float32, (M,), dev) if stats and post else None
     _call("residual_norm_fwd", lib.residual_norm_fwd, dev, y.data_ptr(), ldy, _addr(residual), ldr,
           _addr(w_post), _addr(w_pre), _addr(gate), ldg, kind, scale, out.data_ptr(), ldo,
           _addr(norm), ldn, _addr(rstd_post), _addr(rstd_pre), int(post), int(pre), M, N, eps, code,
@@ -743,12 +744,12 @@ def residual_norm_bwd(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, rstd_
     ldy = _rows("y", y, dt, shape, dev)
     wdt = _affine(dt, N, dev, w_post=w_post, w_pre=w_pre, dw_post=dw_post, dw_pre=dw_pre,
                   gate=_vectors(gate), dgate=_vectors(dgate))
-    kind, ldg = _gate("gate", gate, dt, wdt, shape, dev)
+    kind, ldg = _gate("gate", gate, dt, shape, dev)
     lddg = 0
     if dgate is not None:
         if gate is None or dgate.shape != gate.shape:
             raise ValueError("dgate must have the gate's shape")
-        lddg = _gate("dgate", dgate, dt, wdt, shape, dev)[1]
+        lddg = _gate("dgate", dgate, dt, shape, dev)[1]
     # the residual stream's type: of the first one given
     rdt, lds = None, []
     for name, t in (("dout", dout), ("out", out if dnorm is not None else None),

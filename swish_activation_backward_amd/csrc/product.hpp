@@ -131,7 +131,18 @@ __global__ __launch_bounds__(256) void product_join_kernel(Product g, ProductGri
     if (p >= g.P || q >= g.Q) continue;
     const float* src = part + (int64_t)tile * P * P + in * 8;
     f32x4 lo = *reinterpret_cast<const f32x4*>(src), hi = *reinterpret_cast<const f32x4*>(src + 4);
-    for (int s = 1; s < splits; ++s) {
+    int s = 1;
+    for (; s + 4 <= splits; s += 4) {   // the loads of four ranges in flight
+      f32x4 v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = *reinterpret_cast<const f32x4*>(src + (s + i) * plane);
+        v[2 * i + 1] = *reinterpret_cast<const f32x4*>(src + (s + i) * plane + 4);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lo += v[2 * i], hi += v[2 * i + 1];
+    }
+    for (; s < splits; ++s) {
       lo += *reinterpret_cast<const f32x4*>(src + s * plane);
       hi += *reinterpret_cast<const f32x4*>(src + s * plane + 4);
     }

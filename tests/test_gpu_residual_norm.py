@@ -55,6 +55,8 @@ def check_fwd(d, r, scale, post=True, pre=True, residual="residual", eps=EPS):
     ro, rn, rs, rp = R.residual_norm_ref(to64(d["y"]), f64(res), f64(d["w_post"]), f64(d["w_pre"]),
                                          f64(d["gate"]), scale, eps, post, pre)
     models = fwd_models(d["y"], res, d["w_post"], d["w_pre"], d["gate"], scale, rs, rp, ro)
+    # what is not asked for is not there
+    assert len(r) == 4
     for name, got, ref, e in zip(("out", "norm", "rstd_post", "rstd_pre"), r, (ro, rn, rs, rp),
                                  models):
         assert (got is None) == (ref is None), name
@@ -99,7 +101,7 @@ def run_both(d, M, N, dt, rdt, wdt, scale, post, pre):
 
     r = swg.residual_norm_fwd(
         d["y"], d["residual"], d["w_post"], d["w_pre"], d["gate"], scale, post, pre,
-        out=new((M, N), rdt), norm=new((M, N), dt) if pre else None,
+        out=new((M, N), rdt), norm=new((M, N), dt) if pre else None, stats=True,
         rstd_post=new((M,), FP32) if post else None, rstd_pre=new((M,), FP32) if pre else None,
         eps=EPS)
     got = grads(d, post, pre, M, N, dt, rdt, wdt, new)
@@ -145,10 +147,10 @@ def test_in_place(N, post, pre):
     M = 37
     d = make(M, N, BF16, BF16, BF16, "channel", seed=3)
     a = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], d["gate"], 0.5, post,
-                              pre, eps=EPS)
+                              pre, stats=True, eps=EPS)
     stream = d["residual"].clone()
     b = swg.residual_norm_fwd(d["y"], stream, d["w_post"], d["w_pre"], d["gate"], 0.5, post, pre,
-                              out=stream, eps=EPS)
+                              out=stream, stats=True, eps=EPS)
     assert b.out is stream
     both = []
     for src, dst in ((d["dout"], torch.empty(M, N, dtype=BF16, device=stream.device)),
@@ -171,7 +173,7 @@ def test_optional_operands(N):
     d = make(M, N, BF16, FP32, FP32, "full", seed=4)
     d["w_post"] = d["w_pre"] = None
     out = torch.empty(M, N, dtype=FP32, device=dev)
-    r = swg.residual_norm_fwd(d["y"], None, gate=d["gate"], scale=2.0, out=out, eps=EPS)
+    r = swg.residual_norm_fwd(d["y"], None, gate=d["gate"], scale=2.0, out=out, stats=True, eps=EPS)
     check_fwd(d, r, 2.0, residual=None)
     for dout, dnorm in (("dout", None), (None, "dnorm"), (None, None)):
         for want in ("dy", "dresidual", "dw_post", "dw_pre", "dgate"):
@@ -191,7 +193,8 @@ def test_optional_operands(N):
 def test_accumulate(M, N):
     d = make(M, N, FP16, FP16, FP32, "channel", seed=5)
     dev = d["y"].device
-    r = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], d["gate"], eps=EPS)
+    r = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], d["gate"],
+                              stats=True, eps=EPS)
     init = {n: torch.randn(N, device=dev) for n in ("dw_post", "dw_pre", "dgate")}
     for accumulate in (False, True):
         got = {n: t.clone() for n, t in init.items()}
@@ -212,7 +215,8 @@ def test_repeats_bit_for_bit():
     d = make(M, N, BF16, FP32, FP32, "channel", seed=6)
     first = None
     for _ in range(3):
-        r = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], d["gate"])
+        r = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], d["gate"],
+                                  stats=True)
         got = grads(d, True, True, M, N, BF16, FP32, FP32,
                     lambda s, t: torch.empty(s, dtype=t, device=r.out.device))
         swg.residual_norm_bwd(d["dout"], d["dnorm"], d["y"], r.out, d["w_post"], d["w_pre"],
@@ -228,13 +232,14 @@ def test_special_rows(N):
     """A row of zeros, one with a NaN and one with an infinity; the others keep their values."""
     M = 6
     d = make(M, N, FP32, FP32, FP32, "none", seed=7)
-    want = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], eps=EPS)
+    want = swg.residual_norm_fwd(d["y"], d["residual"], d["w_post"], d["w_pre"], stats=True,
+                                 eps=EPS)
     y, res = d["y"].clone(), d["residual"].clone()
     y[1] = 0
     res[1] = 0
     y[2, N // 2] = float("nan")
     res[4, 0] = float("inf")
-    r = swg.residual_norm_fwd(y, res, d["w_post"], d["w_pre"], eps=EPS)
+    r = swg.residual_norm_fwd(y, res, d["w_post"], d["w_pre"], stats=True, eps=EPS)
     torch.cuda.synchronize()
     keep = [0, 3, 5]
     for a, b in zip(r, want):

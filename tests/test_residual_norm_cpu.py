@@ -118,7 +118,7 @@ def test_binding_refuses(t):
         dict(residual=t.f(8, 4).t()), dict(w_post=t.f(7, dt=f32)), dict(w_pre=t.f(8)),
         dict(gate=t.f(4)), dict(gate=t.f(4, 2)), dict(gate=t.f(8)), dict(gate=t.f(4, 1, dt=f32)),
         dict(gate=t.f(4, 8, dt=f32)), dict(out=t.f(4, 8)), dict(norm=t.f(4, 8, dt=f32)),
-        dict(rstd_post=t.f(5, dt=f32)), dict(rstd_pre=t.f(4)), dict(residual=torch.empty(4, 8)),
+        dict(stats=True, rstd_post=t.f(5, dt=f32)), dict(stats=True, rstd_pre=t.f(4)), dict(residual=torch.empty(4, 8)),
         dict(gate=torch.empty(4, 8, dtype=torch.bfloat16)),
     ]
     for kw in bad:
