@@ -12,8 +12,10 @@ kernel (the Ascend C custom-backward page, "突破自动微分瓶颈: 基于 Asc
 算子实战", section 4.2, Python-side registration); the weight layout [K, N] is the SwiGLU
 page's.  Leading dimensions of x are flattened into M.
 
-Around the gate, in the same manner: ``layer_norm`` / ``LayerNorm``, ``token_logprobs`` (log
-probability of given tokens and entropy) and ``distill_loss`` (a teacher's top logits).
+Around the gate, in the same manner: ``layer_norm`` / ``LayerNorm``, ``linear`` / ``Linear`` (with
+bias, activation and residual), ``residual_norm`` (the norms around a block with its gate and the
+residual sum), ``token_logprobs`` (log probability of given tokens and entropy) and ``distill_loss``
+(a teacher's top logits).  ``Block`` puts a gated feed-forward together from them.
 """
 from __future__ import annotations
 
@@ -156,6 +158,153 @@ class LayerNorm(torch.nn.Module):
 
     def forward(self, x):
         return layer_norm(x, self.w, self.b, self.eps)
+
+
+class LinearFunction(torch.autograd.Function):
+    """x [M, K], w [K, N] (or the transpose of a [N, K]), b [N] or None, residual [M, N] or None
+    -> y [M, N]."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, residual, act, beta):
+        M, N = x.shape[0], w.shape[1]
+        z = None
+        if act != "none" and any(ctx.needs_input_grad[:3]):
+            z = torch.empty(M, N, dtype=x.dtype, device=x.device)
+        y = _lib.linear_fwd(x, w, b, residual, act, beta, z=z)
+        ctx.save_for_backward(x, w, z)
+        ctx.act, ctx.beta = act, beta
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        dy = _rows_of(dy)
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        (M, K), N, dev = x.shape, w.shape[1], x.device
+        dx = torch.empty(M, K, dtype=x.dtype, device=dev) if need_x else None
+        dw = None
+        if need_w:   # stored as w is
+            rows = N <= 1 or w.stride(1) == 1
+            dw = torch.empty((K, N) if rows else (N, K), dtype=x.dtype, device=dev)
+            dw = dw if rows else dw.t()
+        db = torch.empty(N, dtype=x.dtype, device=dev) if need_b else None
+        if need_x or need_w or need_b:
+            _lib.linear_bwd(dy, x if need_w else None, w if need_x else None, z, dx, dw, db,
+                            ctx.act, ctx.beta)
+        return dx, dw, db, dy if need_r else None, None, None
+
+
+def linear(x, w, b=None, residual=None, act="none", beta=1.0):
+    """act(x w + b) + residual over the last dimension of x (any leading shape), w [K, N] or the
+    transpose of a [N, K], residual [..., N].  ``act``: "none", "relu", "swish" (z sigma(beta z)),
+    "gelu" or "gelu_tanh"."""
+    if residual is not None:
+        residual = _rows_of(residual)
+    y = LinearFunction.apply(_rows_of(x), w, b, residual, act, beta)
+    return y.view(*x.shape[:-1], w.shape[1])
+
+
+class Linear(torch.nn.Module):
+    """Parameters w [in_features, out_features] and b (optional); forward(x, residual) is
+    act(x w + b) + residual."""
+
+    def __init__(self, in_features, out_features, bias=True, act="none", beta=1.0, device=None,
+                 dtype=torch.bfloat16):
+        super().__init__()
+        kw = {"device": device, "dtype": dtype}
+        self.act, self.beta = act, beta
+        self.w = torch.nn.Parameter(torch.empty(in_features, out_features, **kw))
+        if bias:
+            self.b = torch.nn.Parameter(torch.zeros(out_features, **kw))
+        else:
+            self.register_parameter("b", None)
+        bound = 1.0 / math.sqrt(in_features)
+        with torch.no_grad():
+            self.w.uniform_(-bound, bound)
+
+    def forward(self, x, residual=None):
+        return linear(x, self.w, self.b, residual, self.act, self.beta)
+
+
+class ResidualNormFunction(torch.autograd.Function):
+    """y [M, N], residual [M, N] or None, w_post, w_pre [N] or None, gate [N], [M, 1], [M, N] or
+    None -> out [M, N], norm [M, N] (None where ``pre`` is off)."""
+
+    @staticmethod
+    def forward(ctx, y, residual, w_post, w_pre, gate, scale, eps, post, pre):
+        r = _lib.residual_norm_fwd(y, residual, w_post, w_pre, gate, scale, post, pre, eps=eps,
+                                   stats=True)
+        ctx.save_for_backward(y, r.out, w_post, w_pre, gate, r.rstd_post, r.rstd_pre)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return r.out, r.norm
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dnorm):
+        none = (None,) * 4
+        if dout is None and dnorm is None:
+            return (None,) * 5 + none
+        y, out, w_post, w_pre, gate, rstd_post, rstd_pre = ctx.saved_tensors
+        need_y, need_r, need_wp, need_wq, need_g = ctx.needs_input_grad[:5]
+        new = lambda t, like, need: (torch.empty(like.shape, dtype=t.dtype,  # noqa: E731
+                                                 device=t.device) if need else None)
+        dy, dr = new(y, y, need_y), new(out, out, need_r)
+        # a weight of a norm that is off has no part in the result
+        dwp = new(w_post, w_post, True) if need_wp and rstd_post is not None else None
+        dwq = new(w_pre, w_pre, True) if need_wq and rstd_pre is not None else None
+        dg = new(gate, gate, True) if need_g else None
+        _lib.residual_norm_bwd(None if dout is None else _rows_of(dout),
+                               None if dnorm is None else _rows_of(dnorm), y, out, w_post, w_pre,
+                               gate, rstd_post, rstd_pre, dy, dr, dwp, dwq, dg, scale=ctx.scale)
+        return (dy, dr, dwp, dwq, dg) + none
+
+
+def residual_norm(y, residual=None, w_post=None, w_pre=None, gate=None, scale=1.0, eps=1e-5,
+                  post=True, pre=True):
+    """The root mean square norm after a block (``post``), its gate, the residual sum and the norm
+    before the next block (``pre``) over the last dimension of y (any leading shape): returns
+
+        out = residual + scale * gate * rms(y) w_post  and  norm = rms(out) w_pre
+
+    (norm None without ``pre``).  ``gate`` is None, [N], or of y's leading shape with 1 or N
+    elements a row."""
+    if residual is not None:
+        residual = _rows_of(residual)
+    if gate is not None and gate.dim() != 1:
+        gate = gate.reshape(-1, 1) if gate.shape[-1] == 1 else _rows_of(gate)
+    out, norm = ResidualNormFunction.apply(_rows_of(y), residual, w_post, w_pre, gate, scale, eps,
+                                           post, pre)
+    return out.view(y.shape), None if norm is None else norm.view(y.shape)
+
+
+class Block(torch.nn.Module):
+    """A gated feed-forward between two norms: forward(stream, normed) returns the next stream and
+    the norm that the next block takes,
+
+        y = linear(swiglu(normed)),  stream + scale * gate * rms(y) w_post,  rms(that) w_pre
+
+    The norms' weights and the gate (one value a channel) are fp32; ``enter`` norms a stream for
+    the first block."""
+
+    def __init__(self, features, hidden, scale=1.0, eps=1e-5, bias=True, device=None,
+                 dtype=torch.bfloat16):
+        super().__init__()
+        self.scale, self.eps = scale, eps
+        self.swiglu = SwiGLU(features, hidden, bias, device, dtype)
+        self.out = Linear(hidden, features, bias, device=device, dtype=dtype)
+        ones = lambda: torch.nn.Parameter(torch.ones(features, device=device))  # noqa: E731
+        self.w_post, self.w_pre, self.gate = ones(), ones(), ones()
+
+    @staticmethod
+    def enter(stream, w=None, eps=1e-5):
+        """The norm in front of the first block."""
+        return residual_norm(stream, None, None, w, eps=eps, post=False)[1]
+
+    def forward(self, stream, normed):
+        y = self.out(self.swiglu(normed))
+        return residual_norm(y, stream, self.w_post, self.w_pre, self.gate, self.scale, self.eps)
 
 
 class TokenLogprobsFunction(torch.autograd.Function):
