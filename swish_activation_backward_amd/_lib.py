@@ -840,8 +840,8 @@ def linear_fwd(x, w, bias=None, residual=None, act="none", beta=1.0, y=None, z=N
         y = torch.empty((M, N), dtype=dt, device=dev)
     ldy = _rows("y", y, dt, (M, N), dev)
     rows16 = _rows16(x, ldx) and _rows16(w, ldw)
-    ws = _workspace(_workspace_bytes("linear_fwd_workspace_size", M, K, N, nk, code, rows16),
-                    workspace, dev, None)
+    # not remembered: the size goes by the thread's tile setting
+    ws = _workspace(lib.linear_fwd_workspace_size(M, K, N, nk, code, rows16), workspace, dev, None)
     _call("linear_fwd", lib.linear_fwd, dev, x.data_ptr(), ldx, w.data_ptr(), ldw, nk, _addr(bias),
           _addr(residual), ldr, y.data_ptr(), ldy, _addr(z), ldz, M, K, N, kind, beta, code,
           _addr(ws), _size(ws))
@@ -896,8 +896,8 @@ def linear_bwd(dy, x, w, z, dx, dw, db=None, act="none", beta=1.0, accumulate=Fa
         raise ValueError(f"act {act!r} needs z")
     _gpu(dev)
     nk = bool(nk)
-    ws = _workspace(_workspace_bytes("linear_bwd_workspace_size", M, K, N, nk, kind, code, rows16),
-                    workspace, dev, None)
+    ws = _workspace(lib.linear_bwd_workspace_size(M, K, N, nk, kind, code, rows16), workspace, dev,
+                    None)
     _call("linear_bwd", lib.linear_bwd, dev, dy.data_ptr(), lddy, _addr(x), ldx, _addr(w), ldw, nk,
           _addr(z), ldz, _addr(dx), lddx, _addr(dw), lddw, _addr(db), int(accumulate), M, K, N, kind,
           beta, code, _addr(ws), _size(ws))

@@ -56,6 +56,18 @@ def test_both_tiles(gen, tile, edge, M, K, N, nk):
         assert ((got.double() - ref).abs() <= sum_bound(BF16, mag)(ref)).all()
 
 
+def test_tile_setting_between_calls_of_one_shape(gen, tile):
+    """The workspace a call allocates is the one of its tile."""
+    x, w = rnd(gen, 130, 4096), rnd(gen, 4096, 136, scale=1 / 64)
+    ref = x.double() @ w.double()
+    for edge in (0, 128, 256, 128, 0):
+        tile(edge)
+        y = swg.linear_fwd(x, w)
+        torch.cuda.synchronize()
+        bound = sum_bound(BF16, x.double().abs() @ w.double().abs())(ref)
+        assert ((y.double() - ref).abs() <= bound).all(), edge
+
+
 # tiles of 256: 17 x 16 (one whole round and 16 left, split), 33 x 17; fp32: 64-tiles
 @pytest.mark.parametrize("M,K,N,dt", [(4350, 1032, 4096, BF16), (8200, 2056, 4304, FP16),
                                       (2080, 1000, 2052, FP32)])
