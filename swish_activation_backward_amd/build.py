@@ -16,7 +16,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libswiglu_bwd.so")
 SOURCES = ["api.cpp", "elementwise.hip", "strided.hip", "gemm.hip", "gemm32.hip", "norm.hip",
            "residual_norm.hip", "linear.hip", "product.hip", "product32.hip",
-           "vocab.hip"]
+           "product_few.hip", "vocab.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 ops are switched off: the device code is written in plain fp32 and

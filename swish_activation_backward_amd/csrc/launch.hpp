@@ -186,6 +186,7 @@ struct Product {
 };
 hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
                           hipStream_t stream);
+hipError_t launch_product_few(int dtype, const Product& a, hipStream_t stream);
 hipError_t launch_product32(Product a, const ProductPlan& p, void* ws, hipStream_t stream);
 hipError_t launch_product16(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
                             hipStream_t stream);

@@ -16,6 +16,7 @@ namespace swg {
 
 hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
                           hipStream_t stream) {
+  if (p.few) return launch_product_few(dtype, a, stream);
   if (dtype != 2) return launch_product16(dtype, a, p, ws, cus, stream);
   return launch_product32(a, p, ws, stream);
 }

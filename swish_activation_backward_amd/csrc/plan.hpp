@@ -386,6 +386,7 @@ inline ActBwdPlan plan_act_bwd(int64_t M, int64_t N) {
 // item's stages (32 deep) and what it spends before and after them, plus the partial sums' trip
 // through memory and the launches.  force_f: 4 or 2 overrides the tile (16-bit).
 struct ProductPlan {
+  bool few;                // the form for few rows, which takes nothing of the workspace
   int f;
   int64_t np, nq, whole;
   int64_t splits, len;
@@ -418,9 +419,28 @@ inline int64_t product_items_ns(int64_t items, int64_t len, const ProductCost& c
   return ceil_div(items, kGemmSlots * share) * (stages * stage + c.ends);
 }
 
+// Whether few rows go by the form without a split.  It pays while its workgroup of 16 columns has
+// read its rows (30 bytes a ns) before the tiles have all of the weight (4800 bytes a ns, and 7 us
+// of launches), and, 16-bit, while reading the rows again for every 16 columns is cheap: at 4096 x
+// 12288 it takes 20.3 us for one row against 24.2, 24.6 against 24.6 for 8, 29.4 against 25.0 for
+// 16; at 14336 x 1024 17.6 against 13.6 for one.  The fp32 tiles are slower.
+inline bool few_rows(int dtype, int64_t P, int64_t Q, int64_t R, bool a_deep, bool b_deep) {
+  if (P > 16 || !a_deep || !b_deep || R <= 0 || Q <= 0 || R > (1 << 20) || Q > (1 << 25))
+    return false;
+  const int64_t row = R * (dtype == 2 ? 4 : 2);
+  if (16 * row > 210000 + Q * row / 160) return false;
+  return dtype == 2 || Q * R * (16 + P) <= int64_t(1) << 30;
+}
+
 inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool pack_a,
                                 bool a_deep, bool pack_b, bool b_deep, int force_f) {
   ProductPlan p{};
+  p.splits = 1;
+  p.len = 1;
+  if ((dtype == 2 || force_f == 0) && few_rows(dtype, P, Q, R, a_deep, b_deep)) {
+    p.few = true;
+    return p;
+  }
   int64_t best = -1;
   auto consider = [&](const ProductCost& c, int64_t whole, int64_t rest, int64_t s) {
     int64_t t = product_items_ns(whole, R, c) + product_items_ns(rest * s, ceil_div(R, s), c);

@@ -102,6 +102,20 @@ def test_shapes_types_layouts(M, K, N, dt, nk):
              keep=i % 4 != 0)
 
 
+# few rows whose weight has its contraction contiguous (K forward of [N, K], N backward of [K, N]):
+# the ends of a lane's 16 bytes, of a step, of a wave's run and of a turn of all waves
+@pytest.mark.parametrize("nk", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("deep", [1, 7, 8, 9, 31, 33, 64, 127, 128, 129, 2047, 2048, 2049, 4225])
+@pytest.mark.parametrize("M,other", [(1, 16), (2, 1), (15, 17), (16, 250)])
+def test_few_rows(M, other, deep, dt, nk):
+    K, N = (deep, other) if nk else (other, deep)
+    note(f"linear few rows M={M} K={K} N={N} {dt} nk={nk}")
+    i = M + deep
+    run_both(make(M, K, N, dt, nk, pad=deep % 3), M, K, N, dt, nk, ACTS[i % 5], bias=i % 2 == 0,
+             residual=i % 3 != 0)
+
+
 @pytest.mark.parametrize("act,beta", [(a, 1.0) for a in ACTS] + [("swish", 1.702), ("swish", 0.0),
                                                                  ("swish", -2.0)])
 @pytest.mark.parametrize("dt", TYPES)

@@ -171,3 +171,13 @@ def test_oracle_gradients(act, beta):
             v.copy_(base)
             # central differences: an error of the order of the step's square
             assert abs(float((up - down) / 2e-5) - float((step.numpy() * got).sum())) < 1e-7
+
+
+def test_a_token_against_contiguous_columns_needs_no_workspace():
+    bf, f32 = torch.bfloat16, torch.float32
+    for dt in (bf, f32):
+        assert swg.linear_fwd_workspace_size(1, 4096, 4096, dt, True) == 0
+        assert swg.linear_fwd_workspace_size(16, 1001, 77, dt, True) == 0
+    # one row of tiles that would leave most of the chip idle is split, and joined from there
+    assert swg.linear_fwd_workspace_size(1, 16384, 64, bf, True) > 0
+    assert swg.linear_fwd_workspace_size(17, 4096, 4096, bf, True) > 0
