@@ -405,7 +405,7 @@ struct ProductCost {
   int f;
   int64_t busy, least, ends, share;
 };
-constexpr ProductCost kProduct16[2] = {{4, 800, 800, 12000, 1}, {2, 270, 600, 4000, 2}};
+constexpr ProductCost kProduct16[2] = {{4, 800, 800, 12000, 1}, {2, 270, 300, 4000, 2}};
 constexpr ProductCost kProduct32[2] = {{2, 1900, 1900, 4000, 2}, {1, 480, 700, 2000, 4}};
 constexpr int64_t kJoinNs = 6000;     // the join's launch and, of whole rounds before, the split's
 
