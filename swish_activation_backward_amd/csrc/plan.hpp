@@ -499,8 +499,8 @@ inline ProductPlan plan_product(int64_t P, int64_t Q, int64_t R, int dtype, bool
 }
 
 // Workspace of the linear layer's backward pass, from its start: dz (where there is an activation;
-// rows of a multiple of 8 elements), the partial rows of db, then what the products take one after
-// the other.
+// rows of packed_ld), the partial rows of db, then, from a line's start on, what the products take
+// one after the other.
 struct LinearBwdPlan {
   ActBwdPlan act;
   int64_t lddz;
@@ -512,8 +512,8 @@ inline LinearBwdPlan plan_linear_bwd(int64_t M, int64_t N, int act, int dtype) {
   LinearBwdPlan p{};
   p.act = plan_act_bwd(M, N);
   p.lddz = packed_ld(N);
-  p.part_at = act != 0 ? (size_t)(ceil_div(M * p.lddz * elem_size(dtype), 16) * 16) : 0;
-  p.product_at = p.part_at + (size_t)(p.act.parts * p.act.np) * sizeof(float);
+  p.part_at = act != 0 ? (size_t)(M * p.lddz * elem_size(dtype)) : 0;
+  p.product_at = p.part_at + (size_t)(ceil_div(p.act.parts * p.act.np, 32) * 128);
   return p;
 }
 
