@@ -153,10 +153,11 @@ int swiglu_bwd_gemm_tile(int stage, int64_t M, int64_t K, int64_t N, swg_dtype d
 
 /*
  * Tile override, for tuning and tests: edge 256 or 128 makes swiglu_bwd_w, swiglu_bwd_x,
- * swiglu_bwd_wx, their workspace-size queries and swiglu_bwd_gemm_tile, when called
- * afterwards on the calling thread, use that tile edge instead of the planner's choice
- * (bf16 / fp16; the w stage's M splits follow the tile count, so query the workspace size
- * under the same setting); 0 restores the planner.  SWG_ERR_INVALID for other values.
+ * swiglu_bwd_wx, linear_fwd, linear_bwd, their workspace-size queries and
+ * swiglu_bwd_gemm_tile, when called afterwards on the calling thread, use that tile edge
+ * instead of the planner's choice (bf16 / fp16; the splits follow the tile count, so query
+ * the workspace size under the same setting); 0 restores the planner.  SWG_ERR_INVALID for
+ * other values.
  */
 swg_status swg_set_gemm_tile(int edge);
 
@@ -357,10 +358,11 @@ size_t residual_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
  *   SWG_ACT_GELU       z Phi(z), Phi the normal distribution function
  *   SWG_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
  * beta is finite and used by SWG_ACT_SWISH only.  Bias, activation and residual are applied to the
- * fp32 sums.  y may be exactly the residual (same pointer and stride).  K and N below 2^22
- * (SWG_ERR_UNSUPPORTED).  K = 0: z = bias (the empty sums).
+ * fp32 sums.  y may be exactly the residual (same pointer and stride).  K and N below 2^22, M below
+ * 2^31 - 1024 (SWG_ERR_UNSUPPORTED).  K = 0: z = bias (the empty sums).
  * workspace: linear_fwd_workspace_size bytes, 16-byte aligned; rows16 says whether every row of x
- * and of W as stored starts at a multiple of 16 bytes (rows16 = 0 covers both).
+ * and of W as stored starts at a multiple of 16 bytes, with strides below 2^22 (rows16 = 0 covers
+ * both).
  */
 typedef enum {
   SWG_ACT_NONE = 0,

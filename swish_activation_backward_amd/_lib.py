@@ -804,8 +804,8 @@ def _weight(name, t, dtype, shape, device, nk=None):
 
 
 def _rows16(t, ld):
-    """Whether every row starts at a multiple of 16 bytes."""
-    return (t.data_ptr() | ld * t.element_size()) % 16 == 0
+    """Whether every row starts at a multiple of 16 bytes, with a stride that tiles reach."""
+    return ld < 1 << 22 and (t.data_ptr() | ld * t.element_size()) % 16 == 0
 
 
 def linear_fwd_workspace_size(M: int, K: int, N: int, dtype, w_nk=False, rows16=False) -> int:

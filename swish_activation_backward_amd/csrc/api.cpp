@@ -816,13 +816,17 @@ swg_status residual_norm_bwd(const void* dout, int64_t lddo, const void* dnorm, 
 // ------------------------------------------------------------------- linear layer
 namespace {
 
-// Types, sizes, activation and the stride of a weight [K, N] (nk: stored as [N, K]).
+// A contraction over rows is stepped beyond its end, by some hundred, in 32 bits.
+constexpr int64_t kMaxLinearRows = (int64_t(1) << 31) - 1024;
+
+// Types, sizes and activation.
 swg_status linear_checks(int dtype, int act, float beta, int64_t M, int64_t K, int64_t N) {
   if (!dtype_ok(dtype) || act < SWG_ACT_NONE || act > SWG_ACT_GELU_TANH || !is_finite(beta) ||
       !row_dims_ok(M, K) || !row_dims_ok(M, N))
     return SWG_ERR_INVALID;
-  return K < kMaxGemmDim && N < kMaxGemmDim ? SWG_OK : SWG_ERR_UNSUPPORTED;
+  return K < kMaxGemmDim && N < kMaxGemmDim && M < kMaxLinearRows ? SWG_OK : SWG_ERR_UNSUPPORTED;
 }
+// The stride of a weight [K, N] (nk: stored as [N, K])
 bool weight_stride_ok(int64_t K, int64_t N, int64_t ldw, int nk) {
   return nk ? stride_ok(N, K, ldw) : stride_ok(K, N, ldw);
 }

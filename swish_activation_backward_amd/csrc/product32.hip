@@ -18,6 +18,7 @@ namespace swg {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr uint32_t kLaunchTiles = 1u << 22;
 
 // One operand's part of a stage: V 16-byte vectors a thread.
 template <bool DEEP, int F> struct Part {
@@ -257,8 +258,15 @@ hipError_t launch_product32(Product g, const ProductPlan& p, void* ws, hipStream
                     : layouts<1>(g, p, grid, part, stream);
   };
   if (p.whole > 0) {
-    e = run(product_grid(p, true), nullptr);
-    if (e != hipSuccess || p.splits == 1) return e;
+    // a launch has less than 2^32 threads
+    ProductGrid grid = product_grid(p, true);
+    for (const uint32_t all = grid.tiles; grid.first < all; grid.first += kLaunchTiles) {
+      grid.tiles = all - grid.first < kLaunchTiles ? all - grid.first : kLaunchTiles;
+      grid.items = grid.tiles;
+      e = run(grid, nullptr);
+      if (e != hipSuccess) return e;
+    }
+    if (p.splits == 1) return hipSuccess;
   }
   const ProductGrid rest = product_grid(p, false);
   float* part = reinterpret_cast<float*>(w + p.part_at);

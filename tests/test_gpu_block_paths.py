@@ -218,3 +218,43 @@ def test_residual_norm_beyond_32_bit_offsets(gen):
     for a, b in zip(r, small):
         assert torch.equal(a[-64:], b)
     assert torch.equal(dy[-64:], dsmall)
+
+
+def test_linear_rows_far_apart(gen):
+    """Strides that the tiles' windows do not reach: the operands are laid out again."""
+    far = (1 << 22) + 8
+    note(f"linear strides {far}")
+    x = torch.zeros(33, far, dtype=BF16, device="cuda")[:, :64]
+    x.copy_(rnd(gen, 33, 64))
+    w = torch.zeros(64, far, dtype=BF16, device="cuda")[:, :72]
+    w.copy_(rnd(gen, 64, 72, scale=0.1))
+    dy = torch.zeros(33, far, dtype=BF16, device="cuda")[:, :72]
+    dy.copy_(rnd(gen, 33, 72))
+    y, dx = torch.zeros_like(dy), torch.empty(33, 64, dtype=BF16, device="cuda")
+    dw = torch.empty(64, 72, dtype=BF16, device="cuda")
+    swg.linear_fwd(x, w, y=y)
+    swg.linear_bwd(dy, x, w, None, dx, dw)
+    x, w, dy = x.double().cpu(), w.double().cpu(), dy.double().cpu()
+    for got, a, b in ((y, x, w), (dx, dy, w.t()), (dw, x.t(), dy)):
+        ref, mag = a @ b, a.abs() @ b.abs()
+        assert ((got.double().cpu() - ref).abs() <= sum_bound(BF16, mag)(ref)).all()
+
+
+def test_linear_more_tiles_than_a_launch(gen):
+    """fp32 tiles of 2^30 rows are launched in parts."""
+    M = (1 << 30) + 70
+    note(f"linear M={M} K=4 N=4 fp32")
+    w = rnd(gen, 4, 4, dt=FP32)
+    x = torch.empty(M, 4, dtype=FP32, device="cuda")
+    line = rnd(gen, 4099, 4, dt=FP32)
+    for r in range(0, M, 4099 * 4096):
+        part = x[r:r + 4099 * 4096]
+        part.copy_(line.repeat(4096, 1)[:part.shape[0]])
+    y = swg.linear_fwd(x, w)
+    want = swg.linear_fwd(line, w)
+    ref = line.double() @ w.double()
+    mag = line.double().abs() @ w.double().abs()
+    assert ((want.double() - ref).abs() <= sum_bound(FP32, mag)(ref)).all()
+    for r in range(0, M, 4099 * 4096):
+        part = y[r:r + 4099 * 4096]
+        assert torch.equal(part, want.repeat(4096, 1)[:part.shape[0]]), r

@@ -181,3 +181,12 @@ def test_a_token_against_contiguous_columns_needs_no_workspace():
     # one row of tiles that would leave most of the chip idle is split, and joined from there
     assert swg.linear_fwd_workspace_size(1, 16384, 64, bf, True) > 0
     assert swg.linear_fwd_workspace_size(17, 4096, 4096, bf, True) > 0
+
+
+def test_row_limit(lib):
+    most = (1 << 31) - 1024
+    wide = dict(x=addr(0), w=None, y=None, z=None)
+    assert fwd(lib, M=most, **wide) == UNSUPPORTED
+    assert fwd(lib, M=most - 1, **wide) == NULLPTR
+    assert bwd(lib, M=most, dy=None) == UNSUPPORTED
+    assert bwd(lib, M=most - 1, dy=None) == NULLPTR
