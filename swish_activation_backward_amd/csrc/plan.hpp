@@ -419,13 +419,17 @@ inline int64_t product_items_ns(int64_t items, int64_t len, const ProductCost& c
   return ceil_div(items, kGemmSlots * share) * (stages * stage + c.ends);
 }
 
-// Whether few rows go by the form without a split.  It pays while its workgroup of 16 columns has
-// read its rows (30 bytes a ns) before the tiles have all of the weight (4800 bytes a ns, and 7 us
+// Whether few rows go by the form without a split.  Against a flat operand it pays while all waves of
+// a workgroup take one turn, and while the half lines that it reads do not set the time (4096 x
+// 4096: 19.7 us against 12.7; 1024 x 4096: 6.1 against 10.6).  Against a deep one it pays while its
+// workgroup of 16 columns has read its rows (30 bytes a ns) before the tiles have all of the weight (4800 bytes a ns, and 7 us
 // of launches), and, 16-bit, while reading the rows again for every 16 columns is cheap: at 4096 x
 // 12288 it takes 20.3 us for one row against 24.2, 24.6 against 24.6 for 8, 29.4 against 25.0 for
 // 16; at 14336 x 1024 17.6 against 13.6 for one.  The fp32 tiles are slower.
 inline bool few_rows(int dtype, int64_t P, int64_t Q, int64_t R, bool a_deep, bool b_deep) {
-  if (P > 16 || !a_deep || !b_deep || R <= 0 || Q <= 0 || R > (1 << 20) || Q > (1 << 25))
+  if (!a_deep || R <= 0) return false;
+  if (!b_deep) return P <= 4 && Q >= 8 && R <= 2048 && Q * R <= int64_t(1) << 23;
+  if (P > 16 || Q <= 0 || R > (1 << 20) || Q > (1 << 25))
     return false;
   const int64_t row = R * (dtype == 2 ? 4 : 2);
   if (16 * row > 210000 + Q * row / 160) return false;

@@ -1,24 +1,31 @@
-// The linear layer's product for a few rows (a token's, or some users' at once) and a weight whose
-// contraction index is contiguous: C[p, q] = sum over r of A(p, r) B(q, r), both deep, P <= 16.
+// The linear layer's product for a few rows (a token's, or some users' at once):
+//   C[p, q] = sum over r of A(p, r) B(q, r),  A deep
+// with B deep (its contraction index contiguous) and P <= 16, or B flat and P <= 4.
 //
 // Bound by reading B once, and where that takes 10 us and less by the launches and the latencies, so
-// that nothing is split over workgroups and joined: a workgroup takes 16 columns q over the whole
-// contraction.  Its 16 waves take turns at runs of 128 contraction indices (64 of fp32), each lane
-// loading straight into the operands of 16 x 16 matrix instructions (lane l: row l % 16, the 16 bytes
-// of indices at l / 16 of every fourth), and their sums meet in LDS in the waves' order.  A comes
-// from the caches.  Rows at any alignment.
+// that nothing is split over workgroups and joined: a workgroup takes some columns q over the whole
+// contraction, its 16 waves take turns along it, and their sums meet in LDS in the waves' order.  A
+// comes from the caches.  Rows at any alignment.
 //
-// Measured, bf16, one row: 4096 x 4096 6.8 us = 4.9 TB/s (the tiles with their join 12.1), 1024 x
-// 1024 3.2 us (9.1); 16 rows 10.2 (12.9) and 3.8 (9.6).  fp32, one row: 4096 x 14336 48 us = 4.9
-// TB/s (78).  4 waves to a workgroup: 4096 x 4096 8.3 us; 32 columns to one, which halves the reads
-// of A: 10.2 us, and from 8192 columns on 18 against 20 us at 16 rows and 15 against 14 at one.
+// Deep: 16 columns; a wave takes runs of 128 contraction indices (64 of fp32), each lane loading
+// straight into the operands of 16 x 16 matrix instructions (lane l: row l % 16, the 16 bytes of
+// indices at l / 16 of every fourth).  Measured on the GPU, bf16, one row: 4096 x 4096 6.8 us = 4.9
+// TB/s (the tiles with their join 12.1), 1024 x 1024 3.2 us (9.1); 16 rows 10.2 (12.9) and 3.8 (9.6).
+// fp32, one row: 4096 x 14336 48 us = 4.9 TB/s (78).  4 waves to a workgroup: 4096 x 4096 8.3 us; 32
+// columns to one, which halves the reads of A: 10.2 us, and from 8192 columns on 18 against 20 us at
+// 16 rows and 15 against 14 at one.
+//
+// Flat: 32 columns (16 of fp32), whose rows are half a cache line each: long contractions lose by
+// that (4096 x 4096 19.7 us, the tiles 12.7), short ones have no time for a second launch: 1024 x
+// 1024 4.4 us (9.6), 1001 x 1003 5.7 (15.9, which lay the weight out again), 1024 x 4096 6.1 (10.6).
+// 64 columns: 5.9, 8.4 and 5.9 us; 16: 4.4, 4.8 and 7.0.
 #include "product.hpp"
 
 namespace swg {
 
 namespace {
 
-constexpr int kFewWaves = 16;
+constexpr int kFewWaves = 16, kFlatChunks = 4;
 
 template <typename T> struct Few;
 template <> struct Few<bf16> {
@@ -103,12 +110,116 @@ template <typename T> hipError_t few_t(const Product& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ---- rows of B contiguous
+// x[0 .. 8) of a row from index r on, 0 past its end
+template <typename T> __device__ inline void row_of_8(const T* row, int64_t r, int64_t R, float* f) {
+  if (r + 8 <= R) {
+    Chunk<T> c;
+    c.load(row + r);
+    c.widen(f);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = r + i < R ? to_f32(row[r + i]) : 0.0f;
+}
+
+// At most 4 rows of A, whose products do not fill a matrix instruction: a lane multiplies 16 bytes
+// of 8 rows of B, 16 lanes side by side in the contraction (so that their sums add within the
+// registers) times 4 in the columns; the 16 waves take turns at runs of 128 rows.
+template <typename T, int P>
+__global__ __launch_bounds__(64 * kFewWaves) void few_flat_kernel(Product g) {
+  constexpr int V = Few<T>::VEC, G = 64 / kFlatChunks, RUN = 8 * G, COLS = kFlatChunks * V;
+  typedef typename ElVec<T>::type vec;
+  __shared__ float red[kFewWaves][P][COLS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = lane % G, chunk = lane / G;
+  const int64_t q0 = (int64_t)blockIdx.x * COLS, q = q0 + chunk * V;
+  // the last chunk of a row is moved back to its end
+  const int64_t at = q + V <= g.Q ? q : g.Q - V;
+  const T* b = static_cast<const T*>(g.b.p) + at;
+  const T* a[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    a[p] = static_cast<const T*>(g.a.p) + (p < g.P ? p : g.P - 1) * g.a.ld;
+  float acc[P][V];
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[p][i] = 0.0f;
+  auto add = [&](const u32x4 (&w)[8], int64_t r) {
+    float x[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) row_of_8(a[p], r, g.R, x[p]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float f[V];
+      Vec16<T>::widen(w[k], f);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[p][i] = __builtin_fmaf(x[p][k], f[i], acc[p][i]);
+    }
+  };
+  const int64_t whole = g.R / RUN * RUN;
+  int64_t r = wave * RUN;
+  for (; r < whole; r += kFewWaves * RUN) {
+    u32x4 w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w[k] = __builtin_nontemporal_load(
+          reinterpret_cast<const vec*>(b + (r + grp * 8 + k) * g.b.ld));
+    add(w, r + grp * 8);
+  }
+  if (r == whole && whole < g.R) {
+    u32x4 w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      w[k] = u32x4{0, 0, 0, 0};
+      const int64_t row = r + grp * 8 + k;
+      if (row < g.R) w[k] = *reinterpret_cast<const vec*>(b + row * g.b.ld);
+    }
+    add(w, r + grp * 8);
+  }
+  // the row groups' sums, then the waves'
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float v = lanes_sum<G>(acc[p][i]);
+      if (grp == 0) red[wave][p][chunk * V + i] = v;
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < P * COLS; e += 64 * kFewWaves) {
+    const int p = e / COLS, c = e % COLS;
+    if (p >= g.P || q0 + c >= g.Q) continue;
+    // the place of column q0 + c: its chunk may have been moved
+    const int64_t first = q0 + c / V * V;
+    const int back = first + V <= g.Q ? 0 : (int)(first + V - g.Q);
+    float v = red[0][p][c + back];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += red[w][p][c + back];
+    finish<1, T>(g, p, q0 + c, &v);
+  }
+}
+
+template <typename T> hipError_t flat_t(const Product& g, hipStream_t stream) {
+  const dim3 grid((unsigned)ceil_div(g.Q, kFlatChunks * Few<T>::VEC)), block(64 * kFewWaves);
+  if (g.P == 1) SWG_LAUNCH((few_flat_kernel<T, 1>), grid, block, 0, stream, g);
+  else if (g.P == 2) SWG_LAUNCH((few_flat_kernel<T, 2>), grid, block, 0, stream, g);
+  else SWG_LAUNCH((few_flat_kernel<T, 4>), grid, block, 0, stream, g);
+  return hipGetLastError();
+}
+
+template <typename T> hipError_t either(const Product& g, hipStream_t stream) {
+  return g.b.deep ? few_t<T>(g, stream) : flat_t<T>(g, stream);
+}
+
 }  // namespace
 
 hipError_t launch_product_few(int dtype, const Product& g, hipStream_t stream) {
-  if (dtype == 0) return few_t<bf16>(g, stream);
-  if (dtype == 1) return few_t<fp16>(g, stream);
-  return few_t<float>(g, stream);
+  if (dtype == 0) return either<bf16>(g, stream);
+  if (dtype == 1) return either<fp16>(g, stream);
+  return either<float>(g, stream);
 }
 
 }  // namespace swg

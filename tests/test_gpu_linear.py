@@ -116,6 +116,20 @@ def test_few_rows(M, other, deep, dt, nk):
              residual=i % 3 != 0)
 
 
+# up to 4 rows against a weight in rows: the ends of a lane's 8 rows, of a wave's run and of a turn,
+# and of the columns' chunks
+@pytest.mark.parametrize("nk", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("flat", [1, 7, 8, 9, 127, 128, 129, 1921, 2047, 2048, 2049])
+@pytest.mark.parametrize("M,other", [(1, 8), (2, 9), (3, 33), (4, 250)])
+def test_few_rows_against_rows(M, other, flat, dt, nk):
+    K, N = (other, flat) if nk else (flat, other)
+    note(f"linear few rows against rows M={M} K={K} N={N} {dt} nk={nk}")
+    i = M + flat
+    run_both(make(M, K, N, dt, nk, pad=flat % 3), M, K, N, dt, nk, ACTS[i % 5], bias=i % 2 == 0,
+             residual=i % 3 != 0)
+
+
 @pytest.mark.parametrize("act,beta", [(a, 1.0) for a in ACTS] + [("swish", 1.702), ("swish", 0.0),
                                                                  ("swish", -2.0)])
 @pytest.mark.parametrize("dt", TYPES)
