@@ -24,7 +24,9 @@ hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, voi
 // ------------------------------------------------------------------ dz and db
 // dz = dy act'(z) rounded to T, the operand of both products; db sums its fp32 values: one partial
 // row per block of rows, then those in order.  A workgroup takes 512 columns, 8 a thread (or the up
-// to 7 at the end), 4 rows at once, and a thread has the loads of 4 of its rows in flight.
+// to 7 at the end), 4 rows at once, and a thread has the loads of 4 of its rows in flight.  A pass of
+// its own, since both products read dz, one of them across the rows.  Bound by memory: [16384,
+// 14336] bf16 280 us = 5.0 TB/s, the sums' second kernel 5 us.
 constexpr int kActTx = 64, kActTy = 4, kActFlight = 4;
 
 template <typename T>

@@ -8,6 +8,10 @@
 // and written to the other of two LDS buffers: a deep operand as [row][32], of which a lane reads
 // four consecutive indices at once, a flat one as [32][row].  Lane half h takes index 8 j + 4 h + s
 // in step s of a group j, of both operands alike.
+//
+// Bound by the matrix cores and, with flat operands, by their four single LDS reads for one of a
+// deep one: 4096 x 4096 x 4096 127 TF with both deep, 113 with one flat, 97 with both.  [1021, 1023]
+// x 2047 backward: dx 47 us and its join 5, dW 61.
 #include <type_traits>
 
 #include "mma.hpp"

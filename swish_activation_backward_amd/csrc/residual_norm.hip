@@ -16,6 +16,12 @@
 // y, norm and a gate of the rows are of type T (bf16, fp16, fp32), residual and out of type R (T
 // or fp32), wp, wq and a gate of the columns of T or fp32.  All arithmetic, sums and statistics are
 // fp32; each output is rounded once (norm is formed from out before its rounding).
+//
+// Bound by memory: every input is read and every output written once.  Forward [220000, 512] bf16
+// with a gate of the columns 165 us = 5.4 TB/s, one row of 4096 4.5 us (the loads of a row and two
+// sums one after the other).  Backward, with the join of the column sums: [220000, 512] bf16 with a
+// gate an element 317 us = 5.7 TB/s, [16384, 4096] bf16 under an fp32 stream 231 us = 5.2 TB/s,
+// [8191, 1023] fp32 with a gate a row 48 us = 4.2 TB/s.
 #include "launch.hpp"
 #include "rows.hpp"
 
