@@ -5,13 +5,14 @@
 //
 // A workgroup of four waves (2 x 2) owns a tile of edge 64 F, each wave 32 F x 32 F outputs.  A
 // stage of 32 contraction indices is loaded into registers while the two before it are multiplied,
-// and written to the other of two LDS buffers: a deep operand as [row][32], of which a lane reads
-// four consecutive indices at once, a flat one as [32][row].  Lane half h takes index 8 j + 4 h + s
-// in step s of a group j, of both operands alike.
+// and written to the other of two LDS buffers as [row][32], of which a lane reads four consecutive
+// indices at once; a flat operand is transposed on the way, 4 rows by 4 (2) indices a thread.  Lane
+// half h takes index 8 j + 4 h + s in step s of a group j, of both operands alike.  Registers are
+// held to two workgroups a CU (F = 2) or four.
 //
-// Bound by the matrix cores and, with flat operands, by their four single LDS reads for one of a
-// deep one: 4096 x 4096 x 4096 127 TF with both deep, 113 with one flat, 97 with both.  [1021, 1023]
-// x 2047 backward: dx 47 us and its join 5, dW 61.
+// Bound by the matrix cores and the loads' and stores' instructions beside them: 4096 x 4096 x 4096
+// 133 TF with both deep, 118 with one flat, 112 with both (97 with flat operands read from [32][row]
+// and one workgroup a CU).  [1021, 1023] x 2047 backward: dx 47 us and its join 5, dW 53 to 61.
 #include <type_traits>
 
 #include "mma.hpp"
@@ -27,8 +28,7 @@ constexpr uint32_t kLaunchTiles = 1u << 22;
 // One operand's part of a stage: V 16-byte vectors a thread.
 template <bool DEEP, int F> struct Part {
   static constexpr int P = 64 * F, V = P * kDepth / 4 / kThreads;
-  static constexpr int PITCH = DEEP ? kDepth + 4 : P + 4;
-  static constexpr int FLOATS = DEEP ? P * PITCH : kDepth * PITCH;
+  static constexpr int PITCH = kDepth + 4, FLOATS = P * PITCH;
   f32x4 v[V];
 
   // row and contraction index of vector h
@@ -36,7 +36,7 @@ template <bool DEEP, int F> struct Part {
     return DEEP ? threadIdx.x / 8 + 32 * h : (threadIdx.x % (P / 4)) * 4;
   }
   static __device__ inline int deep(int h) {
-    return DEEP ? (threadIdx.x % 8) * 4 : threadIdx.x / (P / 4) + kThreads / (P / 4) * h;
+    return DEEP ? (threadIdx.x % 8) * 4 : threadIdx.x / (P / 4) * V + h;
   }
 
   // The vectors' places in memory, a stage further with every load.  Every load is executed, so that
@@ -106,25 +106,35 @@ template <bool DEEP, int F> struct Part {
       }
     }
   }
+  // the place of group c of four contraction indices of a row; a flat operand's groups change places
+  // with the row, since its lanes write rows four apart
+  static __device__ inline int place(int row, int c) {
+    return row * PITCH + 4 * (DEEP ? c : c ^ ((row >> 2) & 7));
+  }
   __device__ inline void store(float* lds) const {
+    if constexpr (DEEP) {
 #pragma unroll
-    for (int h = 0; h < V; ++h)
-      *reinterpret_cast<f32x4*>(lds + (DEEP ? row(h) * PITCH + deep(h)
-                                            : deep(h) * PITCH + row(h))) = v[h];
+      for (int h = 0; h < V; ++h)
+        *reinterpret_cast<f32x4*>(lds + place(row(h), deep(h) / 4)) = v[h];
+    } else {   // V indices of each of four rows
+      typedef float vec __attribute__((ext_vector_type(V)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        vec t;
+#pragma unroll
+        for (int h = 0; h < V; ++h) t[h] = v[h][e];
+        *reinterpret_cast<vec*>(lds + place(row(0) + e, deep(0) / 4) + deep(0) % 4) = t;
+      }
+    }
   }
   // the four steps' values of group j, of the row `at`
   static __device__ inline f32x4 read(const float* lds, int at, int j, int half) {
-    const int r = 8 * j + 4 * half;
-    if constexpr (DEEP) return *reinterpret_cast<const f32x4*>(lds + at * PITCH + r);
-    f32x4 f;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) f[s] = lds[(r + s) * PITCH + at];
-    return f;
+    return *reinterpret_cast<const f32x4*>(lds + place(at, 2 * j + half));
   }
 };
 
 template <bool AD, bool BD, int F>
-__global__ __launch_bounds__(kThreads) void product32_kernel(Product g, ProductGrid grid,
+__global__ __launch_bounds__(kThreads, F == 2 ? 2 : 4) void product32_kernel(Product g, ProductGrid grid,
                                                              float* part, int pad_a, int pad_b) {
   typedef Part<AD, F> A;
   typedef Part<BD, F> B;
