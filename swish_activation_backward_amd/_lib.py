@@ -634,8 +634,8 @@ def layer_norm_bwd(dy, x, w, mean, rstd, dx, dw, db, accumulate=False, workspace
 
 class ResidualNorm(NamedTuple):
     """What ``residual_norm_fwd`` returns: the new residual stream out [M, N], its norm [M, N] (None
-    where ``pre`` is off) and, where they were asked for, the fp32 statistics [M] of the norms that
-    are on."""
+    where ``pre`` is off) and, where they were asked for or a buffer was given, the fp32 statistics
+    [M] of the norms that are on."""
     out: torch.Tensor
     norm: Optional[torch.Tensor]
     rstd_post: Optional[torch.Tensor]
@@ -676,9 +676,10 @@ def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0
 
     ``residual`` [M, N] (None: 0) and ``out`` have y's dtype or fp32, ``w_post`` and ``w_pre`` [N]
     (None: 1) y's dtype or fp32.  ``gate`` is None, [N] (of the weights' type), or [M, 1] or [M, N]
-    (of y's).  ``out`` may be ``residual``; outputs that are not given are allocated.  ``stats``
-    asks for the statistics that ``residual_norm_bwd`` takes (``rstd_post`` and ``rstd_pre`` [M],
-    allocated if not given).  Returns ``ResidualNorm``."""
+    (of y's).  ``out`` may be ``residual``; outputs that are not given are allocated.  The
+    statistics that ``residual_norm_bwd`` takes, ``rstd_post`` and ``rstd_pre`` [M], are written
+    where they are given; ``stats`` asks for both (allocated if not given).  What is given for a
+    norm that is off is not touched.  Returns ``ResidualNorm``."""
     if stream is not None:
         with _on_stream(stream, y):
             return residual_norm_fwd(y, residual, w_post, w_pre, gate, scale, post, pre, out, norm,
@@ -711,8 +712,11 @@ def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0
         ldn = _rows("norm", norm, dt, shape, dev)
     else:
         norm = None
-    rstd_pre = _out("rstd_pre", rstd_pre, torch.float32, (M,), dev) if stats and pre else None
-    rstd_post = _out("rstd_post", rstd_post, torch.float32, (M,), dev) if stats and post else None
+    f32 = torch.float32
+    rstd_pre = (_out("rstd_pre", rstd_pre, f32, (M,), dev)
+                if pre and (stats or rstd_pre is not None) else None)
+    rstd_post = (_out("rstd_post", rstd_post, f32, (M,), dev)
+                 if post and (stats or rstd_post is not None) else None)
     _call("residual_norm_fwd", lib.residual_norm_fwd, dev, y.data_ptr(), ldy, _addr(residual), ldr,
           _addr(w_post), _addr(w_pre), _addr(gate), ldg, kind, scale, out.data_ptr(), ldo,
           _addr(norm), ldn, _addr(rstd_post), _addr(rstd_pre), int(post), int(pre), M, N, eps, code,
