@@ -834,6 +834,12 @@ bool weight_stride_ok(int64_t K, int64_t N, int64_t ldw, int nk) {
 bool rows16_ok(const void* p, int64_t ld, int64_t es) {
   return aligned(p, 16) && ld * es % 16 == 0 && ld < kMaxGemmDim;
 }
+// The stride of a matrix's rows; that of a single row, which the caller may leave at anything, is
+// its length (the tiles' windows are as long as their rows' strides).
+int64_t stride_of(int64_t rows, int64_t cols, int64_t ld) { return rows > 1 ? ld : cols; }
+int64_t weight_stride(int64_t K, int64_t N, int64_t ldw, int nk) {
+  return nk ? stride_of(N, K, ldw) : stride_of(K, N, ldw);
+}
 // Rows of x and W that are no multiple of 8 long end inside a 16-byte vector.  dz as the call
 // itself lays it out is never loose; dy in its place may be.
 ProductPlan plan_linear_fwd(int64_t M, int64_t K, int64_t N, bool nk, int dtype, bool x, bool w) {
@@ -873,6 +879,11 @@ swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     return SWG_ERR_INVALID;
   if (M == 0 || N == 0) return SWG_OK;
   if (!y || (K > 0 && (!x || !w))) return SWG_ERR_NULLPTR;
+  ldx = stride_of(M, K, ldx);
+  ldw = weight_stride(K, N, ldw, w_nk);
+  ldr = stride_of(M, N, ldr);
+  ldy = stride_of(M, N, ldy);
+  ldz = stride_of(M, N, ldz);
   const int64_t es = elem_size(dtype);
   for (const void* p : {x, w, bias, residual, (const void*)y, (const void*)z})
     if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
@@ -884,7 +895,7 @@ swg_status linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, in
   st = workspace_check(workspace, workspace_bytes, need);
   if (st != SWG_OK) return st;
   // y may be exactly the residual
-  const bool in_place = y == residual && (ldy == ldr || M == 1);
+  const bool in_place = y == residual && ldy == ldr;
   const Span outs[] = {{y, rows_bytes(M, N, ldy, es)}, {z, z ? rows_bytes(M, N, ldz, es) : 0},
                        {workspace, (int64_t)need}};
   const Span ins[] = {{x, rows_bytes(M, K, ldx, es)}, weight_span(w, K, N, ldw, w_nk, es),
@@ -934,6 +945,12 @@ swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   const bool sums = M > 0 && N > 0;
   if (sums && (!dy || (act != SWG_ACT_NONE && !z) || (dw && !x) || (dx && !w)))
     return SWG_ERR_NULLPTR;
+  lddy = stride_of(M, N, lddy);
+  ldx = stride_of(M, K, ldx);
+  ldw = weight_stride(K, N, ldw, w_nk);
+  ldz = stride_of(M, N, ldz);
+  lddx = stride_of(M, K, lddx);
+  lddw = weight_stride(K, N, lddw, w_nk);
   const int64_t es = elem_size(dtype);
   for (const void* p : {dy, x, w, z, (const void*)dx, (const void*)dw, (const void*)db})
     if (!aligned(p, (size_t)es)) return SWG_ERR_INVALID;
