@@ -960,7 +960,7 @@ swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   // what the call takes of the workspace
   const bool nk = w_nk != 0;
   const LinearBwdPlan plan = plan_linear_bwd(M, N, act, dtype);
-  const bool own_dz = act != SWG_ACT_NONE && (dx || dw);
+  const bool own_dz = sums && act != SWG_ACT_NONE && (dx || dw);
   const bool loose_dz = !own_dz && (!rows16_ok(dy, lddy, es) || N % 8 != 0);
   ProductPlan plan_dx{}, plan_dw{};
   if (dx) plan_dx = plan_linear_dx(M, K, N, nk, dtype, loose_dz, !rows16_ok(w, ldw, es));
