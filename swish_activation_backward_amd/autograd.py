@@ -106,7 +106,7 @@ class SwiGLU(torch.nn.Module):
 
 def _rows_of(x):
     """x [..., N] as a matrix of contiguous rows (a view where its layout allows)."""
-    x2 = x.reshape(-1, x.shape[-1])
+    x2 = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
     R, C = x2.shape
     if (C > 1 and x2.stride(1) != 1) or (R > 1 and x2.stride(0) < C):
         x2 = x2.contiguous()
