@@ -381,7 +381,8 @@ size_t linear_fwd_workspace_size(int64_t M, int64_t K, int64_t N, int w_nk, swg_
 
 /*
  * Its gradients:
- *   dz = dy act'(z)  (rounded to dtype: the operand of the two products; relu's slope at 0 is 0)
+ *   dz = dy act'(z)  (rounded to dtype: the operand of the two products; relu's slope at 0 is 0,
+ *   and a z of +-infinity, as a sum beyond dtype is kept, has the slope of large z)
  *   dx = dz W^T,  dw = x^T dz,  db = sum_m dz  (of the fp32 values of dz)
  * dx [M, K], dw (stored as W is, row stride lddw) and db [N] may be NULL (not wanted); z is needed
  * for an activation, x for dw and W for dx.  The gradient of the residual is dy.  accumulate = 0:

@@ -62,18 +62,30 @@ __device__ inline void activate8(int act, float beta, float* v) {
 #undef SWG_EACH
 }
 
+// v held within most on either side, in one instruction; a NaN, which is not kept, comes out of the
+// other term of the slopes below
+__device__ inline float held(float v, float most) {
+  return __builtin_amdgcn_fmed3f(v, -most, most);
+}
+
+// A z of +-infinity, as a 16-bit z beyond its type is kept, has the slope of large z: what vanishes
+// there multiplies an argument that is held where it is 0 in fp32 anyway.
 __device__ inline float activation_slope(int act, float beta, float z) {
   switch (act) {
     case kActRelu: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
-    case kActSwish: return swish_factor(beta * z);
+    case kActSwish: {
+      const float t = beta * z;
+      const SigmoidParts p = sigmoid_parts(t);         // sigma (1 - sigma) is 0 from |t| = 104 on
+      return __builtin_fmaf(held(t, 128.0f), p.s1ms, p.s);
+    }
+    case kActHalf: return z != z ? z : 0.5f;
     case kActGelu: {
-      float e;
+      float e;                                         // 0 from |z| = 14.5 on
       const float cdf = normal_cdf(z, &e);
-      return __builtin_fmaf(z, kInvSqrt2Pi * e, cdf);
+      return __builtin_fmaf(held(z, 16.0f), kInvSqrt2Pi * e, cdf);
     }
     case kActGeluTanh: {
-      // sigma (1 - sigma) is 0 in fp32 from |z| = 12 on: the powers of z stay finite
-      const float c = __builtin_fminf(__builtin_fmaxf(z, -16.0f), 16.0f);
+      const float c = held(z, 16.0f);                  // sigma (1 - sigma) is 0 from |z| = 12 on
       const SigmoidParts p = sigmoid_parts(z * __builtin_fmaf(kTanh3 * z, z, kTanh1));
       return __builtin_fmaf(c * __builtin_fmaf(3.0f * kTanh3 * c, c, kTanh1), p.s1ms, p.s);
     }

@@ -984,7 +984,8 @@ swg_status linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, 
   Operand dz = {dy, lddy, true};
   if (own_dz || db) {
     ActBwdArgs a{};
-    a.dy = dy; a.lddy = lddy; a.z = z; a.ldz = ldz; a.db = db; a.M = M; a.N = N; a.act = act;
+    a.dy = dy; a.lddy = lddy; a.z = z; a.ldz = ldz; a.db = db; a.M = M; a.N = N;
+    a.act = act == SWG_ACT_SWISH && beta == 0.0f ? (int)kActHalf : (int)act;
     a.beta = beta; a.accumulate = accumulate != 0;
     if (own_dz) {
       a.dz = ws;

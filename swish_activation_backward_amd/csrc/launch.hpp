@@ -164,7 +164,10 @@ hipError_t launch_residual_norm_bwd(int dtype, int rdtype, const ResidualNormArg
 // Linear layer.  One of its products: out[p, q] = sum over r < R of A(p, r) B(q, r), with the
 // epilogue v = sum + bias[q], z = v, out = act(v) + residual (or added to out).  Pointers that a
 // call does not use are null.
-enum ActKind { kActNone = 0, kActRelu = 1, kActSwish = 2, kActGelu = 3, kActGeluTanh = 4 };
+// kActHalf is swish of beta = 0, z / 2, in the backward pass (beta z of an infinite z is no number).
+enum ActKind {
+  kActNone = 0, kActRelu = 1, kActSwish = 2, kActGelu = 3, kActGeluTanh = 4, kActHalf = 5
+};
 struct Operand {
   const void* p;
   int64_t ld;
