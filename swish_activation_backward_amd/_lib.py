@@ -567,7 +567,7 @@ def _affine(dtype, N, device, **named):
         if t is None:
             continue
         if wdtype is None:
-            wdtype = t.dtype
+            wdtype = getattr(t, "dtype", None)      # _packed refuses what is no tensor
         _packed(name, t, wdtype, (N,), device)
     wdtype = dtype if wdtype is None else wdtype
     if wdtype not in DTYPE_CODE:
@@ -699,7 +699,7 @@ def residual_norm_fwd(y, residual, w_post=None, w_pre=None, gate=None, scale=1.0
         rdt = residual.dtype
         ldr = _rows("residual", residual, rdt, shape, dev)
     elif out is not None:
-        rdt = out.dtype
+        rdt = getattr(out, "dtype", dt)             # _rows refuses what is no tensor
     _gpu(dev)
     if out is None:
         out = torch.empty(shape, dtype=rdt, device=dev)
@@ -751,6 +751,8 @@ def residual_norm_bwd(dout, dnorm, y, out, w_post, w_pre, gate, rstd_post, rstd_
     kind, ldg = _gate("gate", gate, dt, shape, dev)
     lddg = 0
     if dgate is not None:
+        if not isinstance(dgate, torch.Tensor):
+            raise TypeError("dgate must be a torch.Tensor")
         if gate is None or dgate.shape != gate.shape:
             raise ValueError("dgate must have the gate's shape")
         lddg = _gate("dgate", dgate, dt, shape, dev)[1]
