@@ -14,7 +14,9 @@ constexpr float kTanh3 = 0.07135481627159929f;
 // Phi(z), the normal distribution function, and e = exp(-z^2 / 2).  The tail beyond |z| is
 // e t p(t) for t = 1 / (1 + 0.3 x), x = |z| / sqrt(2), where t p(t) is half the scaled complementary
 // error function exp(x^2) erfc(x): p of degree 8 by weighted least squares on 0 <= x <= 14, 4e-8
-// off relatively, and 2.5e-7 in all with the roundings of its evaluation.
+// off relatively.  With the roundings of its evaluation Phi is within 3e-7 (measured 2.7e-7, next to
+// 0).  Relative to itself the tail loses with z^2, as the exponent is rounded twice: within
+// (32 + 1.25 z^2) 2^-24 (measured 5.6e-7 from -2 to 0, 9.4e-7 to -4, 3.2e-6 to -8, 7.7e-6 to -12.5).
 __device__ inline float normal_cdf(float z, float* e) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.21213204f, __builtin_fabsf(z), 1.0f));
   float p = -0.06330819f;
