@@ -49,13 +49,14 @@ __device__ inline uint32_t clamp_bytes(int64_t rows, int64_t row_bytes) {
 // the window reading zeros.  Issued as inline asm: the loads' completion is tracked by
 // the explicit vmcnt waits of the pipeline (the compiler's own tracking of LDS-DMA stores
 // would add conservative waits that drain the ring).  The constant OFS is added to M0
-// inside the asm so one scalar base serves all loads of a stage.
+// inside the asm so one scalar base serves all loads of a stage; a load to LDS needs one wait
+// state behind the scalar unit's write of M0, which the compiler does not see to inside asm.
 template <int OFS>
 __device__ inline void dma16s(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
                               const uint16_t* dst) {
   const uint32_t lds = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(LDS_AS const void*)dst);
-  asm volatile("s_add_u32 m0, %2, %3\n\tbuffer_load_dwordx4 %0, %1, %4 offen lds"
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %4 offen lds"
                :
                : "v"(voff), "s"(r), "s"(lds), "i"(OFS), "s"(soff)
                : "memory", "scc");   // s_add_u32 writes SCC
