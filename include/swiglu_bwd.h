@@ -303,7 +303,8 @@ size_t layer_norm_bwd_workspace_size(int64_t M, int64_t N, swg_dtype dtype);
  *   SWG_GATE_CHANNEL  [N] of wdtype, contiguous; ldg is not used
  *   SWG_GATE_ROW      one value a row, of dtype, ldg elements apart
  *   SWG_GATE_FULL     [M, N] of dtype, row stride ldg
- * norm is formed from the fp32 value of out.  rstd_post = rs and rstd_pre = rp, [M], are for the
+ * The sums of squares are fp32: a row's sqrt(sum y^2) has to stay below 1.8e19 (beyond, rs = 0),
+ * and with eps = 0 above 1e-19.  norm is formed from the fp32 value of out.  rstd_post = rs and rstd_pre = rp, [M], are for the
  * backward pass; either may be NULL.  scale: finite; eps: finite, >= 0.  out may be exactly the
  * residual (same pointer and stride).  What belongs to a part that is off is not touched.
  */

@@ -285,8 +285,8 @@ class Block(torch.nn.Module):
 
         y = linear(swiglu(normed)),  stream + scale * gate * rms(y) w_post,  rms(that) w_pre
 
-    The norms' weights and the gate (one value a channel) are fp32; ``enter`` norms a stream for
-    the first block."""
+    The norms' weights and the gate (one value a channel) are fp32.  The stream is of ``dtype`` or
+    fp32, ``normed`` of ``dtype``; ``enter`` norms a stream for the first block."""
 
     def __init__(self, features, hidden, scale=1.0, eps=1e-5, bias=True, device=None,
                  dtype=torch.bfloat16):
@@ -299,7 +299,8 @@ class Block(torch.nn.Module):
 
     @staticmethod
     def enter(stream, w=None, eps=1e-5):
-        """The norm in front of the first block."""
+        """The norm in front of the first block, of the stream's dtype: an fp32 stream over 16-bit
+        blocks is cast before (``Block.enter(stream.to(dtype))``) or its norm after."""
         return residual_norm(stream, None, None, w, eps=eps, post=False)[1]
 
     def forward(self, stream, normed):

@@ -283,8 +283,9 @@ inline unsigned row_grid(int64_t rows) {
   return (unsigned)(rows < (int64_t(1) << 20) ? rows : (int64_t(1) << 20));
 }
 
-// Workgroups of the norm's forward pass, `rows` rows at a time each: all resident at once, so
-// that each walks over its rows with the next ones' loads in flight.
+// Workgroups of a norm's forward pass, `rows` rows at a time each: as many as a kernel of up to 64
+// registers has resident at once, so that each walks over its rows with the next ones' loads in
+// flight.
 inline unsigned norm_fwd_grid(int64_t M, int rows, int threads) {
   const int64_t n = ceil_div(M, rows), all = 2048 * 256 / threads;
   return (unsigned)(n < all ? n : all);

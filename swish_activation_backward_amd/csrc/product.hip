@@ -24,8 +24,10 @@
 // Bound by the matrix cores, whose clock falls under their power: a stage of a 256-wide tile takes
 // 0.75 (both flat) to 0.80 us, 0.535 where the operands are zeros; a tile's way out 12 to 15 us.  A
 // stage of 128-wide tiles takes 0.28 to 0.40 us alone, 0.54 where two share a CU.  bf16, [16384,
-// 4096] x 14336 with gelu_tanh and z kept 1549 us = 1242 TF; its backward 3316 us; [220000, 1024] x
-// 512 with a residual 282 us = 818 TF (the ends weigh more); [1, 14336] x 4096 22 us and the join 4.
+// 4096] x 14336 with gelu_tanh and z kept 1550 to 1645 us by box = 1240 to 1170 TF; its backward 3320
+// to 3450 us; [220000, 1024] x 512 with a residual 282 to 292 us = 818 to 790 TF (the ends weigh more).
+// [1, 14336] x 4096 24 us and the join 5 with W from memory, 22 and 4 with W in the last cache; 32
+// rows against a deep W [14336, 4096] 33 us = 3.6 TB/s and 5, or 22.5 and 4.
 #include <type_traits>
 #include <utility>
 

@@ -8,7 +8,7 @@
 // and written to the other of two LDS buffers as [row][32], of which a lane reads four consecutive
 // indices at once; a flat operand is transposed on the way, 4 rows by 4 (2) indices a thread.  Lane
 // half h takes index 8 j + 4 h + s in step s of a group j, of both operands alike.  Registers are
-// held to two workgroups a CU (F = 2) or four.
+// held to two workgroups a CU (F = 2) or four, for which F = 2 with both operands flat spills 6.
 //
 // Bound by the matrix cores and the loads' and stores' instructions beside them: 4096 x 4096 x 4096
 // 133 TF with both deep, 118 with one flat, 112 with both (97 with flat operands read from [32][row]

@@ -9,8 +9,10 @@
 //
 // Deep: 16 columns; a wave takes runs of 128 contraction indices (64 of fp32), each lane loading
 // straight into the operands of 16 x 16 matrix instructions (lane l: row l % 16, the 16 bytes of
-// indices at l / 16 of every fourth).  Measured on the GPU, bf16, one row: 4096 x 4096 6.8 us = 4.9
-// TB/s (the tiles with their join 12.1), 1024 x 1024 3.2 us (9.1); 16 rows 10.2 (12.9) and 3.8 (9.6).
+// indices at l / 16 of every fourth).  Measured on the GPU with W in the last cache, where these
+// sizes mostly stay, bf16, one row: 4096 x 4096 6.8 us = 4.9 TB/s (the tiles with their join 12.1),
+// 1024 x 1024 3.2 us (9.1); 16 rows 10.2 (12.9) and 3.8 (9.6).  With W from memory, each kernel on its
+// own, 4096 x 4096 takes 10.4 us (12.7 and 3.9) for one row, 12.6 (12.2 and 3.9) for 16.
 // fp32, one row: 4096 x 14336 48 us = 4.9 TB/s (78).  4 waves to a workgroup: 4096 x 4096 8.3 us; 32
 // columns to one, which halves the reads of A: 10.2 us, and from 8192 columns on 18 against 20 us at
 // 16 rows and 15 against 14 at one.

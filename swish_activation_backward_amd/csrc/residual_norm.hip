@@ -18,10 +18,15 @@
 // fp32; each output is rounded once (norm is formed from out before its rounding).
 //
 // Bound by memory: every input is read and every output written once.  Forward [220000, 512] bf16
-// with a gate of the columns 165 us = 5.4 TB/s, one row of 4096 4.5 us (the loads of a row and two
+// with a gate of the columns 167 us = 5.4 TB/s, one row of 4096 4.5 us (the loads of a row and two
 // sums one after the other).  Backward, with the join of the column sums: [220000, 512] bf16 with a
 // gate an element 317 us = 5.7 TB/s, [16384, 4096] bf16 under an fp32 stream 231 us = 5.2 TB/s,
 // [8191, 1023] fp32 with a gate a row 48 us = 4.2 TB/s.
+// Not so where the backward pass spills registers, with two chunks a thread: above 1024 columns with
+// a gate an element (112 to 158 registers under an fp32 stream, 4 to 26 else; [16384, 4096] bf16
+// under fp32 344 us = 4.3 TB/s, fp32 576 us = 3.7) or all of fp32 (13 to 18, 337 us = 4.8), and
+// above 8192 columns in every form (83 to 155; [4096, 16384] 404 to 873 us = 2.0 to 2.6 TB/s).  The
+// forward spills 10 to 19 above 8192 columns with a gate an element under fp32 (4.2 to 4.8 TB/s).
 #include "launch.hpp"
 #include "rows.hpp"
 
@@ -60,6 +65,8 @@ template <typename T> __device__ inline float row_scale(const ResidualNormArgs& 
 }
 
 // ------------------------------------------------------------------ rows of any length
+// Forward three passes over a row, backward three launches with a thread a block of rows for the
+// column sums: [1000, 40000] bf16 with a gate of the columns 93 and 323 us, [220000, 7] 117 and 581.
 // `out` may be `residual`: each thread writes the elements that only it reads, after its last use
 // of them.
 template <typename T, typename R, int NT>
@@ -271,8 +278,8 @@ __device__ inline void store_chunk(T* p, const float* f, int skip, bool once) {
   c.store_stream(p);
 }
 
-// Forward.  All workgroups are resident and walk over the rows with the next row's loads in
-// flight.  A row that is changed in place and whose end is held twice is written once: without a
+// Forward.  Workgroups walk over the rows with the next row's loads in flight (2048 of 256 threads, of
+// which the registers let 768 to 2048 run at once).  A row that is changed in place and whose end is held twice is written once: without a
 // norm no barrier orders the first write before the second read.
 template <typename T, typename R, bool FULL, int G, int EC>
 __global__ __launch_bounds__(G > 256 ? G : 256) void rnorm_fwd_kernel(ResidualNormArgs a) {
