@@ -35,6 +35,16 @@ CallTiming& call_timing();
 
 constexpr int64_t kMaxStreamBlocks = 8192;
 
+// Workgroups over two dimensions of a grid, for counts whose threads may be 2^32 and more: a
+// dimension that holds as many is cut off without an error.  wide_block() is a workgroup's index; the
+// last ones may be beyond the count.
+inline dim3 wide_grid(int64_t blocks) {
+  constexpr int64_t most = int64_t(1) << 20;
+  return blocks <= most ? dim3((unsigned)blocks)
+                        : dim3((unsigned)most, (unsigned)((blocks + most - 1) / most));
+}
+__device__ inline int64_t wide_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 hipError_t launch_swish_grad(int dtype, const void* grad, const void* x, void* out, int64_t n,
                              float beta, bool vector_path, hipStream_t stream);
 

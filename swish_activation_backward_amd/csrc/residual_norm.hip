@@ -643,7 +643,7 @@ __global__ __launch_bounds__(256) void rnorm_finalize_kernel(ResidualNormArgs a,
   constexpr int Q = 16, P = 256 / Q;
   __shared__ f32x4 red[P][Q];
   const int q = threadIdx.x % Q, lane = threadIdx.x / Q;
-  const int64_t c = ((int64_t)blockIdx.x * Q + q) * 4;   // column of the 2 Np
+  const int64_t c = (wide_block() * Q + q) * 4;   // column of the 2 Np
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < 2 * Np) {
 #pragma unroll 4
@@ -657,7 +657,7 @@ __global__ __launch_bounds__(256) void rnorm_finalize_kernel(ResidualNormArgs a,
     __syncthreads();
   }
   if (threadIdx.x >= 4 * Q) return;
-  const int64_t e = (int64_t)blockIdx.x * 4 * Q + threadIdx.x;
+  const int64_t e = wide_block() * 4 * Q + threadIdx.x;
   const int64_t col = e < Np ? e : e - Np;
   if (e >= 2 * Np || col >= a.N) return;
   const float v = red[0][threadIdx.x >> 2][threadIdx.x & 3];
@@ -775,8 +775,8 @@ static hipError_t rnorm_bwd_t(const ResidualNormArgs& a, const ResidualNormPlan&
   if (!cols) return hipSuccess;
   // M = 0: no partial rows, the empty sums
   const int64_t np = ceil_div(a.N, 4) * 4, parts = a.M > 0 ? p.parts : 0;
-  SWG_TRY(SWG_LAUNCH((rnorm_finalize_kernel<T>), dim3((unsigned)ceil_div(2 * np, 64)), dim3(256), 0,
-                     stream, a, part, parts, np));
+  SWG_TRY(SWG_LAUNCH((rnorm_finalize_kernel<T>), wide_grid(ceil_div(2 * np, 64)), dim3(256), 0, stream,
+                     a, part, parts, np));
   return hipSuccess;
 }
 
