@@ -470,7 +470,7 @@ __global__ __launch_bounds__(256) void norm_finalize_kernel(const float* part, i
   constexpr int P = 256 / Q;
   __shared__ f32x4 red[P][Q];
   const int q = threadIdx.x % Q, lane = threadIdx.x / Q;
-  const int64_t c = ((int64_t)blockIdx.x * Q + q) * 4;   // column of the 2 Np
+  const int64_t c = (wide_block() * Q + q) * 4;   // column of the 2 Np
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < 2 * Np) {
 #pragma unroll 4
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(256) void norm_finalize_kernel(const float* part, i
     __syncthreads();
   }
   if (threadIdx.x >= 4 * Q) return;
-  const int64_t e = (int64_t)blockIdx.x * 4 * Q + threadIdx.x;
+  const int64_t e = wide_block() * 4 * Q + threadIdx.x;
   const int64_t col = e < Np ? e : e - Np;
   W* dst = e < Np ? dw : db;
   if (e >= 2 * Np || col >= N || dst == nullptr) return;
@@ -578,7 +578,7 @@ static hipError_t norm_bwd_t(const NormArgs& a, const NormPlan& p, float* part,
                        dim3(256), 0, stream, part, parts, static_cast<W*>(a.dw),
                        static_cast<W*>(a.db), a.N, np, a.accumulate));
   else
-    SWG_TRY(SWG_LAUNCH((norm_finalize_kernel<W, 16>), dim3((unsigned)ceil_div(2 * np, 64)),
+    SWG_TRY(SWG_LAUNCH((norm_finalize_kernel<W, 16>), wide_grid(ceil_div(2 * np, 64)),
                        dim3(256), 0, stream, part, parts, static_cast<W*>(a.dw),
                        static_cast<W*>(a.db), a.N, np, a.accumulate));
   return hipSuccess;
