@@ -77,6 +77,8 @@ typedef enum {
  * (fp32 column partials; contents on entry are ignored, contents on return unspecified);
  * it may be NULL when that size is 0.  No output (dg, dfc, db_g, db_fc, workspace) may
  * overlap another buffer (SWG_ERR_INVALID); the inputs are only read and may share memory.
+ * Columns that are taken one by one (an odd N, pointers off 16 bytes): below 2^29
+ * (SWG_ERR_UNSUPPORTED).
  */
 swg_status swiglu_bwd_b(const void* dy, const void* g, const void* fc,
                         void* dg, void* dfc, void* db_g, void* db_fc,

@@ -302,6 +302,8 @@ static swg_status b_checks(const void* dy, const void* g, const void* fc, void* 
   const bool vec = aligned(dy, 16) && aligned(g, 16) && aligned(fc, 16) && aligned(dg, 16) &&
                    aligned(dfc, 16);
   *plan = plan_b(M, N, dtype, vec);
+  // a launch's dimension has less than 2^32 threads (odd N of 2^29 and more)
+  if (plan->nstrips >= (int64_t(1) << 32) / kBThreads) return SWG_ERR_UNSUPPORTED;
   if (own_ws) {
     if (workspace_bytes < plan->ws_bytes) return SWG_ERR_WORKSPACE;
     if (plan->ws_bytes > 0 && workspace == nullptr) return SWG_ERR_NULLPTR;

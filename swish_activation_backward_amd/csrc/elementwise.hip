@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256) void db_finalize_kernel(const float* part, T* 
                                                           int64_t N, int64_t nchunks) {
   const int lane = threadIdx.x & 15;
   const int grp = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 16 + lane;
+  const int64_t col = wide_block() * 16 + lane;
   const int64_t W = 2 * N;
   float s = 0.0f;
   if (col < W) {
@@ -317,7 +317,7 @@ static hipError_t b_stage_t(const BPlan& p, const void* dy, const void* g, const
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  SWG_LAUNCH((db_finalize_kernel<T>), dim3((unsigned)ceil_div(2 * N, 16)), dim3(256), 0,
+  SWG_LAUNCH((db_finalize_kernel<T>), wide_grid(ceil_div(2 * N, 16)), dim3(256), 0,
                      stream, part, static_cast<T*>(db_g), static_cast<T*>(db_fc), N, p.nwalk);
   return hipGetLastError();
 }
