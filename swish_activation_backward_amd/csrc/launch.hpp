@@ -33,6 +33,14 @@ CallTiming& call_timing();
     }                                                                                     \
   } while (0)
 
+// A launch whose error the launcher returns.
+#define SWG_TRY(EXPR)                          \
+  do {                                         \
+    EXPR;                                      \
+    const hipError_t e_ = hipGetLastError();   \
+    if (e_ != hipSuccess) return e_;           \
+  } while (0)
+
 constexpr int64_t kMaxStreamBlocks = 8192;
 
 // Workgroups over two dimensions of a grid, for counts whose threads may be 2^32 and more: a

@@ -7,13 +7,6 @@
 
 namespace swg {
 
-#define SWG_TRY(EXPR)                          \
-  do {                                         \
-    EXPR;                                      \
-    const hipError_t e_ = hipGetLastError();   \
-    if (e_ != hipSuccess) return e_;           \
-  } while (0)
-
 hipError_t launch_product(int dtype, const Product& a, const ProductPlan& p, void* ws, int cus,
                           hipStream_t stream) {
   if (p.few) return launch_product_few(dtype, a, stream);

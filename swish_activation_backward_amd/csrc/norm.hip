@@ -492,13 +492,6 @@ __global__ __launch_bounds__(256) void norm_finalize_kernel(const float* part, i
   dst[col] = from_f32<W>(acc ? to_f32(dst[col]) + v : v);
 }
 
-#define SWG_TRY(EXPR)                          \
-  do {                                         \
-    EXPR;                                      \
-    const hipError_t e_ = hipGetLastError();   \
-    if (e_ != hipSuccess) return e_;           \
-  } while (0)
-
 template <typename T, typename W>
 static hipError_t norm_fwd_t(const NormArgs& a, hipStream_t stream) {
   const T* x = static_cast<const T*>(a.x);

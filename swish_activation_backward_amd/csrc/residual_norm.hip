@@ -683,13 +683,6 @@ __global__ __launch_bounds__(256) void rnorm_finalize_kernel(ResidualNormArgs a,
   if (channel) put(a.dgate, a.scale * w * v);
 }
 
-#define SWG_TRY(EXPR)                          \
-  do {                                         \
-    EXPR;                                      \
-    const hipError_t e_ = hipGetLastError();   \
-    if (e_ != hipSuccess) return e_;           \
-  } while (0)
-
 template <typename T, typename R>
 static hipError_t rnorm_fwd_t(const ResidualNormArgs& a, hipStream_t stream) {
 #define SWG_FWD(G, EC)                                                                         \
